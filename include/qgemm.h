@@ -437,6 +437,129 @@ qg_status qgemm_w8a8_int8_dynamic(const uint16_t *a_bf16, const int8_t *w_i8,
                                   void *workspace, size_t workspace_bytes,
                                   qg_stream stream);
 
+/*
+ * ---- the operators between two products of a decoder block ------------------
+ * Each does in one pass what stands between two of the products above and
+ * leaves its output in the form the next one reads: bf16 (qgemm_w4a16*), e4m3
+ * codes with fp32 row scales (qgemm_w8a8_fp8, qgemm_w4a8_fp8*) or int8 codes
+ * with fp32 row scales (qgemm_w8a8_int8).  Arithmetic is fp32 from the bf16
+ * inputs to the output, which is rounded once (to bf16 or to its code); the
+ * norm's sum of squares is fp64.
+ * Row lengths are multiples of 8 (rows stay 16-byte aligned) up to 2^20, rows
+ * number fewer than 2^22 and elements fewer than 2^35, else QG_ERR_SHAPE.
+ * Rows are independent, and no result depends on the other rows of a call.
+ *
+ * rms_norm -- h = x + residual, y = (h * rsqrt(mean(h^2) + eps)) * weight.
+ *
+ *   x_bf16         in   [M, K].
+ *   residual_bf16  in   [M, K], or NULL: h = x.
+ *   weight_bf16    in   [K].
+ *   eps            a positive normal number (QG_ERR_SHAPE otherwise).
+ *   h_bf16         out  [M, K] h rounded to bf16 (the new residual stream), or
+ *                  NULL.  The norm takes the unrounded h.  It may be the memory
+ *                  of x_bf16 or of residual_bf16.
+ *   y_bf16         out  [M, K].
+ * rms_norm_quant, rms_norm_quant_int8 -- the same with a quantized output:
+ *   y_e4m3 / y_i8  out  [M, K] codes of y, y_scale out [M]: s = max|y| / 448
+ *                  (/ 127) in IEEE fp32, codes rnd(y / s) of the fp32 quotient
+ *                  (to one unit in its last place), saturated at the largest
+ *                  code; a zero row gives s = 0 and codes 0.
+ *   y_bf16         out  [M, K] y as bf16 too (a router reads it), or NULL.
+ */
+qg_status rms_norm(const uint16_t *x_bf16, const uint16_t *residual_bf16,
+                   const uint16_t *weight_bf16, float eps, int M, int K,
+                   uint16_t *h_bf16, uint16_t *y_bf16, qg_stream stream);
+qg_status rms_norm_quant(const uint16_t *x_bf16, const uint16_t *residual_bf16,
+                         const uint16_t *weight_bf16, float eps, int M, int K,
+                         uint16_t *h_bf16, uint16_t *y_bf16, uint8_t *y_e4m3,
+                         float *y_scale, qg_stream stream);
+qg_status rms_norm_quant_int8(const uint16_t *x_bf16, const uint16_t *residual_bf16,
+                              const uint16_t *weight_bf16, float eps, int M, int K,
+                              uint16_t *h_bf16, uint16_t *y_bf16, int8_t *y_i8,
+                              float *y_scale, qg_stream stream);
+
+/*
+ * swiglu -- y[m, i] = silu(gate_up[m, i]) * gate_up[m, I + i], silu(g) =
+ * g / (1 + exp(-g)): the gated unit on the output of a fused gate_up product.
+ *   gate_up_bf16  in   [M, 2 I], the gate in the first I columns (I % 8 == 0).
+ *   y_bf16        out  [M, I]; or, for swiglu_quant and swiglu_quant_int8, codes
+ *                 and y_scale as those of rms_norm_quant.
+ */
+qg_status swiglu(const uint16_t *gate_up_bf16, int M, int I, uint16_t *y_bf16,
+                 qg_stream stream);
+qg_status swiglu_quant(const uint16_t *gate_up_bf16, int M, int I,
+                       uint8_t *y_e4m3, float *y_scale, qg_stream stream);
+qg_status swiglu_quant_int8(const uint16_t *gate_up_bf16, int M, int I,
+                            int8_t *y_i8, float *y_scale, qg_stream stream);
+
+/*
+ * ---- into and out of the expert-grouped products -----------------------------
+ * B tokens with k experts each make B k slots; slot (b, j) is choice j of token
+ * b.  Sorted by expert, slots in order inside an expert, the slots are the
+ * routed rows of qgemm_w4a16_grouped and its W4A8 siblings (T = B k).  A slot
+ * whose expert id lies outside 0 .. E - 1 (padding, an expert held elsewhere)
+ * has no row: the rows from offsets[E] on belong to no expert and are neither
+ * written here nor by the grouped products.  One token may name an expert
+ * twice; it then has two rows there.
+ * 1 <= k <= 1024, 1 <= E <= 1024, B k <= 2^24, row sizes up to 2^21 bytes
+ * (QG_ERR_SHAPE otherwise; also when the rows of all tokens together would
+ * need 2^24 or more workgroups of 256 pieces).
+ *
+ * moe_dispatch -- sort the slots and copy each token's row to its routed rows.
+ *   expert_ids     in   int32 [B, k].
+ *   rows           in   [B] rows of row_bytes bytes each (row_bytes % 8 == 0):
+ *                  bf16 activations, or 8-bit codes.  NULL: sort only
+ *                  (row_bytes is then not read).
+ *   row_scale      in   fp32 [B] scales that travel with 8-bit rows, or NULL.
+ *   offsets        out  int32 [E + 1] as the grouped products read them.
+ *   row_of_slot    out  int32 [B, k]: the routed row of the slot, -1 for none.
+ *   rows_out       out  [B k] rows; NULL exactly when rows is.
+ *   row_scale_out  out  fp32 [B k]; NULL exactly when row_scale is.
+ *   workspace      qg_moe_dispatch_workspace_bytes(B, k, E) bytes (NULL when
+ *                  that is 0), 4-byte aligned, no initial contents needed.
+ *                  Calls sharing it must not overlap in time.
+ * B == 0 writes zero offsets.  The result does not depend on timing.
+ *
+ * moe_gather -- copy another tensor's rows by the row_of_slot of a dispatch.
+ *
+ * moe_combine -- y[b] = residual[b] + sum over j of weights[b, j] *
+ * rows[row_of_slot[b, j]], summed in fp32 in slot order and rounded once; slots
+ * without a row add nothing.
+ *   rows_bf16      in   [B k, K] (K % 8 == 0), e.g. the output of a grouped down
+ *                  projection.
+ *   weights        in   fp32 [B, k], or NULL: 1 (with NULL weights and residual
+ *                  this is the gradient of moe_dispatch's and moe_gather's rows).
+ *   residual_bf16  in   [B, K], or NULL.  It may be the memory of y_bf16.
+ *   y_bf16         out  [B, K].
+ *
+ * moe_combine_backward -- the gradients of moe_combine (that of the residual is
+ * dy itself): drows[row_of_slot[b, j]] = weights[b, j] * dy[b], dweights[b, j] =
+ * the fp32 sum of dy[b] * rows[row_of_slot[b, j]], 0 for a slot without a row.
+ *   drows_bf16     out  [B k, K], or NULL; rows of no slot keep their contents.
+ *   dweights       out  fp32 [B, k], or NULL (rows_bf16 is then not read and may
+ *                  be NULL).  One of the two is required.
+ *
+ * row_of_slot is read on the device; an entry outside 0 .. B k - 1 means no row,
+ * so malformed entries cause no access out of bounds (repeated ones give
+ * unspecified contents of the routed row they share).
+ */
+size_t qg_moe_dispatch_workspace_bytes(int64_t B, int64_t k, int64_t E);
+qg_status moe_dispatch(const int32_t *expert_ids, const void *rows,
+                       const float *row_scale, int B, int k, int E, int row_bytes,
+                       int32_t *offsets, int32_t *row_of_slot, void *rows_out,
+                       float *row_scale_out, void *workspace, size_t workspace_bytes,
+                       qg_stream stream);
+qg_status moe_gather(const void *rows, const float *row_scale,
+                     const int32_t *row_of_slot, int B, int k, int row_bytes,
+                     void *rows_out, float *row_scale_out, qg_stream stream);
+qg_status moe_combine(const uint16_t *rows_bf16, const int32_t *row_of_slot,
+                      const float *weights, const uint16_t *residual_bf16,
+                      int B, int k, int K, uint16_t *y_bf16, qg_stream stream);
+qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf16,
+                               const int32_t *row_of_slot, const float *weights,
+                               int B, int k, int K, uint16_t *drows_bf16,
+                               float *dweights, qg_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -3,26 +3,14 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/qgemm.h"
+#include "abi_common.h"
 #include "launch.h"
+
+using namespace qg;
 
 namespace {
 
-// Limits that keep every index the kernels form inside its integer type.
-constexpr int64_t kMaxDim = int64_t(1) << 24;        // M, N
-constexpr int64_t kMaxK = int64_t(1) << 20;          // K
-constexpr int64_t kMaxElems = int64_t(1) << 38;      // elements of one matrix
 constexpr int64_t kMaxKInt8 = int64_t(1) << 17;      // int8 GEMM: 127^2 * K fits int32
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// K % 128, N % 16, bounds.  M may be 0.
-bool shape_ok(int64_t M, int64_t N, int64_t K) {
-    if (M < 0 || N <= 0 || K <= 0) return false;
-    if (K % 128 != 0 || N % 16 != 0) return false;
-    if (M > kMaxDim || N > kMaxDim || K > kMaxK) return false;
-    if (N * K > kMaxElems || M * K > kMaxElems || M * N > kMaxElems) return false;
-    return true;
-}
 
 // Expert-grouped shapes: E experts of [K, N], T routed rows.
 bool grouped_ok(int64_t E, int64_t T, int64_t N, int64_t K) {
@@ -30,12 +18,6 @@ bool grouped_ok(int64_t E, int64_t T, int64_t N, int64_t K) {
     if (E * N * K > 64 * kMaxElems) return false;
     return T == 0 || qg::w4a16_grouped_max_items((int)E, (int)T) <= 65535;
 }
-
-qg_status launched() {
-    return hipGetLastError() == hipSuccess ? QG_OK : QG_ERR_HIP;
-}
-
-hipStream_t as_stream(qg_stream s) { return reinterpret_cast<hipStream_t>(s); }
 
 }  // namespace
 

@@ -99,4 +99,24 @@ void launch_qgemm_w8a8_fp8_dyn(const uint16_t* a, const uint8_t* w, const float*
 void launch_qgemm_w8a8_i8_dyn(const uint16_t* a, const int8_t* w, const float* sw, uint16_t* y,
                               int M, int N, int K, void* ws, hipStream_t st);
 
+// Row operators around the products (norm.hip).  With codes (e4m3 / int8) q and
+// s are the per-token codes and scales; with bf16 they are null.
+enum class ActFormat { bf16, e4m3, int8 };
+void launch_rms_norm(const uint16_t* x, const uint16_t* r, const uint16_t* w, float eps, int M, int K,
+                     uint16_t* h, uint16_t* y, void* q, float* s, ActFormat fmt, hipStream_t st);
+void launch_swiglu(const uint16_t* gu, int M, int I, uint16_t* y, void* q, float* s, ActFormat fmt,
+                   hipStream_t st);
+
+// Expert routing (moe.hip): B tokens, k choices each, T = B k slots
+size_t moe_dispatch_workspace_bytes(int B, int k, int E);
+void launch_moe_dispatch(const int* ids, const void* rows, const float* scale, int B, int k, int E, int row_bytes,
+                         int* offsets, int* row_of_slot, void* out, float* scale_out, void* ws, hipStream_t st);
+void launch_moe_gather(const void* rows, const float* scale, const int* row_of_slot, int B, int k, int row_bytes,
+                       void* out, float* scale_out, hipStream_t st);
+void launch_moe_combine(const uint16_t* rows, const int* row_of_slot, const float* weights, const uint16_t* residual,
+                        int B, int k, int K, uint16_t* y, hipStream_t st);
+void launch_moe_combine_backward(const uint16_t* dy, const uint16_t* rows, const int* row_of_slot,
+                                 const float* weights, int B, int k, int K, uint16_t* drows, float* dweights,
+                                 hipStream_t st);
+
 }  // namespace qg

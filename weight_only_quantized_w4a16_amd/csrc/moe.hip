@@ -1,0 +1,361 @@
+// The way into and out of the expert-grouped products: B tokens with k chosen
+// experts each make T = B k slots; the slots, sorted by expert (stable: slot
+// order inside an expert), are the routed rows.
+//
+//   dispatch  offsets[e] = first row of expert e, row_of_slot[b, j] = the row of
+//             slot (b, j), out[row_of_slot[b, j]] = rows[b]
+//   combine   y[b] = sum_j w[b, j] rows[row_of_slot[b, j]] + residual[b], fp32
+//   gradient  drows[row_of_slot[b, j]] = w[b, j] dy[b],
+//             dw[b, j] = <dy[b], rows[row_of_slot[b, j]]>
+//
+// A slot whose expert id lies outside [0, E) has no row (row_of_slot = -1) and
+// takes part in nothing.  Every kernel works by token: a token's row is read
+// once however many experts chose it, and its k routed rows meet in registers
+// in slot order, so no atomics and no second order of summation exist.  All of
+// them are bound by memory.
+#include <algorithm>
+
+#include "device_common.h"
+#include "launch.h"
+#include "rows.h"
+
+namespace qg {
+
+// ---------------------------------------------------------------------------
+// The sort: a counting sort in two launches.  Segment i of the slots (one
+// workgroup, `seg` slots) counts its experts into hist[i][e]; then every
+// segment derives the first row of each expert (totals over all segments) and
+// of its own share (totals over the segments before it), and numbers its slots
+// in order.
+// ---------------------------------------------------------------------------
+constexpr int SORT_WAVES = 4;
+constexpr int SORT_NT = SORT_WAVES * 64;
+constexpr int SORT_MIN_SEG = 1024;
+constexpr int SORT_MAX_SEGS = 256;
+
+// slots per segment, a multiple of SORT_NT
+static int sort_seg(int T) {
+    const int seg = std::max(SORT_MIN_SEG, (T + SORT_MAX_SEGS - 1) / SORT_MAX_SEGS);
+    return (seg + SORT_NT - 1) / SORT_NT * SORT_NT;
+}
+
+__global__ __launch_bounds__(SORT_NT) void moe_count_kernel(const int* __restrict__ ids, int T, int E, int seg,
+                                                            int* __restrict__ hist) {
+    extern __shared__ int count[];               // [E]
+    for (int e = threadIdx.x; e < E; e += SORT_NT) count[e] = 0;
+    __syncthreads();
+    const int s0 = blockIdx.x * seg;
+    const int s1 = min(s0 + seg, T);
+    for (int s = s0 + (int)threadIdx.x; s < s1; s += SORT_NT) {
+        const int e = ids[s];
+        if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += SORT_NT) hist[(size_t)blockIdx.x * E + e] = count[e];
+}
+
+// lanes of the wave whose `key` (below 2^bits) equals this lane's, among `live`
+__device__ __forceinline__ uint64_t same_key(int key, int bits, uint64_t live) {
+    uint64_t m = live;
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t one = __ballot((key >> b) & 1);
+        m &= ((key >> b) & 1) ? one : ~one;
+    }
+    return m;
+}
+
+__global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restrict__ ids, int T, int E, int bits, int seg,
+                                                            const int* __restrict__ hist, int* __restrict__ offsets,
+                                                            int* __restrict__ row_of_slot) {
+    extern __shared__ int lds[];
+    int* first = lds;                            // [E]: first row of the expert's share in this segment
+    int* next = lds + E;                         // [SORT_WAVES][E]: next row, by wave
+    __shared__ int wave_total[SORT_WAVES];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    const int nseg = gridDim.x;
+    const int mine = blockIdx.x;
+
+    // totals of each expert over all segments, scanned over the experts
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += SORT_NT) {
+        const int e = e0 + tid;
+        int all = 0, before = 0;
+        if (e < E) {
+            for (int i = 0; i < nseg; ++i) {
+                const int c = hist[(size_t)i * E + e];
+                all += c;
+                before += i < mine ? c : 0;
+            }
+        }
+        int incl = all;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(incl, d, 64);
+            if (lane >= d) incl += v;
+        }
+        if (lane == 63) wave_total[wave] = incl;
+        __syncthreads();
+        int base = carry;
+        for (int w = 0; w < SORT_WAVES; ++w) {
+            base += w < wave ? wave_total[w] : 0;
+            carry += wave_total[w];
+        }
+        if (e < E) {
+            first[e] = base + incl - all + before;
+            if (mine == 0) offsets[e + 1] = base + incl;
+        }
+        __syncthreads();                         // wave_total is written again
+    }
+    if (mine == 0 && tid == 0) offsets[0] = 0;
+
+    // each wave numbers a contiguous quarter of the segment: its experts'
+    // counts first, then the first row of each (expert, wave)
+    for (int i = tid; i < SORT_WAVES * E; i += SORT_NT) next[i] = 0;
+    __syncthreads();
+    const int per = seg / SORT_WAVES;
+    const int s0 = mine * seg + wave * per;
+    const int s1 = min(s0 + per, T);
+    int* cnt = next + wave * E;
+    for (int s = s0 + lane; s < s1; s += 64) {
+        const int e = ids[s];
+        if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += SORT_NT) {
+        int at = first[e];
+        for (int w = 0; w < SORT_WAVES; ++w) {
+            const int c = next[w * E + e];
+            next[w * E + e] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    for (int s = s0; s < s1; s += 64) {          // uniform in the wave
+        const bool in = s + lane < s1;
+        const int e = in ? ids[s + lane] : -1;
+        const bool kept = e >= 0 && e < E;
+        const uint64_t live = __ballot(kept);
+        const uint64_t m = same_key(kept ? e : 0, bits, live);
+        int row = -1;
+        int at = 0;
+        if (kept) {
+            at = cnt[e];
+            row = at + __popcll(m & ((1ull << lane) - 1));
+        }
+        __builtin_amdgcn_wave_barrier();         // every lane has read before one writes
+        if (kept && (m >> lane) == 1ull) cnt[e] = at + __popcll(m);   // the last lane of each key
+        __builtin_amdgcn_wave_barrier();
+        if (in) row_of_slot[s + lane] = row;
+    }
+}
+
+static int bits_of(int E) {
+    int b = 0;
+    while ((1 << b) < E) ++b;
+    return b;
+}
+
+size_t moe_dispatch_workspace_bytes(int B, int k, int E) {
+    const int T = B * k;
+    if (T == 0) return 0;
+    const int seg = sort_seg(T);
+    return (size_t)((T + seg - 1) / seg) * E * sizeof(int);
+}
+
+static void launch_sort(const int* ids, int T, int E, int* offsets, int* row_of_slot, void* ws, hipStream_t st) {
+    const int seg = sort_seg(T);
+    const int nseg = (T + seg - 1) / seg;
+    int* hist = static_cast<int*>(ws);
+    hipLaunchKernelGGL(moe_count_kernel, dim3(nseg), dim3(SORT_NT), E * sizeof(int), st, ids, T, E, seg, hist);
+    hipLaunchKernelGGL(moe_place_kernel, dim3(nseg), dim3(SORT_NT), (1 + SORT_WAVES) * E * sizeof(int), st, ids, T, E,
+                       bits_of(E), seg, hist, offsets, row_of_slot);
+}
+
+// offsets of a call without slots
+__global__ void moe_no_rows_kernel(int E, int* __restrict__ offsets) {
+    for (int e = threadIdx.x; e <= E; e += 256) offsets[e] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// Token kernels.  A row is `chunks` pieces; `tpb` tokens share a workgroup when
+// rows are short (tpb * span = 256 threads, span a power of two), else `parts`
+// workgroups share a token, 256 pieces each.
+// ---------------------------------------------------------------------------
+struct TokenGrid {
+    int span_log2;               // threads per token
+    int parts;                   // workgroups per token
+    unsigned blocks;
+};
+
+static TokenGrid token_grid(int B, int chunks) {
+    TokenGrid g{};
+    if (chunks >= 256) {
+        g.span_log2 = 8;
+        g.parts = (chunks + 255) / 256;
+        g.blocks = (unsigned)B * (unsigned)g.parts;
+    } else {
+        while ((1 << g.span_log2) < chunks) ++g.span_log2;
+        const int tpb = 256 >> g.span_log2;
+        g.parts = 1;
+        g.blocks = (unsigned)((B + tpb - 1) / tpb);
+    }
+    return g;
+}
+
+// token and piece of this thread; false: none
+__device__ __forceinline__ bool token_piece(int B, int chunks, int span_log2, int parts, int& b, int& c) {
+    if (parts > 1) {
+        b = blockIdx.x / parts;
+        c = (int)(blockIdx.x - b * parts) * 256 + (int)threadIdx.x;
+    } else {
+        b = (int)(blockIdx.x << (8 - span_log2)) + ((int)threadIdx.x >> span_log2);
+        c = threadIdx.x & ((1 << span_log2) - 1);
+    }
+    return b < B && c < chunks;
+}
+
+template <class V>
+__global__ __launch_bounds__(256) void moe_gather_kernel(const V* __restrict__ rows, const float* __restrict__ scale,
+                                                         const int* __restrict__ row_of_slot, int B, int k, int chunks,
+                                                         int span_log2, int parts, V* __restrict__ out,
+                                                         float* __restrict__ scale_out) {
+    int b, c;
+    if (!token_piece(B, chunks, span_log2, parts, b, c)) return;
+    const int T = B * k;
+    const V v = rows[(size_t)b * chunks + c];
+    const float s = scale && c == 0 ? scale[b] : 0.0f;
+    for (int j = 0; j < k; ++j) {
+        const int r = row_of_slot[b * k + j];
+        if ((unsigned)r >= (unsigned)T) continue;
+        out[(size_t)r * chunks + c] = v;
+        if (scale && c == 0) scale_out[r] = s;
+    }
+}
+
+void launch_moe_gather(const void* rows, const float* scale, const int* row_of_slot, int B, int k, int row_bytes,
+                       void* out, float* scale_out, hipStream_t st) {
+    auto go = [&](auto* piece) {
+        using V = std::remove_pointer_t<decltype(piece)>;
+        const int chunks = row_bytes / (int)sizeof(V);
+        const TokenGrid g = token_grid(B, chunks);
+        hipLaunchKernelGGL(moe_gather_kernel<V>, dim3(g.blocks), dim3(256), 0, st, static_cast<const V*>(rows), scale,
+                           row_of_slot, B, k, chunks, g.span_log2, g.parts, static_cast<V*>(out), scale_out);
+    };
+    if (row_bytes % 16 == 0) go((u32x4*)nullptr);
+    else go((uint2*)nullptr);
+}
+
+void launch_moe_dispatch(const int* ids, const void* rows, const float* scale, int B, int k, int E, int row_bytes,
+                         int* offsets, int* row_of_slot, void* out, float* scale_out, void* ws, hipStream_t st) {
+    if (B == 0) {
+        hipLaunchKernelGGL(moe_no_rows_kernel, dim3(1), dim3(256), 0, st, E, offsets);
+        return;
+    }
+    launch_sort(ids, B * k, E, offsets, row_of_slot, ws, st);
+    if (rows) launch_moe_gather(rows, scale, row_of_slot, B, k, row_bytes, out, scale_out, st);
+}
+
+__global__ __launch_bounds__(256) void moe_combine_kernel(const u32x4* __restrict__ rows,
+                                                          const int* __restrict__ row_of_slot,
+                                                          const float* __restrict__ weights, const u32x4* residual, int B,
+                                                          int k, int chunks, int span_log2, int parts, u32x4* y) {
+    int b, c;
+    if (!token_piece(B, chunks, span_log2, parts, b, c)) return;
+    const int T = B * k;
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        const int r = row_of_slot[b * k + j];
+        if ((unsigned)r >= (unsigned)T) continue;
+        const float w = weights ? weights[b * k + j] : 1.0f;
+        float v[8];
+        unpack8(rows[(size_t)r * chunks + c], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+    }
+    const size_t at = (size_t)b * chunks + c;
+    if (residual) {
+        float v[8];
+        unpack8(residual[at], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += v[i];
+    }
+    y[at] = pack8(acc);
+}
+
+void launch_moe_combine(const uint16_t* rows, const int* row_of_slot, const float* weights, const uint16_t* residual,
+                        int B, int k, int K, uint16_t* y, hipStream_t st) {
+    const int chunks = K / 8;
+    const TokenGrid g = token_grid(B, chunks);
+    hipLaunchKernelGGL(moe_combine_kernel, dim3(g.blocks), dim3(256), 0, st, reinterpret_cast<const u32x4*>(rows),
+                       row_of_slot, weights, reinterpret_cast<const u32x4*>(residual), B, k, chunks, g.span_log2,
+                       g.parts, reinterpret_cast<u32x4*>(y));
+}
+
+// One workgroup per token: its threads hold the pieces of dy, and the slots'
+// products <dy, row> are reduced over the workgroup, J slots at a time.
+template <int J>
+__global__ __launch_bounds__(256) void moe_combine_backward_kernel(
+    const u32x4* __restrict__ dy, const u32x4* __restrict__ rows, const int* __restrict__ row_of_slot,
+    const float* __restrict__ weights, int B, int k, int chunks, u32x4* __restrict__ drows, float* __restrict__ dweights) {
+    __shared__ float red[4][J];
+    const int b = blockIdx.x;
+    const int T = B * k;
+    const int tid = threadIdx.x;
+    for (int j0 = 0; j0 < k; j0 += J) {
+        int r[J];
+        float w[J], dot[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const bool in = j0 + j < k;
+            r[j] = in ? row_of_slot[b * k + j0 + j] : -1;
+            if ((unsigned)r[j] >= (unsigned)T) r[j] = -1;
+            w[j] = in && weights ? weights[b * k + j0 + j] : 1.0f;
+            dot[j] = 0.0f;
+        }
+        for (int c = tid; c < chunks; c += 256) {
+            float g[8];
+            unpack8(dy[(size_t)b * chunks + c], g);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (r[j] < 0) continue;
+                const size_t at = (size_t)r[j] * chunks + c;
+                if (dweights) {
+                    float v[8];
+                    unpack8(rows[at], v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], v[i], dot[j]);
+                }
+                if (drows) {
+                    float d[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) d[i] = w[j] * g[i];
+                    drows[at] = pack8(d);
+                }
+            }
+        }
+        if (dweights) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                dot[j] = wave_sum(dot[j]);
+                if ((tid & 63) == 0) red[tid >> 6][j] = dot[j];
+            }
+            __syncthreads();
+            if (tid < J && j0 + tid < k)
+                dweights[b * k + j0 + tid] = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
+            __syncthreads();
+        }
+    }
+}
+
+void launch_moe_combine_backward(const uint16_t* dy, const uint16_t* rows, const int* row_of_slot, const float* weights,
+                                 int B, int k, int K, uint16_t* drows, float* dweights, hipStream_t st) {
+    hipLaunchKernelGGL(moe_combine_backward_kernel<8>, dim3(B), dim3(256), 0, st, reinterpret_cast<const u32x4*>(dy),
+                       reinterpret_cast<const u32x4*>(rows), row_of_slot, weights, B, k, K / 8,
+                       reinterpret_cast<u32x4*>(drows), dweights);
+}
+
+}  // namespace qg

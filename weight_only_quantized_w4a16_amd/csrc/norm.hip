@@ -1,0 +1,411 @@
+// The activation steps between two quantized products of a decoder block, each
+// in one pass: the residual's addition with the root-mean-square norm, and the
+// gated unit of the feed-forward layer, both with a bf16 output or with the
+// per-token 8-bit codes and scales that the W8A8 and W4A8 products read.
+//
+//   rms_norm   h = x + residual, y = (h * rsqrt(mean(h^2) + eps)) * weight
+//   swiglu     y = gate / (1 + exp(-gate)) * up
+//   codes      s = max|y| / q_max (IEEE), q = rnd(y / s); a zero row: s = 0, q = 0
+//
+// Everything between the bf16 inputs and the output is fp32 (the sum of squares
+// fp64): y is rounded once, to bf16 or to its code, and h (stored as bf16)
+// enters the norm unrounded.
+// Both are bound by memory: a row is read once and stays in registers between
+// the reductions and the encoding.
+
+#include <algorithm>
+
+#include "device_common.h"
+#include "formats.h"
+#include "launch.h"
+#include "rows.h"
+
+namespace qg {
+
+struct FmtNone {                               // bf16 output only
+    static constexpr float qmax = 1.0f;
+    __device__ static __forceinline__ uint32_t encode2(float, float) { return 0u; }
+};
+template <class Fmt>
+constexpr bool kCodes = !std::is_same<Fmt, FmtNone>::value;
+
+// The codes of eight values: quotients by the corrected reciprocal product
+// (three operations, within one unit in the last place of the IEEE quotient).
+template <class Fmt>
+__device__ __forceinline__ uint2 encode8(const float* y, float s, float r, bool fast) {
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        b[j] = Fmt::encode2(dyn_quotient<Fmt>(y[2 * j], s, r, fast), dyn_quotient<Fmt>(y[2 * j + 1], s, r, fast));
+    return make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+}
+
+// Reduction over the NT threads of a row (`red`: one LDS word per wave, used
+// once per launch); every thread gets the result.  The order is fixed.
+template <int NT>
+__device__ __forceinline__ double row_sum(double v, double* red) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0;
+#pragma unroll
+        for (int w = 0; w < NT / 64; ++w) v += red[w];
+    }
+    return v;
+}
+template <int NT>
+__device__ __forceinline__ float row_max(float v, float* red) {
+    v = wave_max(v);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NT / 64; ++w) v = fmaxf(v, red[w]);
+    }
+    return v;
+}
+
+struct RowScale {
+    float s, r;
+    bool fast;
+    template <class Fmt>
+    __device__ static __forceinline__ RowScale of(float amax) {
+        RowScale q;
+        q.s = amax / Fmt::qmax;                              // IEEE fp32 quotient
+        q.r = 1.0f / q.s;
+        q.fast = q.s >= 0x1p-100f && q.s < __builtin_inff(); // a smaller one divides
+        return q;
+    }
+    template <class Fmt>
+    __device__ __forceinline__ uint2 codes(const float* y) const {
+        return s == 0.0f ? make_uint2(0u, 0u) : encode8<Fmt>(y, s, r, fast);
+    }
+};
+
+// ---------------------------------------------------------------------------
+// rms_norm: NT threads per row (64: one wave per row, four rows per workgroup;
+// else one row per workgroup), CPT 16-byte chunks per thread in registers.
+// x, residual and h may be the same memory: a thread reads its elements before
+// it writes them, and no other thread touches them.
+// ---------------------------------------------------------------------------
+struct NormArgs {
+    const u32x4* x;
+    const u32x4* r;          // residual or null
+    const u32x4* w;
+    u32x4* h;                // or null
+    u32x4* y;                // or null with codes
+    uint2* q;
+    float* s;
+    float eps;
+    int M, K;
+};
+
+// The squares are summed in fp64: rows near either end of bf16's range (1e30,
+// 1e-30) neither overflow nor vanish, and the result does not depend on how a
+// row is split over threads.  It costs nothing visible beside the row's bytes.
+__device__ __forceinline__ float rstd_of(double sum, int K, float eps) {
+    return (float)(1.0 / sqrt(sum / (double)K + (double)eps));   // eps > 0
+}
+
+template <class Fmt, int NT, int CPT>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs p) {
+    __shared__ double red_sum[NT < 256 ? 4 : NT / 64];
+    __shared__ float red_max[NT < 256 ? 4 : NT / 64];
+    const int tid = threadIdx.x % NT;
+    const int m = NT == 64 ? blockIdx.x * 4 + (int)(threadIdx.x >> 6) : (int)blockIdx.x;
+    if (m >= p.M) return;                                    // whole waves (NT = 64) or workgroups
+    const int chunks = p.K >> 3;
+    const size_t row = (size_t)m * chunks;
+    u32x4 xv[CPT], rv[CPT];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        const int c = tid + i * NT;
+        xv[i] = c < chunks ? p.x[row + c] : u32x4{0u, 0u, 0u, 0u};
+    }
+    if (p.r) {
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            const int c = tid + i * NT;
+            rv[i] = c < chunks ? p.r[row + c] : u32x4{0u, 0u, 0u, 0u};
+        }
+    }
+    float v[CPT][8];
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        unpack8(xv[i], v[i]);
+        if (p.r) {
+            float f[8];
+            unpack8(rv[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] += f[j];
+        }
+        const int c = tid + i * NT;
+        if (p.h && c < chunks) p.h[row + c] = pack8(v[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fma((double)v[i][j], (double)v[i][j], sum);
+    }
+    const float rstd = rstd_of(row_sum<NT>(sum, red_sum), p.K, p.eps);
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        const int c = tid + i * NT;
+        float f[8];
+        unpack8(c < chunks ? p.w[c] : u32x4{0u, 0u, 0u, 0u}, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[i][j] = v[i][j] * rstd * f[j];
+            amax = fmaxf(amax, fabsf(v[i][j]));
+        }
+        if (p.y && c < chunks) p.y[row + c] = pack8(v[i]);
+    }
+    if constexpr (kCodes<Fmt>) {
+        const RowScale sc = RowScale::of<Fmt>(row_max<NT>(amax, red_max));
+        if (tid == 0) p.s[m] = sc.s;
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+            const int c = tid + i * NT;
+            if (c < chunks) p.q[row + c] = sc.codes<Fmt>(v[i]);
+        }
+    }
+}
+
+// Rows too long for registers: the row is read again for every step (h last, so
+// that it may overwrite x or the residual).
+template <class Fmt>
+__global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs p) {
+    constexpr int NT = 1024;
+    __shared__ double red_sum[NT / 64];
+    __shared__ float red_max[NT / 64];
+    const int tid = threadIdx.x;
+    const int m = blockIdx.x;
+    const int chunks = p.K >> 3;
+    const size_t row = (size_t)m * chunks;
+    auto load = [&](int c, float* v) {
+        unpack8(p.x[row + c], v);
+        if (p.r) {
+            float f[8];
+            unpack8(p.r[row + c], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += f[j];
+        }
+    };
+    double sum = 0.0;
+    for (int c = tid; c < chunks; c += NT) {
+        float v[8];
+        load(c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fma((double)v[j], (double)v[j], sum);
+    }
+    const float rstd = rstd_of(row_sum<NT>(sum, red_sum), p.K, p.eps);
+    auto norm = [&](int c, float* v) {
+        float f[8];
+        unpack8(p.w[c], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * f[j];
+    };
+    RowScale sc{};
+    if constexpr (kCodes<Fmt>) {
+        float amax = 0.0f;
+        for (int c = tid; c < chunks; c += NT) {
+            float v[8];
+            load(c, v);
+            norm(c, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+        }
+        sc = RowScale::of<Fmt>(row_max<NT>(amax, red_max));
+        if (tid == 0) p.s[m] = sc.s;
+    }
+    for (int c = tid; c < chunks; c += NT) {
+        float v[8];
+        load(c, v);
+        if (p.h) p.h[row + c] = pack8(v);
+        norm(c, v);
+        if (p.y) p.y[row + c] = pack8(v);
+        if constexpr (kCodes<Fmt>) p.q[row + c] = sc.codes<Fmt>(v);
+    }
+}
+
+template <class Fmt>
+static void launch_norm(const NormArgs& p, hipStream_t st) {
+    const int chunks = p.K / 8;
+    const dim3 rows(p.M);
+    if (chunks <= 64)
+        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 64, 1>), dim3((p.M + 3) / 4), dim3(256), 0, st, p);
+    else if (chunks <= 128)
+        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 64, 2>), dim3((p.M + 3) / 4), dim3(256), 0, st, p);
+    else if (chunks <= 256)
+        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 256, 1>), rows, dim3(256), 0, st, p);
+    else if (chunks <= 512)
+        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 256, 2>), rows, dim3(256), 0, st, p);
+    else if (chunks <= 1024)
+        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 256, 4>), rows, dim3(256), 0, st, p);
+    else if (chunks <= 2048)
+        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 512, 4>), rows, dim3(512), 0, st, p);
+    else if (chunks <= 4096)
+        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 1024, 4>), rows, dim3(1024), 0, st, p);
+    else
+        hipLaunchKernelGGL(rms_norm_long_kernel<Fmt>, rows, dim3(1024), 0, st, p);
+}
+
+void launch_rms_norm(const uint16_t* x, const uint16_t* r, const uint16_t* w, float eps, int M, int K, uint16_t* h,
+                     uint16_t* y, void* q, float* s, ActFormat fmt, hipStream_t st) {
+    const NormArgs p{reinterpret_cast<const u32x4*>(x), reinterpret_cast<const u32x4*>(r),
+                     reinterpret_cast<const u32x4*>(w), reinterpret_cast<u32x4*>(h), reinterpret_cast<u32x4*>(y),
+                     static_cast<uint2*>(q), s, eps, M, K};
+    if (fmt == ActFormat::bf16) launch_norm<FmtNone>(p, st);
+    else if (fmt == ActFormat::e4m3) launch_norm<FmtE4M3>(p, st);
+    else launch_norm<FmtI8>(p, st);
+}
+
+// ---------------------------------------------------------------------------
+// swiglu on the fused gate_up output [M, 2I]: gate in the first I columns.
+// ---------------------------------------------------------------------------
+struct SwigluArgs {
+    const u32x4* gu;
+    u32x4* y;                // bf16 output
+    uint2* q;
+    float* s;
+    int M, I;
+};
+
+// exp(x) to about one unit in the last place: 2^(x log2 e) with the rounding
+// of the product carried into the result (the hardware's 2^t alone would be
+// off by |x| 2^-24).
+__device__ __forceinline__ float exp_f32(float x) {
+    constexpr float kLog2E = 1.44269504088896341f;
+    constexpr float kLog2ELo = 1.92596299e-8f;               // log2(e) - kLog2E
+    constexpr float kLn2 = 0.693147180559945309f;
+    const float t = x * kLog2E;
+    const float e = fmaf(x, kLog2ELo, fmaf(x, kLog2E, -t));
+    const float p = __builtin_amdgcn_exp2f(t);
+    return fmaf(p, e * kLn2, p);
+}
+
+__device__ __forceinline__ void swiglu8(u32x4 gate, u32x4 up, float* y) {
+    float g[8], u[8];
+    unpack8(gate, g);
+    unpack8(up, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        // with e = exp(-|g|) <= 1 nothing overflows: the sigmoid is 1 / (1 + e)
+        // or e / (1 + e), and 1 + e lies in [1, 2]
+        const float e = exp_f32(-fabsf(g[j]));
+        const float n = g[j] < 0.0f ? g[j] * e : g[j];
+        const float d = 1.0f + e;
+        const float r = __builtin_amdgcn_rcpf(d);
+        const float a = n * r;
+        y[j] = fmaf(fmaf(-a, d, n), r, a) * u[j];
+    }
+}
+
+// no row reduction: the grid covers the chunks of all rows
+__global__ __launch_bounds__(256) void swiglu_kernel(SwigluArgs p) {
+    const int chunks = p.I >> 3;
+    const size_t total = (size_t)p.M * chunks;
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    const size_t m = i / chunks;
+    const u32x4* gate = p.gu + i + m * chunks;
+    float y[8];
+    swiglu8(gate[0], gate[chunks], y);
+    p.y[i] = pack8(y);
+}
+
+template <class Fmt, int NT, int CPT>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void swiglu_quant_kernel(SwigluArgs p) {
+    __shared__ float red[NT < 256 ? 4 : NT / 64];
+    const int tid = threadIdx.x % NT;
+    const int m = NT == 64 ? blockIdx.x * 4 + (int)(threadIdx.x >> 6) : (int)blockIdx.x;
+    if (m >= p.M) return;
+    const int chunks = p.I >> 3;
+    const u32x4* gate = p.gu + (size_t)m * 2 * chunks;
+    u32x4 g[CPT], u[CPT];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        const int c = tid + i * NT;
+        g[i] = u[i] = u32x4{0u, 0u, 0u, 0u};
+        if (c < chunks) {
+            g[i] = gate[c];
+            u[i] = gate[chunks + c];
+        }
+    }
+    float y[CPT][8];
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        swiglu8(g[i], u[i], y[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[i][j]));
+    }
+    const RowScale sc = RowScale::of<Fmt>(row_max<NT>(amax, red));
+    if (tid == 0) p.s[m] = sc.s;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        const int c = tid + i * NT;
+        if (c < chunks) p.q[(size_t)m * chunks + c] = sc.codes<Fmt>(y[i]);
+    }
+}
+
+template <class Fmt>
+__global__ __launch_bounds__(1024) void swiglu_quant_long_kernel(SwigluArgs p) {
+    constexpr int NT = 1024;
+    __shared__ float red[NT / 64];
+    const int m = blockIdx.x;
+    const int chunks = p.I >> 3;
+    const u32x4* gate = p.gu + (size_t)m * 2 * chunks;
+    float amax = 0.0f;
+    for (int c = threadIdx.x; c < chunks; c += NT) {
+        float y[8];
+        swiglu8(gate[c], gate[chunks + c], y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
+    }
+    const RowScale sc = RowScale::of<Fmt>(row_max<NT>(amax, red));
+    if (threadIdx.x == 0) p.s[m] = sc.s;
+    for (int c = threadIdx.x; c < chunks; c += NT) {
+        float y[8];
+        swiglu8(gate[c], gate[chunks + c], y);
+        p.q[(size_t)m * chunks + c] = sc.codes<Fmt>(y);
+    }
+}
+
+template <class Fmt>
+static void launch_swiglu_quant(const SwigluArgs& p, hipStream_t st) {
+    const int chunks = p.I / 8;
+    const dim3 rows(p.M);
+    if (chunks <= 64)
+        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 64, 1>), dim3((p.M + 3) / 4), dim3(256), 0, st, p);
+    else if (chunks <= 128)
+        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 64, 2>), dim3((p.M + 3) / 4), dim3(256), 0, st, p);
+    else if (chunks <= 256)
+        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 256, 1>), rows, dim3(256), 0, st, p);
+    else if (chunks <= 512)
+        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 256, 2>), rows, dim3(256), 0, st, p);
+    else if (chunks <= 1024)
+        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 256, 4>), rows, dim3(256), 0, st, p);
+    else if (chunks <= 2048)
+        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 512, 4>), rows, dim3(512), 0, st, p);
+    else if (chunks <= 4096)
+        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 1024, 4>), rows, dim3(1024), 0, st, p);
+    else
+        hipLaunchKernelGGL(swiglu_quant_long_kernel<Fmt>, rows, dim3(1024), 0, st, p);
+}
+
+void launch_swiglu(const uint16_t* gu, int M, int I, uint16_t* y, void* q, float* s, ActFormat fmt, hipStream_t st) {
+    const SwigluArgs p{reinterpret_cast<const u32x4*>(gu), reinterpret_cast<u32x4*>(y), static_cast<uint2*>(q), s, M, I};
+    if (fmt == ActFormat::e4m3) {
+        launch_swiglu_quant<FmtE4M3>(p, st);
+    } else if (fmt == ActFormat::int8) {
+        launch_swiglu_quant<FmtI8>(p, st);
+    } else {
+        const size_t total = (size_t)M * (I / 8);
+        hipLaunchKernelGGL(swiglu_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, p);
+    }
+}
+
+}  // namespace qg

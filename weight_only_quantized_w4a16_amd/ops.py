@@ -26,6 +26,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
+_F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
 _SIGS = {
@@ -60,6 +61,17 @@ _SIGS = {
     "qg_w4a8_grouped_dynamic_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
     "qg_w4a8_grouped_dynamic_kernel_for": (ctypes.c_char_p, [_I64, _I64, _I64, _I64]),
     "qgemm_w4a8_fp8_grouped_dynamic": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _SZ, _P]),
+    "rms_norm": (_I, [_P, _P, _P, _F, _I, _I, _P, _P, _P]),
+    "rms_norm_quant": (_I, [_P, _P, _P, _F, _I, _I, _P, _P, _P, _P, _P]),
+    "rms_norm_quant_int8": (_I, [_P, _P, _P, _F, _I, _I, _P, _P, _P, _P, _P]),
+    "swiglu": (_I, [_P, _I, _I, _P, _P]),
+    "swiglu_quant": (_I, [_P, _I, _I, _P, _P, _P]),
+    "swiglu_quant_int8": (_I, [_P, _I, _I, _P, _P, _P]),
+    "qg_moe_dispatch_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "moe_dispatch": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_gather": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "moe_combine": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P]),
+    "moe_combine_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -252,6 +264,105 @@ def qgemm_w4a8_fp8_grouped_dynamic(a_bf16, offsets_i32, packed, scales, y_bf16, 
            _lib.qgemm_w4a8_fp8_grouped_dynamic(_ptr(a_bf16), _ptr(offsets_i32), _ptr(packed), _ptr(scales),
                                                _ptr(y_bf16), E, T, N, K, _ptr(workspace), workspace_bytes,
                                                _stream(stream)))
+
+
+# ---- the operators between two products: raw entry points ----------------------
+# They launch on the device their tensors are on, on that device's current
+# stream unless one is given.
+
+def _ptrs(*tensors):
+    """Device addresses (None stays None) and the one device the tensors are on."""
+    dev = -1
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensor must be on the GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        d = t.get_device()
+        if d != dev:
+            if dev >= 0:
+                raise ValueError("tensors must be on one device")
+            dev = d
+        out.append(t.data_ptr())
+    if dev < 0:
+        raise ValueError("no tensor was given")
+    return out, dev
+
+
+def _launch(fn, dev, stream, *args):
+    if stream is None:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    elif stream.device_index != dev:
+        raise ValueError("the stream belongs to another device than the tensors")
+    else:
+        raw = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != 0:
+        raise QGemmError(fn.__name__, status)
+
+
+def rms_norm(x_bf16, residual_bf16, weight_bf16, eps, M, K, h_bf16, y_bf16, stream=None):
+    (x, r, w, h, y), dev = _ptrs(x_bf16, residual_bf16, weight_bf16, h_bf16, y_bf16)
+    _launch(_lib.rms_norm, dev, stream, x, r, w, eps, M, K, h, y)
+
+
+def rms_norm_quant(x_bf16, residual_bf16, weight_bf16, eps, M, K, h_bf16, y_bf16, y_e4m3, y_scale, stream=None):
+    (x, r, w, h, y, q, s), dev = _ptrs(x_bf16, residual_bf16, weight_bf16, h_bf16, y_bf16, y_e4m3, y_scale)
+    _launch(_lib.rms_norm_quant, dev, stream, x, r, w, eps, M, K, h, y, q, s)
+
+
+def rms_norm_quant_int8(x_bf16, residual_bf16, weight_bf16, eps, M, K, h_bf16, y_bf16, y_i8, y_scale, stream=None):
+    (x, r, w, h, y, q, s), dev = _ptrs(x_bf16, residual_bf16, weight_bf16, h_bf16, y_bf16, y_i8, y_scale)
+    _launch(_lib.rms_norm_quant_int8, dev, stream, x, r, w, eps, M, K, h, y, q, s)
+
+
+def swiglu(gate_up_bf16, M, I, y_bf16, stream=None):
+    (g, y), dev = _ptrs(gate_up_bf16, y_bf16)
+    _launch(_lib.swiglu, dev, stream, g, M, I, y)
+
+
+def swiglu_quant(gate_up_bf16, M, I, y_e4m3, y_scale, stream=None):
+    (g, q, s), dev = _ptrs(gate_up_bf16, y_e4m3, y_scale)
+    _launch(_lib.swiglu_quant, dev, stream, g, M, I, q, s)
+
+
+def swiglu_quant_int8(gate_up_bf16, M, I, y_i8, y_scale, stream=None):
+    (g, q, s), dev = _ptrs(gate_up_bf16, y_i8, y_scale)
+    _launch(_lib.swiglu_quant_int8, dev, stream, g, M, I, q, s)
+
+
+def moe_dispatch_workspace_bytes(B, k, E):
+    return _lib.qg_moe_dispatch_workspace_bytes(B, k, E)
+
+
+def moe_dispatch(expert_ids, rows, row_scale, B, k, E, row_bytes, offsets, row_of_slot, rows_out, row_scale_out,
+                 workspace=None, workspace_bytes=0, stream=None):
+    (i, r, s, o, ros, ro, so, ws), dev = _ptrs(expert_ids, rows, row_scale, offsets, row_of_slot, rows_out, row_scale_out,
+                                               workspace)
+    _launch(_lib.moe_dispatch, dev, stream, i, r, s, B, k, E, row_bytes, o, ros, ro, so, ws, workspace_bytes)
+
+
+def moe_gather(rows, row_scale, row_of_slot, B, k, row_bytes, rows_out, row_scale_out, stream=None):
+    (r, s, ros, ro, so), dev = _ptrs(rows, row_scale, row_of_slot, rows_out, row_scale_out)
+    _launch(_lib.moe_gather, dev, stream, r, s, ros, B, k, row_bytes, ro, so)
+
+
+def moe_combine(rows_bf16, row_of_slot, weights, residual_bf16, B, k, K, y_bf16, stream=None):
+    (r, ros, w, res, y), dev = _ptrs(rows_bf16, row_of_slot, weights, residual_bf16, y_bf16)
+    _launch(_lib.moe_combine, dev, stream, r, ros, w, res, B, k, K, y)
+
+
+def moe_combine_backward(dy_bf16, rows_bf16, row_of_slot, weights, B, k, K, drows_bf16, dweights, stream=None):
+    (d, r, ros, w, dr, dw), dev = _ptrs(dy_bf16, rows_bf16, row_of_slot, weights, drows_bf16, dweights)
+    _launch(_lib.moe_combine_backward, dev, stream, d, r, ros, w, B, k, K, dr, dw)
 
 
 # ---- tensor-level helpers (allocate outputs with torch, then call the above) --
@@ -510,3 +621,151 @@ class W8A8Int8Linear:
         else:
             qgemm_w8a8_int8(qa, sa, self.w.codes, self.w.scales, y, M, self.w.N, K, ws, need, stream)
         return y
+
+
+# ---- the operators between two products: tensor-level helpers --------------------
+
+def _is(t, dtypes, shape, what):
+    """Raises unless t has one of the dtypes and this shape."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_CODES = {"e4m3": torch.uint8, "int8": torch.int8}
+
+
+def _codes(M, K, fmt, device):
+    if fmt not in _CODES:
+        raise ValueError(f"fmt must be 'e4m3' or 'int8', got {fmt!r}")
+    return (torch.empty((M, K), dtype=_CODES[fmt], device=device),
+            torch.empty(M, dtype=torch.float32, device=device))
+
+
+class RMSNorm:
+    """Residual addition and root-mean-square norm with a bf16 weight [K]."""
+
+    def __init__(self, weight, eps=1e-5):
+        self.weight, self.eps = _is(weight, _BF16, (weight.numel(),), "weight"), float(eps)
+
+    def _inputs(self, x, residual):
+        M, K = x.shape
+        _is(x, _BF16, (M, self.weight.numel()), "x")
+        h = None
+        if residual is not None:
+            _is(residual, _BF16, (M, K), "residual")
+            h = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+        return M, K, h
+
+    def __call__(self, x, residual=None, stream=None):
+        """(y, h): the bf16 norm and the new residual stream (x itself without a residual)."""
+        M, K, h = self._inputs(x, residual)
+        y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+        rms_norm(x, residual, self.weight, self.eps, M, K, h, y, stream)
+        return y, x if h is None else h
+
+    def quantized(self, x, residual=None, fmt="e4m3", with_bf16=False, stream=None):
+        """(q, s, h): per-token codes and scales of the norm; with_bf16: (q, s, h, y)."""
+        M, K, h = self._inputs(x, residual)
+        q, s = _codes(M, K, fmt, x.device)
+        y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if with_bf16 else None
+        call = rms_norm_quant if fmt == "e4m3" else rms_norm_quant_int8
+        call(x, residual, self.weight, self.eps, M, K, h, y, q, s, stream)
+        out = (q, s, x if h is None else h)
+        return out + (y,) if with_bf16 else out
+
+
+def gated_silu(gate_up, stream=None):
+    """silu(gate) * up of a fused [M, 2 I] gate_up output, as bf16 [M, I]."""
+    M, n = gate_up.shape
+    if n % 2:
+        raise ValueError("gate_up: the gate and up halves need an even number of columns")
+    _is(gate_up, _BF16, (M, n), "gate_up")
+    y = torch.empty((M, n // 2), dtype=torch.bfloat16, device=gate_up.device)
+    swiglu(gate_up, M, n // 2, y, stream)
+    return y
+
+
+def gated_silu_quantized(gate_up, fmt="e4m3", stream=None):
+    """The same as per-token codes and scales (q, s)."""
+    M, n = gate_up.shape
+    if n % 2:
+        raise ValueError("gate_up: the gate and up halves need an even number of columns")
+    _is(gate_up, _BF16, (M, n), "gate_up")
+    q, s = _codes(M, n // 2, fmt, gate_up.device)
+    (swiglu_quant if fmt == "e4m3" else swiglu_quant_int8)(gate_up, M, n // 2, q, s, stream)
+    return q, s
+
+
+class MoeRouting:
+    """The slots of B tokens with k experts each, sorted by expert: `offsets` int32
+    [E + 1] for the grouped products and `row_of_slot` int32 [B, k] (-1: no row)."""
+
+    def __init__(self, offsets, row_of_slot):
+        self.offsets, self.row_of_slot = offsets, row_of_slot
+        self.B, self.k = row_of_slot.shape
+
+    @classmethod
+    def dispatch(cls, expert_ids, E, rows=None, row_scale=None, stream=None):
+        """(routing, rows [B k, ...], scales [B k] or None) of int32 expert ids [B, k];
+        rows: [B, K] bf16 activations, or 8-bit codes with their fp32 row_scale [B].
+        Rows from offsets[E] on belong to no expert and are not written."""
+        B, k = expert_ids.shape
+        _is(expert_ids, (torch.int32,), (B, k), "expert_ids")
+        dev = expert_ids.device
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        row = torch.empty((B, k), dtype=torch.int32, device=dev)
+        out, scale_out, width = cls._rows_out(rows, row_scale, B, k)
+        need = moe_dispatch_workspace_bytes(B, k, E)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        moe_dispatch(expert_ids, rows, row_scale, B, k, E, width, offsets, row, out, scale_out, ws, need, stream)
+        return cls(offsets, row), out, scale_out
+
+    @staticmethod
+    def _rows_out(rows, row_scale, B, k):
+        if rows is None:
+            if row_scale is not None:
+                raise ValueError("row_scale needs rows")
+            return None, None, 0
+        if rows.dim() != 2 or rows.shape[0] != B:
+            raise ValueError(f"rows: expected [{B}, K], got {tuple(rows.shape)}")
+        out = torch.empty((B * k, rows.shape[1]), dtype=rows.dtype, device=rows.device)
+        scale_out = None
+        if row_scale is not None:
+            _is(row_scale, (torch.float32,), (B,), "row_scale")
+            scale_out = torch.empty(B * k, dtype=torch.float32, device=rows.device)
+        return out, scale_out, rows.shape[1] * rows.element_size()
+
+    def gather(self, rows, row_scale=None, stream=None):
+        """(rows [B k, K], scales or None): another tensor's rows in the routed order."""
+        out, scale_out, width = self._rows_out(rows, row_scale, self.B, self.k)
+        moe_gather(rows, row_scale, self.row_of_slot, self.B, self.k, width, out, scale_out, stream)
+        return out, scale_out
+
+    def _weights(self, weights):
+        return None if weights is None else _is(weights, (torch.float32,), (self.B, self.k), "weights")
+
+    def combine(self, rows, weights=None, residual=None, out=None, stream=None):
+        """sum_j weights[b, j] rows[row_of_slot[b, j]] + residual[b], bf16 [B, K].
+        Without weights and residual: the gradient of dispatch's and gather's rows."""
+        K = rows.shape[1]
+        _is(rows, _BF16, (self.B * self.k, K), "rows")
+        if residual is not None:
+            _is(residual, _BF16, (self.B, K), "residual")
+        y = _is(out, _BF16, (self.B, K), "out") if out is not None else \
+            torch.empty((self.B, K), dtype=torch.bfloat16, device=rows.device)
+        moe_combine(rows, self.row_of_slot, self._weights(weights), residual, self.B, self.k, K, y, stream)
+        return y
+
+    def combine_backward(self, dy, rows, weights=None, stream=None):
+        """(drows bf16 [B k, K], dweights fp32 [B, k]) of combine; rows of no slot are not written."""
+        K = dy.shape[1]
+        _is(dy, _BF16, (self.B, K), "dy")
+        _is(rows, _BF16, (self.B * self.k, K), "rows")
+        drows = torch.empty((self.B * self.k, K), dtype=torch.bfloat16, device=dy.device)
+        dw = torch.empty((self.B, self.k), dtype=torch.float32, device=dy.device)
+        moe_combine_backward(dy, rows, self.row_of_slot, self._weights(weights), self.B, self.k, K, drows, dw, stream)
+        return drows, dw
