@@ -493,6 +493,31 @@ qg_status swiglu_quant_int8(const uint16_t *gate_up_bf16, int M, int I,
                             int8_t *y_i8, float *y_scale, qg_stream stream);
 
 /*
+ * qgemm_w4a16_epilogue -- qgemm_w4a16 with what follows the product done on its
+ * fp32 accumulators: y = act(a . w_hat + bias) + residual, rounded once.
+ *   bias_bf16      in   [N] (4-byte aligned), or NULL: none.
+ *   activation     QG_ACT_NONE, QG_ACT_RELU, QG_ACT_GELU (x Phi(x)),
+ *                  QG_ACT_GELU_TANH (0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715
+ *                  x^3)))), QG_ACT_SILU (x / (1 + exp(-x))); QG_ERR_SHAPE otherwise.
+ *   residual_bf16  in   [M, N], or NULL: none.  It may be the memory of y_bf16.
+ * Everything else, the workspace (qg_w4a16_workspace_bytes) included, as
+ * qgemm_w4a16; without bias, activation and residual the same bits.
+ */
+typedef enum {
+    QG_ACT_NONE = 0,
+    QG_ACT_RELU = 1,
+    QG_ACT_GELU = 2,
+    QG_ACT_GELU_TANH = 3,
+    QG_ACT_SILU = 4
+} qg_activation;
+qg_status qgemm_w4a16_epilogue(const uint16_t *a_bf16, const uint32_t *packed,
+                               const uint16_t *scales, const uint16_t *bias_bf16,
+                               int activation, const uint16_t *residual_bf16,
+                               uint16_t *y_bf16, int M, int N, int K,
+                               void *workspace, size_t workspace_bytes,
+                               qg_stream stream);
+
+/*
  * ---- into and out of the expert-grouped products -----------------------------
  * B tokens with k experts each make B k slots; slot (b, j) is choice j of token
  * b.  Sorted by expert, slots in order inside an expert, the slots are the

@@ -125,3 +125,29 @@ def test_binding_refuses_host_tensors(ops):
         ops.rms_norm(x, None, x[0], 1e-5, 2, 64, None, x)
     with pytest.raises(ValueError):
         ops.moe_combine(None, None, None, None, 0, 1, 8, None)
+
+
+EPILOGUE = dict(a=FAKE, w=FAKE, sc=FAKE, b=FAKE, act=1, res=FAKE, y=FAKE, M=4, N=64, K=256, ws=None, wsb=0)
+
+
+def test_epilogue_refusals(ops):
+    name = "qgemm_w4a16_epilogue"
+    for changed in (dict(M=-1), dict(N=8), dict(K=64), dict(act=-1), dict(act=5), dict(M=1 << 25)):
+        assert call(ops, name, EPILOGUE, **changed) == QG_ERR_SHAPE, changed
+    for p in ("a", "w", "sc", "y"):
+        assert call(ops, name, EPILOGUE, **{p: None}) == QG_ERR_NULL, p
+    for p in ("a", "w", "sc", "b", "res", "y"):
+        assert call(ops, name, EPILOGUE, **{p: FAKE + 2}) == QG_ERR_ALIGN, p
+    assert call(ops, name, EPILOGUE, M=100) == QG_ERR_NULL            # needs a workspace
+    assert call(ops, name, EPILOGUE, M=100, ws=FAKE, wsb=16) == QG_ERR_WORKSPACE
+    assert call(ops, name, EPILOGUE, M=100, ws=FAKE + 4, wsb=1 << 30) == QG_ERR_ALIGN
+    assert call(ops, name, EPILOGUE, M=0, a=None) == QG_OK
+
+
+def test_activation_names(ops):
+    import re
+    text = open(os.path.join(ROOT, "include", "qgemm.h")).read()
+    codes = {n.lower(): int(v) for n, v in re.findall(r"QG_ACT_(\w+) = (\d+)", text)}
+    assert codes == ops.ACTIVATIONS
+    from oracle import block
+    assert set(block.EPILOGUE_ACTIVATIONS) == set(codes)

@@ -85,6 +85,27 @@ qg_status swiglu_quant_int8(const uint16_t* gate_up_bf16, int M, int I, int8_t* 
     return gated(gate_up_bf16, M, I, nullptr, y_i8, y_scale, ActFormat::int8, stream);
 }
 
+qg_status qgemm_w4a16_epilogue(const uint16_t* a_bf16, const uint32_t* packed, const uint16_t* scales,
+                               const uint16_t* bias_bf16, int activation, const uint16_t* residual_bf16,
+                               uint16_t* y_bf16, int M, int N, int K, void* workspace, size_t workspace_bytes,
+                               qg_stream stream) {
+    if (!shape_ok(M, N, K) || activation < QG_ACT_NONE || activation > QG_ACT_SILU) return QG_ERR_SHAPE;
+    if (M == 0) return QG_OK;
+    if (!a_bf16 || !packed || !scales || !y_bf16) return QG_ERR_NULL;
+    if (!aligned(a_bf16, 16) || !aligned(packed, 16) || !aligned(scales, 4) || !aligned(bias_bf16, 4) ||
+        !aligned(residual_bf16, 16) || !aligned(y_bf16, 16))
+        return QG_ERR_ALIGN;
+    const size_t need = w4a16_workspace_bytes(M, N, K);
+    if (need > 0) {
+        if (!workspace) return QG_ERR_NULL;
+        if (workspace_bytes < need) return QG_ERR_WORKSPACE;
+        if (!aligned(workspace, 16)) return QG_ERR_ALIGN;
+    }
+    launch_qgemm_w4a16_epilogue(a_bf16, packed, scales, bias_bf16, activation, residual_bf16, y_bf16, M, N, K, workspace,
+                                as_stream(stream));
+    return launched();
+}
+
 // ---- expert routing ----
 
 size_t qg_moe_dispatch_workspace_bytes(int64_t B, int64_t k, int64_t E) {

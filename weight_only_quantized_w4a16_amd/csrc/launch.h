@@ -49,6 +49,10 @@ size_t w4a16_workspace_bytes(int M, int N, int K);
 const char* w4a16_kernel_for(int M, int N, int K);
 void launch_qgemm_w4a16(const uint16_t* a, const uint32_t* packed, const uint16_t* scales,
                         uint16_t* y, int M, int N, int K, void* ws, hipStream_t s);
+// y = act(a . w_hat + bias) + residual; bias and residual may be null
+void launch_qgemm_w4a16_epilogue(const uint16_t* a, const uint32_t* packed, const uint16_t* scales,
+                                 const uint16_t* bias, int activation, const uint16_t* residual, uint16_t* y, int M,
+                                 int N, int K, void* ws, hipStream_t s);
 
 // Expert-grouped W4A16 (w4a16.hip)
 constexpr int kGroupedMaxExperts = 1024;

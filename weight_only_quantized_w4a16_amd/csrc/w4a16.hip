@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "device_common.h"
+#include "epilogue.h"
 #include "launch.h"
 
 namespace qg {
@@ -222,12 +223,12 @@ void launch_dequant_int4_g128(const uint32_t* packed, const uint16_t* scales, in
 
 // The work of one workgroup: column tiles [nt0, nt0 + CT) of y[M, N] =
 // a[M, K] . w_hat[K, N] (M <= 16 * MT).
-template <int MT, int CT, int NWAVE, int U, bool PIPE>
+template <int MT, int CT, int NWAVE, int U, bool PIPE, class EP = NoEpilogue>
 __device__ __forceinline__ void small_m_tile(const uint16_t* __restrict__ a,
                                              const uint32_t* __restrict__ wq,
                                              const uint16_t* __restrict__ sc,
-                                             uint16_t* __restrict__ y, int M, int N, int K,
-                                             int nt0) {
+                                             typename EP::out_ptr y, int M, int N, int K,
+                                             int nt0, EP ep = EP{}) {
     const int G = K >> 7;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // uniform
@@ -373,15 +374,17 @@ __device__ __forceinline__ void small_m_tile(const uint16_t* __restrict__ a,
 #pragma unroll
         for (int w = 0; w < NWAVE; ++w) sum += red[w][ct][mt][l][i];
         const int n = (nt0 + ct) * 16 + (l & 15);
-        y[(size_t)m * N + n] = (uint16_t)f32_to_bf16_rne(sum);
+        float v[1] = {sum};
+        ep.template apply<1>(v, N, [](int) { return true; }, [&](int) { return m; }, [&](int) { return n; });
+        y[(size_t)m * N + n] = (uint16_t)f32_to_bf16_rne(v[0]);
     }
 }
 
-template <int MT, int CT, int NWAVE, int U, bool PIPE>
+template <int MT, int CT, int NWAVE, int U, bool PIPE, class EP>
 __global__ __launch_bounds__(NWAVE * 64) void w4a16_small_m_kernel(
     const uint16_t* __restrict__ a, const uint32_t* __restrict__ wq,
-    const uint16_t* __restrict__ sc, uint16_t* __restrict__ y, int M, int N, int K) {
-    small_m_tile<MT, CT, NWAVE, U, PIPE>(a, wq, sc, y, M, N, K, blockIdx.x * CT);
+    const uint16_t* __restrict__ sc, typename EP::out_ptr y, int M, int N, int K, EP ep) {
+    small_m_tile<MT, CT, NWAVE, U, PIPE, EP>(a, wq, sc, y, M, N, K, blockIdx.x * CT, ep);
 }
 
 // ---------------------------------------------------------------------------
@@ -439,11 +442,11 @@ __global__ __launch_bounds__(NWAVE * 64) void w4a16_grouped_kernel(
 #endif
 constexpr int DK_NWAVE = QG_DK_NWAVE;
 
-template <int KW, int U, int D>
+template <int KW, int U, int D, class EP>
 __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
     const uint16_t* __restrict__ a, const uint32_t* __restrict__ wq,
-    const uint16_t* __restrict__ sc, uint16_t* __restrict__ y, int M, int N, int K, int S,
-    int NS, float* __restrict__ part, unsigned* __restrict__ cnt) {
+    const uint16_t* __restrict__ sc, typename EP::out_ptr y, int M, int N, int K, int S,
+    int NS, float* __restrict__ part, unsigned* __restrict__ cnt, EP ep) {
     constexpr int TW = DK_NWAVE / KW;            // tile slots
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     __shared__ int last_flag;
@@ -564,6 +567,8 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
             const int tile = cp_tile;
             if (direct) {
                 const int n = tile * 16 + col;
+                ep.template apply<4>(total, N, [&](int i) { return 4 * kq + i < M; }, [&](int i) { return 4 * kq + i; },
+                                     [&](int) { return n; });
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int m = 4 * kq + i;
@@ -597,7 +602,9 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
         if (S == 1) {
             const int m = 4 * ((r >> 2) >> 4) + (r & 3);
             const int n = (t0 + tl) * 16 + ((r >> 2) & 15);
-            if (m < M) y[(size_t)m * N + n] = (uint16_t)f32_to_bf16_rne(v);
+            float o[1] = {v};
+            ep.template apply<1>(o, N, [&](int) { return m < M; }, [&](int) { return m; }, [&](int) { return n; });
+            if (m < M) y[(size_t)m * N + n] = (uint16_t)f32_to_bf16_rne(o[0]);
         } else {
             __hip_atomic_store(&part[((size_t)split * NT + t0 + tl) * 256 + r], v, __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);
@@ -631,6 +638,12 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[b] += pv[b][k];
         }
+        auto row = [&](int b) { const int r = (e0 + b * DK_NWAVE * 64) & 255; return 4 * ((r >> 2) >> 4) + (r & 3); };
+        auto column = [&](int b) {
+            const int e = e0 + b * DK_NWAVE * 64;
+            return (t0 + (e >> 8)) * 16 + (((e & 255) >> 2) & 15);
+        };
+        ep.template apply<EB>(v, N, [&](int b) { return e0 + b * DK_NWAVE * 64 < T * 256 && row(b) < M; }, row, column);
 #pragma unroll
         for (int b = 0; b < EB; ++b) {
             const int e = e0 + b * DK_NWAVE * 64;
@@ -721,12 +734,12 @@ constexpr int LM_BM = 128;
 // BM = 128 rows (two 32-row blocks per wave) or 64 (one block per wave: half
 // the MFMA work per weight unpacked, for M <= 64 and grids too small to fill
 // the CUs with 128-row tiles).
-template <int NS, int NB, int BM = 128, int WR = 2>
+template <int NS, int NB, int BM = 128, int WR = 2, class EP = NoEpilogue>
 __device__ __forceinline__ void large_m_tile(
     const uint16_t* __restrict__ a, const uint32_t* __restrict__ wq,
-    const uint16_t* __restrict__ sc, const float* __restrict__ corr, uint16_t* __restrict__ y,
+    const uint16_t* __restrict__ sc, const float* __restrict__ corr, typename EP::out_ptr y,
     int M, int Mp, int N, int K, int S, float* __restrict__ part, unsigned* __restrict__ cnt,
-    int tiles, int split, int tile) {
+    int tiles, int split, int tile, EP ep = EP{}) {
     constexpr int NTB = 8 * NB;                  // column tiles per workgroup
     // wave grid: WR = 2 rows x 4 columns of waves (BM/2 rows x 32·NB columns
     // each), or WR = 1 row of 8 waves (BM rows x 32 columns each: every weight
@@ -956,9 +969,11 @@ __device__ __forceinline__ void large_m_tile(
             const int n = nt * 16 + (lane & 15);
 #pragma unroll
             for (int mi = 0; mi < MI; ++mi) {
+                auto row = [&](int i) { return m0 + wm * WROWS + mi * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); };
+                ep.template apply<16>(total[mi][bb], N, [&](int i) { return row(i) < M; }, row, [&](int) { return n; });
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int m = m0 + wm * WROWS + mi * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+                    const int m = row(i);
                     if (m < M) y[(size_t)m * N + n] = (uint16_t)f32_to_bf16_rne(total[mi][bb][i]);
                 }
             }
@@ -1018,6 +1033,9 @@ __device__ __forceinline__ void large_m_tile(
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[b] += pv[b][k];
         }
+        auto row = [&](int b) { return m0 + (e0 + b * 512) / BN; };
+        auto column = [&](int b) { return n0 + (e0 + b * 512) % BN; };
+        ep.template apply<EB>(v, N, [&](int b) { return e0 + b * 512 < BM * BN && row(b) < M && column(b) < N; }, row, column);
 #pragma unroll
         for (int b = 0; b < EB; ++b) {
             const int e = e0 + b * 512;
@@ -1030,15 +1048,15 @@ __device__ __forceinline__ void large_m_tile(
 }
 
 // grid = tiles x S K-slices
-template <int NS, int NB, int BM, int WR>
+template <int NS, int NB, int BM, int WR, class EP>
 __global__ __launch_bounds__(512) void w4a16_large_m_kernel(
     const uint16_t* __restrict__ a, const uint32_t* __restrict__ wq,
-    const uint16_t* __restrict__ sc, const float* __restrict__ corr, uint16_t* __restrict__ y,
-    int M, int Mp, int N, int K, int S, float* __restrict__ part, unsigned* __restrict__ cnt) {
+    const uint16_t* __restrict__ sc, const float* __restrict__ corr, typename EP::out_ptr y,
+    int M, int Mp, int N, int K, int S, float* __restrict__ part, unsigned* __restrict__ cnt, EP ep) {
     const int tiles = gridDim.x / S;
     const int split = blockIdx.x / tiles;
     const int tile = xcd_tile(blockIdx.x - split * tiles, tiles);
-    large_m_tile<NS, NB, BM, WR>(a, wq, sc, corr, y, M, Mp, N, K, S, part, cnt, tiles, split, tile);
+    large_m_tile<NS, NB, BM, WR, EP>(a, wq, sc, corr, y, M, Mp, N, K, S, part, cnt, tiles, split, tile, ep);
 }
 
 // Expert-grouped, many rows per expert: each workgroup takes one work item
@@ -1128,24 +1146,24 @@ static int small_u(int M, int MT, int K) {
     return (K / 128 <= 32 && M <= 8) ? 1 : QG_SM_U;
 }
 
-template <int MT, int CT, int U>
+template <int MT, int CT, int U, class EP>
 static void launch_small_u(const uint16_t* a, const uint32_t* wq, const uint16_t* sc, uint16_t* y,
-                           int M, int N, int K, hipStream_t s) {
+                           int M, int N, int K, const EP& ep, hipStream_t s) {
     constexpr int NWAVE = QG_SM_NWAVE;
     // two items in flight need 2*U*(5*CT + 16*MT) VGPRs of buffers
     constexpr bool PIPE = MT <= 2 && CT <= 2;
     const int NT = N / 16;
-    hipLaunchKernelGGL((w4a16_small_m_kernel<MT, CT, NWAVE, U, PIPE>), dim3(NT / CT), dim3(NWAVE * 64),
-                       0, s, a, wq, sc, y, M, N, K);
+    hipLaunchKernelGGL((w4a16_small_m_kernel<MT, CT, NWAVE, U, PIPE, EP>), dim3(NT / CT), dim3(NWAVE * 64),
+                       0, s, a, wq, sc, y, M, N, K, ep);
 }
 
-template <int MT, int CT>
+template <int MT, int CT, class EP>
 static void launch_small(const uint16_t* a, const uint32_t* wq, const uint16_t* sc, uint16_t* y,
-                         int M, int N, int K, hipStream_t s) {
+                         int M, int N, int K, const EP& ep, hipStream_t s) {
     if (MT == 1 && small_u(M, MT, K) == QG_SM_U)
-        launch_small_u<MT, CT, MT == 1 ? QG_SM_U : 1>(a, wq, sc, y, M, N, K, s);
+        launch_small_u<MT, CT, MT == 1 ? QG_SM_U : 1>(a, wq, sc, y, M, N, K, ep, s);
     else
-        launch_small_u<MT, CT, 1>(a, wq, sc, y, M, N, K, s);
+        launch_small_u<MT, CT, 1>(a, wq, sc, y, M, N, K, ep, s);
 }
 
 // column tiles per workgroup of the small-M kernel: more tiles share each
@@ -1157,16 +1175,16 @@ static int small_ct(int NT) {
     return 1;
 }
 
-template <int MT>
+template <int MT, class EP>
 static void launch_small_ct(const uint16_t* a, const uint32_t* wq, const uint16_t* sc,
-                            uint16_t* y, int M, int N, int K, hipStream_t s) {
+                            uint16_t* y, int M, int N, int K, const EP& ep, hipStream_t s) {
     const int ct = small_ct(N / 16);
     if (ct == 4)
-        launch_small<MT, 4>(a, wq, sc, y, M, N, K, s);
+        launch_small<MT, 4>(a, wq, sc, y, M, N, K, ep, s);
     else if (ct == 2)
-        launch_small<MT, 2>(a, wq, sc, y, M, N, K, s);
+        launch_small<MT, 2>(a, wq, sc, y, M, N, K, ep, s);
     else
-        launch_small<MT, 1>(a, wq, sc, y, M, N, K, s);
+        launch_small<MT, 1>(a, wq, sc, y, M, N, K, ep, s);
 }
 
 // ---- expert-grouped launch ----
@@ -1589,50 +1607,51 @@ static size_t decode_ws_bytes(const DecodeCfg& c, int N) {
     return kCounterBytes + (size_t)c.S * (N / 16) * 256 * sizeof(float);
 }
 
-template <int KW, int U, int D>
+template <int KW, int U, int D, class EP>
 static void launch_decode_t(const uint16_t* a, const uint32_t* wq, const uint16_t* sc, uint16_t* y,
-                            int M, int N, int K, const DecodeCfg& c, int NS, void* ws,
+                            int M, int N, int K, const DecodeCfg& c, int NS, void* ws, const EP& ep,
                             hipStream_t s) {
     static std::atomic<uint64_t> lds_set{0};   // up to the LDS budget (the default limit is 64 KiB)
-    allow_dynamic_lds(reinterpret_cast<const void*>(&w4a16_decode_kernel<KW, U, D>), QG_DK_LDS_BUDGET,
+    allow_dynamic_lds(reinterpret_cast<const void*>(&w4a16_decode_kernel<KW, U, D, EP>), QG_DK_LDS_BUDGET,
                       lds_set);
     unsigned* cnt = ws ? static_cast<unsigned*>(ws) : nullptr;
     float* part = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes) : nullptr;
-    hipLaunchKernelGGL((w4a16_decode_kernel<KW, U, D>), dim3(c.S * NS), dim3(DK_NWAVE * 64), c.lds, s,
-                       a, wq, sc, y, M, N, K, c.S, NS, part, cnt);
+    hipLaunchKernelGGL((w4a16_decode_kernel<KW, U, D, EP>), dim3(c.S * NS), dim3(DK_NWAVE * 64), c.lds, s,
+                       a, wq, sc, y, M, N, K, c.S, NS, part, cnt, ep);
 }
 
-template <int KW, int D>
+template <int KW, int D, class EP>
 static void launch_decode_u(const uint16_t* a, const uint32_t* wq, const uint16_t* sc, uint16_t* y,
-                            int M, int N, int K, const DecodeCfg& c, int NS, void* ws,
+                            int M, int N, int K, const DecodeCfg& c, int NS, void* ws, const EP& ep,
                             hipStream_t s) {
     switch (c.U) {
-        case 8: launch_decode_t<KW, (16 / D >= 8 ? 8 : 1), D>(a, wq, sc, y, M, N, K, c, NS, ws, s); break;
-        case 4: launch_decode_t<KW, (16 / D >= 4 ? 4 : 1), D>(a, wq, sc, y, M, N, K, c, NS, ws, s); break;
-        case 2: launch_decode_t<KW, 2, D>(a, wq, sc, y, M, N, K, c, NS, ws, s); break;
-        default: launch_decode_t<KW, 1, D>(a, wq, sc, y, M, N, K, c, NS, ws, s); break;
+        case 8: launch_decode_t<KW, (16 / D >= 8 ? 8 : 1), D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s); break;
+        case 4: launch_decode_t<KW, (16 / D >= 4 ? 4 : 1), D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s); break;
+        case 2: launch_decode_t<KW, 2, D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s); break;
+        default: launch_decode_t<KW, 1, D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s); break;
     }
 }
 
+template <class EP>
 static void launch_decode(const uint16_t* a, const uint32_t* wq, const uint16_t* sc, uint16_t* y,
-                          int M, int N, int K, const DecodeCfg& c, void* ws, hipStream_t s) {
+                          int M, int N, int K, const DecodeCfg& c, void* ws, const EP& ep, hipStream_t s) {
     const int NS = c.NS;
     switch (c.KW) {
         case 8:
-            if (c.D == QG_DK_WIDE_KW_D) launch_decode_u<8, QG_DK_WIDE_KW_D>(a, wq, sc, y, M, N, K, c, NS, ws, s);
-            else launch_decode_u<8, QG_DK_NARROW_D>(a, wq, sc, y, M, N, K, c, NS, ws, s);
+            if (c.D == QG_DK_WIDE_KW_D) launch_decode_u<8, QG_DK_WIDE_KW_D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s);
+            else launch_decode_u<8, QG_DK_NARROW_D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s);
             break;
         case 4:
-            if (c.D == QG_DK_WIDE_KW_D) launch_decode_u<4, QG_DK_WIDE_KW_D>(a, wq, sc, y, M, N, K, c, NS, ws, s);
-            else launch_decode_u<4, QG_DK_NARROW_D>(a, wq, sc, y, M, N, K, c, NS, ws, s);
+            if (c.D == QG_DK_WIDE_KW_D) launch_decode_u<4, QG_DK_WIDE_KW_D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s);
+            else launch_decode_u<4, QG_DK_NARROW_D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s);
             break;
         case 2:
-            if (c.D == QG_DK_WIDE_KW_D) launch_decode_u<2, QG_DK_WIDE_KW_D>(a, wq, sc, y, M, N, K, c, NS, ws, s);
-            else launch_decode_u<2, QG_DK_NARROW_D>(a, wq, sc, y, M, N, K, c, NS, ws, s);
+            if (c.D == QG_DK_WIDE_KW_D) launch_decode_u<2, QG_DK_WIDE_KW_D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s);
+            else launch_decode_u<2, QG_DK_NARROW_D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s);
             break;
         default:
-            if (c.D == QG_DK_ONE_D) launch_decode_u<1, QG_DK_ONE_D>(a, wq, sc, y, M, N, K, c, NS, ws, s);
-            else launch_decode_u<1, QG_DK_WIDE_D>(a, wq, sc, y, M, N, K, c, NS, ws, s);
+            if (c.D == QG_DK_ONE_D) launch_decode_u<1, QG_DK_ONE_D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s);
+            else launch_decode_u<1, QG_DK_WIDE_D>(a, wq, sc, y, M, N, K, c, NS, ws, ep, s);
             break;
     }
 }
@@ -1743,8 +1762,9 @@ static bool use_large_m(int M, int N, int K) {
     return 4LL * p.tiles * p.S >= (long long)QG_LM_COVER_Q * device_cu_count();
 }
 
+template <class EP>
 static void launch_large(const uint16_t* a, const uint32_t* wq, const uint16_t* sc, void* ws,
-                         uint16_t* y, int M, int N, int K, hipStream_t s) {
+                         uint16_t* y, int M, int N, int K, const EP& ep, hipStream_t s) {
     const LargePlan p = large_plan(M, N, K);
     char* w = static_cast<char*>(ws);
     const float* corr = reinterpret_cast<const float*>(w + p.corr_off);
@@ -1753,8 +1773,8 @@ static void launch_large(const uint16_t* a, const uint32_t* wq, const uint16_t* 
     const dim3 grid((unsigned)(p.tiles * p.S));
     auto go = [&](auto nb, auto bm, auto wr) {
         hipLaunchKernelGGL((w4a16_large_m_kernel<QG_LM_NS, decltype(nb)::value, decltype(bm)::value,
-                                                 decltype(wr)::value>),
-                           grid, dim3(512), 0, s, a, wq, sc, corr, y, M, p.Mp, N, K, p.S, part, cnt);
+                                                 decltype(wr)::value, EP>),
+                           grid, dim3(512), 0, s, a, wq, sc, corr, y, M, p.Mp, N, K, p.S, part, cnt, ep);
     };
     if (p.nb == 1) {
         if (p.bm == 64) go(ic<1>{}, ic<64>{}, ic<2>{});
@@ -1796,25 +1816,38 @@ size_t w4a16_workspace_bytes(int M, int N, int K) {
     return large_plan(M, N, K).bytes;
 }
 
-void launch_qgemm_w4a16(const uint16_t* a, const uint32_t* packed, const uint16_t* scales,
-                        uint16_t* y, int M, int N, int K, void* ws, hipStream_t s) {
+template <class EP>
+static void launch_w4a16(const uint16_t* a, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int M, int N,
+                         int K, void* ws, const EP& ep, hipStream_t s) {
     const DecodeCfg dc = decode_cfg(M, N, K);
     if (dc.ok) {
-        launch_decode(a, packed, scales, y, M, N, K, dc, ws, s);
+        launch_decode(a, packed, scales, y, M, N, K, dc, ws, ep, s);
     } else if (M <= 16) {
-        launch_small_ct<1>(a, packed, scales, y, M, N, K, s);
+        launch_small_ct<1>(a, packed, scales, y, M, N, K, ep, s);
     } else if (!use_large_m(M, N, K) && M <= 32) {
-        launch_small_ct<2>(a, packed, scales, y, M, N, K, s);
+        launch_small_ct<2>(a, packed, scales, y, M, N, K, ep, s);
     } else if (!use_large_m(M, N, K)) {
-        launch_small_ct<4>(a, packed, scales, y, M, N, K, s);
+        launch_small_ct<4>(a, packed, scales, y, M, N, K, ep, s);
     } else {
         const LargePlan p = large_plan(M, N, K);
         float* corr = reinterpret_cast<float*>(static_cast<char*>(ws) + p.corr_off);
         const size_t n = (size_t)(K / 128) * p.Mp * 16;      // 16 lanes per (group, row)
         hipLaunchKernelGGL(w4a16_group_rowsum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256),
                            0, s, a, M, p.Mp, K, corr);
-        launch_large(a, packed, scales, ws, y, M, N, K, s);
+        launch_large(a, packed, scales, ws, y, M, N, K, ep, s);
     }
+}
+
+void launch_qgemm_w4a16(const uint16_t* a, const uint32_t* packed, const uint16_t* scales,
+                        uint16_t* y, int M, int N, int K, void* ws, hipStream_t s) {
+    launch_w4a16(a, packed, scales, y, M, N, K, ws, NoEpilogue{}, s);
+}
+
+void launch_qgemm_w4a16_epilogue(const uint16_t* a, const uint32_t* packed, const uint16_t* scales, const uint16_t* bias,
+                                 int activation, const uint16_t* residual, uint16_t* y, int M, int N, int K, void* ws,
+                                 hipStream_t s) {
+    if (!bias && !residual && activation == 0) launch_qgemm_w4a16(a, packed, scales, y, M, N, K, ws, s);
+    else launch_w4a16(a, packed, scales, y, M, N, K, ws, Epilogue{bias, residual, activation}, s);
 }
 
 }  // namespace qg

@@ -67,6 +67,7 @@ _SIGS = {
     "swiglu": (_I, [_P, _I, _I, _P, _P]),
     "swiglu_quant": (_I, [_P, _I, _I, _P, _P, _P]),
     "swiglu_quant_int8": (_I, [_P, _I, _I, _P, _P, _P]),
+    "qgemm_w4a16_epilogue": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _SZ, _P]),
     "qg_moe_dispatch_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "moe_dispatch": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_gather": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P]),
@@ -339,6 +340,21 @@ def swiglu_quant_int8(gate_up_bf16, M, I, y_i8, y_scale, stream=None):
     _launch(_lib.swiglu_quant_int8, dev, stream, g, M, I, q, s)
 
 
+# qg_activation of include/qgemm.h
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def qgemm_w4a16_epilogue(a_bf16, packed, scales, bias_bf16, activation, residual_bf16, y_bf16, M, N, K, workspace=None,
+                         workspace_bytes=0, stream=None):
+    """activation: a name of ACTIVATIONS or its qg_activation code."""
+    (a, w, sc, b, r, y, ws), dev = _ptrs(a_bf16, packed, scales, bias_bf16, residual_bf16, y_bf16, workspace)
+    if not isinstance(activation, int):
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+        activation = ACTIVATIONS[activation]
+    _launch(_lib.qgemm_w4a16_epilogue, dev, stream, a, w, sc, b, activation, r, y, M, N, K, ws, workspace_bytes)
+
+
 def moe_dispatch_workspace_bytes(B, k, E):
     return _lib.qg_moe_dispatch_workspace_bytes(B, k, E)
 
@@ -403,10 +419,15 @@ class Int4G128Weight:
 
 
 class W4A16Linear:
-    """y = a @ w_hat for a packed INT4 g128 weight; owns a reusable workspace."""
+    """y = act(a @ w_hat + bias) + residual for a packed INT4 g128 weight; owns a
+    reusable workspace.  bias: bf16 [N] or None; activation: a name of ACTIVATIONS."""
 
-    def __init__(self, weight: Int4G128Weight):
+    def __init__(self, weight: Int4G128Weight, bias=None, activation="none"):
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
         self.w = weight
+        self.bias = None if bias is None else _is(bias, _BF16, (weight.N,), "bias")
+        self.activation = activation
         self._ws = None
 
     def workspace(self, M):
@@ -416,13 +437,20 @@ class W4A16Linear:
             self._ws = torch.zeros(need, dtype=torch.uint8, device=self.w.packed.device)
         return (self._ws, need) if need else (None, 0)
 
-    def __call__(self, a, out=None, stream=None):
+    def __call__(self, a, out=None, stream=None, residual=None):
+        """residual: bf16 [M, N] added after the activation; it may be `out` itself."""
         M, K = a.shape
         if K != self.w.K:
             raise ValueError(f"activation K={K} != weight K={self.w.K}")
         y = out if out is not None else torch.empty((M, self.w.N), dtype=torch.bfloat16,
                                                     device=a.device)
         ws, nbytes = self.workspace(M)
+        if residual is not None or self.bias is not None or self.activation != "none":
+            if residual is not None:
+                _is(residual, _BF16, (M, self.w.N), "residual")
+            qgemm_w4a16_epilogue(_bf16(a), self.w.packed, self.w.scales, self.bias, self.activation, residual,
+                                 _is(y, _BF16, (M, self.w.N), "out"), M, self.w.N, K, ws, nbytes, stream)
+            return y
         qgemm_w4a16(_bf16(a), self.w.packed, self.w.scales, y, M, self.w.N, K, ws, nbytes, stream)
         return y
 
