@@ -121,7 +121,7 @@ def test_moe_pointers(ops):
 def test_binding_refuses_host_tensors(ops):
     import torch
     x = torch.zeros((2, 64), dtype=torch.bfloat16)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="on the GPU"):
         ops.rms_norm(x, None, x[0], 1e-5, 2, 64, None, x)
     with pytest.raises(ValueError):
         ops.moe_combine(None, None, None, None, 0, 1, 8, None)

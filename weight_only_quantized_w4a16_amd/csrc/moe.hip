@@ -14,6 +14,7 @@
 // in slot order, so no atomics and no second order of summation exist.  All of
 // them are bound by memory.
 #include <algorithm>
+#include <atomic>
 
 #include "device_common.h"
 #include "launch.h"
@@ -22,15 +23,15 @@
 namespace qg {
 
 // ---------------------------------------------------------------------------
-// The sort: a counting sort in two launches.  Segment i of the slots (one
-// workgroup, `seg` slots) counts its experts into hist[i][e]; then every
-// segment derives the first row of each expert (totals over all segments) and
-// of its own share (totals over the segments before it), and numbers its slots
-// in order.
+// The sort of many slots: a counting sort in two launches.  Segment i of the
+// slots (one workgroup, `seg` slots) counts its experts into hist[i][e]; then
+// every segment derives the first row of each expert (totals over all segments)
+// and of its own share (totals over the segments before it), and numbers its
+// slots in order.  Few large segments: the work is latency, not bandwidth.
 // ---------------------------------------------------------------------------
-constexpr int SORT_WAVES = 4;
+constexpr int SORT_WAVES = 16;
 constexpr int SORT_NT = SORT_WAVES * 64;
-constexpr int SORT_MIN_SEG = 1024;
+constexpr int SORT_MIN_SEG = 4 * SORT_NT;
 constexpr int SORT_MAX_SEGS = 256;
 
 // slots per segment, a multiple of SORT_NT
@@ -64,32 +65,17 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits, uint64_t live) {
     return m;
 }
 
-__global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restrict__ ids, int T, int E, int bits, int seg,
-                                                            const int* __restrict__ hist, int* __restrict__ offsets,
-                                                            int* __restrict__ row_of_slot) {
-    extern __shared__ int lds[];
-    int* first = lds;                            // [E]: first row of the expert's share in this segment
-    int* next = lds + E;                         // [SORT_WAVES][E]: next row, by wave
-    __shared__ int wave_total[SORT_WAVES];
-    const int tid = threadIdx.x;
-    const int lane = tid & 63;
-    const int wave = tid >> 6;
-    const int nseg = gridDim.x;
-    const int mine = blockIdx.x;
-
-    // totals of each expert over all segments, scanned over the experts
+// Exclusive scan over the experts of the totals all[e] in LDS by a workgroup of
+// NW waves (E <= 1024): first[e] = sum of all[0 .. e-1]; offsets, if given, too.
+template <int NW>
+__device__ __forceinline__ void scan_experts(const int* all, int E, int* first, int* offsets, int* wave_total) {
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
     int carry = 0;
-    for (int e0 = 0; e0 < E; e0 += SORT_NT) {
-        const int e = e0 + tid;
-        int all = 0, before = 0;
-        if (e < E) {
-            for (int i = 0; i < nseg; ++i) {
-                const int c = hist[(size_t)i * E + e];
-                all += c;
-                before += i < mine ? c : 0;
-            }
-        }
-        int incl = all;
+    for (int e0 = 0; e0 < E; e0 += NW * 64) {
+        const int e = e0 + (int)threadIdx.x;
+        const int own = e < E ? all[e] : 0;
+        int incl = own;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int v = __shfl_up(incl, d, 64);
@@ -98,22 +84,58 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
         if (lane == 63) wave_total[wave] = incl;
         __syncthreads();
         int base = carry;
-        for (int w = 0; w < SORT_WAVES; ++w) {
+        for (int w = 0; w < NW; ++w) {
             base += w < wave ? wave_total[w] : 0;
             carry += wave_total[w];
         }
         if (e < E) {
-            first[e] = base + incl - all + before;
-            if (mine == 0) offsets[e + 1] = base + incl;
+            if (first) first[e] = base + incl - own;
+            if (offsets) offsets[e + 1] = base + incl;
         }
         __syncthreads();                         // wave_total is written again
     }
-    if (mine == 0 && tid == 0) offsets[0] = 0;
+    if (offsets && threadIdx.x == 0) offsets[0] = 0;
+}
 
-    // each wave numbers a contiguous quarter of the segment: its experts'
-    // counts first, then the first row of each (expert, wave)
+// LDS words of moe_place_kernel
+static int place_words(int E) { return (2 + SORT_WAVES) * E; }
+
+__global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restrict__ ids, int T, int E, int bits, int seg,
+                                                            const int* __restrict__ hist, int* __restrict__ offsets,
+                                                            int* __restrict__ row_of_slot) {
+    extern __shared__ int lds[];
+    int* all = lds;                              // [E]: slots of the expert
+    int* first = lds + E;                        // [E]: first row of the expert, then of its share in this segment
+    int* next = lds + 2 * E;                     // [SORT_WAVES][E]: counts, then next rows, by wave
+    __shared__ int wave_total[SORT_WAVES];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    const int nseg = gridDim.x;
+    const int mine = blockIdx.x;
+
+    // totals over the segments: SORT_NT / 2^bits threads share an expert's column
+    // (up to 2^10 experts: one thread each at least)
     for (int i = tid; i < SORT_WAVES * E; i += SORT_NT) next[i] = 0;
+    for (int e = tid; e < 2 * E; e += SORT_NT) lds[e] = 0;   // all, and first as the count of the segments before
     __syncthreads();
+    {
+        const int e = tid & ((1 << bits) - 1);
+        const int part = tid >> bits;
+        const int parts = SORT_NT >> bits;
+        if (e < E) {
+            int total = 0, before = 0;
+#pragma unroll 8
+            for (int i = part; i < nseg; i += parts) {
+                const int c = hist[(size_t)i * E + e];
+                total += c;
+                before += i < mine ? c : 0;
+            }
+            atomicAdd(&all[e], total);
+            atomicAdd(&first[e], before);
+        }
+    }
+    // meanwhile each wave counts its contiguous part of the segment
     const int per = seg / SORT_WAVES;
     const int s0 = mine * seg + wave * per;
     const int s1 = min(s0 + per, T);
@@ -123,6 +145,7 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
         if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
     }
     __syncthreads();
+    // counts become the first row of each (expert, wave)
     for (int e = tid; e < E; e += SORT_NT) {
         int at = first[e];
         for (int w = 0; w < SORT_WAVES; ++w) {
@@ -132,6 +155,7 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
         }
     }
     __syncthreads();
+    scan_experts<SORT_WAVES>(all, E, first, mine == 0 ? offsets : nullptr, wave_total);
     for (int s = s0; s < s1; s += 64) {          // uniform in the wave
         const bool in = s + lane < s1;
         const int e = in ? ids[s + lane] : -1;
@@ -142,7 +166,7 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
         int at = 0;
         if (kept) {
             at = cnt[e];
-            row = at + __popcll(m & ((1ull << lane) - 1));
+            row = first[e] + at + __popcll(m & ((1ull << lane) - 1));
         }
         __builtin_amdgcn_wave_barrier();         // every lane has read before one writes
         if (kept && (m >> lane) == 1ull) cnt[e] = at + __popcll(m);   // the last lane of each key
@@ -157,20 +181,18 @@ static int bits_of(int E) {
     return b;
 }
 
-size_t moe_dispatch_workspace_bytes(int B, int k, int E) {
-    const int T = B * k;
-    if (T == 0) return 0;
-    const int seg = sort_seg(T);
-    return (size_t)((T + seg - 1) / seg) * E * sizeof(int);
-}
-
 static void launch_sort(const int* ids, int T, int E, int* offsets, int* row_of_slot, void* ws, hipStream_t st) {
     const int seg = sort_seg(T);
     const int nseg = (T + seg - 1) / seg;
     int* hist = static_cast<int*>(ws);
     hipLaunchKernelGGL(moe_count_kernel, dim3(nseg), dim3(SORT_NT), E * sizeof(int), st, ids, T, E, seg, hist);
-    hipLaunchKernelGGL(moe_place_kernel, dim3(nseg), dim3(SORT_NT), (1 + SORT_WAVES) * E * sizeof(int), st, ids, T, E,
-                       bits_of(E), seg, hist, offsets, row_of_slot);
+    static std::atomic<uint64_t> lds_set{0};
+    const int bytes = place_words(E) * (int)sizeof(int);
+    if (bytes > 60 * 1024)                       // beside the static words, over the default limit of 64 KiB
+        allow_dynamic_lds(reinterpret_cast<const void*>(&moe_place_kernel), place_words(kGroupedMaxExperts) * (int)sizeof(int),
+                          lds_set);
+    hipLaunchKernelGGL(moe_place_kernel, dim3(nseg), dim3(SORT_NT), bytes, st, ids, T, E, bits_of(E), seg, hist, offsets,
+                       row_of_slot);
 }
 
 // offsets of a call without slots
@@ -216,6 +238,10 @@ __device__ __forceinline__ bool token_piece(int B, int chunks, int span_log2, in
     return b < B && c < chunks;
 }
 
+// Slots of a token handled together: their row numbers, weights and rows are
+// requested before the first is used.
+constexpr int SLOTS = 8;
+
 template <class V>
 __global__ __launch_bounds__(256) void moe_gather_kernel(const V* __restrict__ rows, const float* __restrict__ scale,
                                                          const int* __restrict__ row_of_slot, int B, int k, int chunks,
@@ -226,11 +252,16 @@ __global__ __launch_bounds__(256) void moe_gather_kernel(const V* __restrict__ r
     const int T = B * k;
     const V v = rows[(size_t)b * chunks + c];
     const float s = scale && c == 0 ? scale[b] : 0.0f;
-    for (int j = 0; j < k; ++j) {
-        const int r = row_of_slot[b * k + j];
-        if ((unsigned)r >= (unsigned)T) continue;
-        out[(size_t)r * chunks + c] = v;
-        if (scale && c == 0) scale_out[r] = s;
+    for (int j0 = 0; j0 < k; j0 += SLOTS) {
+        int r[SLOTS];
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) r[j] = j0 + j < k ? row_of_slot[b * k + j0 + j] : -1;
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            if ((unsigned)r[j] >= (unsigned)T) continue;
+            out[(size_t)r[j] * chunks + c] = v;
+            if (scale && c == 0) scale_out[r[j]] = s;
+        }
     }
 }
 
@@ -247,10 +278,112 @@ void launch_moe_gather(const void* rows, const float* scale, const int* row_of_s
     else go((uint2*)nullptr);
 }
 
+// ---------------------------------------------------------------------------
+// Few slots: sort and copy in one launch without a workspace.  The row of a slot
+// is the number of slots before it in (expert, slot) order, so each token's
+// workgroups count that over all T ids for their k slots (a ballot per 64 ids and
+// slot) while the token's row is on its way from memory; one more workgroup
+// writes the offsets.  The work grows with T per token, so this serves up to
+// DIRECT_MAX_T slots.
+// ---------------------------------------------------------------------------
+#ifndef QG_MOE_DIRECT_MAX_T
+#define QG_MOE_DIRECT_MAX_T 4096
+#endif
+constexpr int DIRECT_MAX_T = QG_MOE_DIRECT_MAX_T;
+
+template <class V>
+__global__ __launch_bounds__(256) void moe_dispatch_direct_kernel(const int* __restrict__ ids, const V* __restrict__ rows,
+                                                                  const float* __restrict__ scale, int B, int k, int E,
+                                                                  int chunks, int parts, int* __restrict__ offsets,
+                                                                  int* __restrict__ row_of_slot, V* __restrict__ out,
+                                                                  float* __restrict__ scale_out) {
+    const int T = B * k;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    if (blockIdx.x == gridDim.x - 1) {           // the offsets
+        __shared__ int all[kGroupedMaxExperts];
+        __shared__ int wave_total[4];
+        for (int e = tid; e < E; e += 256) all[e] = 0;
+        __syncthreads();
+        for (int s = tid; s < T; s += 256) {
+            const int e = ids[s];
+            if (e >= 0 && e < E) atomicAdd(&all[e], 1);
+        }
+        __syncthreads();
+        scan_experts<4>(all, E, nullptr, offsets, wave_total);
+        return;
+    }
+    __shared__ int below[2][4][SLOTS];
+    const int b = blockIdx.x / parts;
+    const int part = blockIdx.x - b * parts;
+    const int c = part * 256 + tid;
+    V v{};
+    if (c < chunks) v = rows[(size_t)b * chunks + c];
+    const float s = scale && c == 0 ? scale[b] : 0.0f;
+    for (int j0 = 0; j0 < k; j0 += SLOTS) {
+        // (expert, slot) as one number: E T <= 2^10 DIRECT_MAX_T fits 32 bits
+        unsigned key[SLOTS];
+        int n[SLOTS];
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            const int slot = b * k + j0 + j;
+            const int e = j0 + j < k ? ids[slot] : -1;
+            key[j] = e >= 0 && e < E ? (unsigned)e * (unsigned)T + (unsigned)slot : 0u;
+            n[j] = 0;
+        }
+        for (int t0 = wave * 64; t0 < T; t0 += 256) {
+            const int t = t0 + lane;
+            const int e = t < T ? ids[t] : -1;
+            const unsigned other = e >= 0 && e < E ? (unsigned)e * (unsigned)T + (unsigned)t : ~0u;
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) n[j] += __popcll(__ballot(other < key[j]));
+        }
+        int (*mine)[SLOTS] = below[(j0 / SLOTS) & 1];
+        if (lane == 0) {
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) mine[wave][j] = n[j];
+        }
+        __syncthreads();                         // the other half of `below` is free again after it
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            if (j0 + j >= k) break;
+            const int slot = b * k + j0 + j;
+            const int e = ids[slot];
+            const bool kept = e >= 0 && e < E;
+            const int r = mine[0][j] + mine[1][j] + mine[2][j] + mine[3][j];
+            if (part == 0 && tid == j) row_of_slot[slot] = kept ? r : -1;
+            if (!kept) continue;
+            if (c < chunks) out[(size_t)r * chunks + c] = v;
+            if (scale && c == 0) scale_out[r] = s;
+        }
+    }
+}
+
+size_t moe_dispatch_workspace_bytes(int B, int k, int E) {
+    const int T = B * k;
+    if (T <= DIRECT_MAX_T) return 0;
+    const int seg = sort_seg(T);
+    return (size_t)((T + seg - 1) / seg) * E * sizeof(int);
+}
+
 void launch_moe_dispatch(const int* ids, const void* rows, const float* scale, int B, int k, int E, int row_bytes,
                          int* offsets, int* row_of_slot, void* out, float* scale_out, void* ws, hipStream_t st) {
     if (B == 0) {
         hipLaunchKernelGGL(moe_no_rows_kernel, dim3(1), dim3(256), 0, st, E, offsets);
+        return;
+    }
+    if (B * k <= DIRECT_MAX_T) {
+        auto go = [&](auto* piece) {
+            using V = std::remove_pointer_t<decltype(piece)>;
+            const int chunks = rows ? row_bytes / (int)sizeof(V) : 0;
+            const int parts = std::max(1, (chunks + 255) / 256);
+            hipLaunchKernelGGL(moe_dispatch_direct_kernel<V>, dim3((unsigned)(B * parts + 1)), dim3(256), 0, st, ids,
+                               static_cast<const V*>(rows), scale, B, k, E, chunks, parts, offsets, row_of_slot,
+                               static_cast<V*>(out), scale_out);
+        };
+        if (row_bytes % 16 == 0) go((u32x4*)nullptr);
+        else go((uint2*)nullptr);
         return;
     }
     launch_sort(ids, B * k, E, offsets, row_of_slot, ws, st);
@@ -267,19 +400,34 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const u32x4* __restric
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-    for (int j = 0; j < k; ++j) {
-        const int r = row_of_slot[b * k + j];
-        if ((unsigned)r >= (unsigned)T) continue;
-        const float w = weights ? weights[b * k + j] : 1.0f;
-        float v[8];
-        unpack8(rows[(size_t)r * chunks + c], v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, v[i], acc[i]);
-    }
     const size_t at = (size_t)b * chunks + c;
+    u32x4 res{0u, 0u, 0u, 0u};
+    if (residual) res = residual[at];
+    for (int j0 = 0; j0 < k; j0 += SLOTS) {
+        int r[SLOTS];
+        float w[SLOTS];
+        u32x4 v[SLOTS];
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            const bool in = j0 + j < k;
+            r[j] = in ? row_of_slot[b * k + j0 + j] : -1;
+            w[j] = in && weights ? weights[b * k + j0 + j] : 1.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j)
+            if ((unsigned)r[j] < (unsigned)T) v[j] = rows[(size_t)r[j] * chunks + c];
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            if ((unsigned)r[j] >= (unsigned)T) continue;
+            float f[8];
+            unpack8(v[j], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+        }
+    }
     if (residual) {
         float v[8];
-        unpack8(residual[at], v);
+        unpack8(res, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] += v[i];
     }

@@ -40,12 +40,11 @@ __device__ __forceinline__ uint2 encode8(const float* y, float s, float r, bool 
     return make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
 }
 
-// Reduction over the NT threads of a row (`red`: one LDS word per wave, used
+// Reductions over the NT threads of a row (`red`: one LDS word per wave, used
 // once per launch); every thread gets the result.  The order is fixed.
 template <int NT>
 __device__ __forceinline__ double row_sum(double v, double* red) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    v = wave_sum(v);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
         __syncthreads();
@@ -57,7 +56,7 @@ __device__ __forceinline__ double row_sum(double v, double* red) {
 }
 template <int NT>
 __device__ __forceinline__ float row_max(float v, float* red) {
-    v = wave_max(v);
+    v = wave_max_abs(v);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
         __syncthreads();
@@ -66,6 +65,26 @@ __device__ __forceinline__ float row_max(float v, float* red) {
         for (int w = 0; w < NT / 64; ++w) v = fmaxf(v, red[w]);
     }
     return v;
+}
+// both at once: one barrier
+template <int NT>
+__device__ __forceinline__ void row_sum_max(double& sum, float& top, double* red_sum, float* red_max) {
+    sum = wave_sum(sum);
+    top = wave_max_abs(top);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) {
+            red_sum[threadIdx.x >> 6] = sum;
+            red_max[threadIdx.x >> 6] = top;
+        }
+        __syncthreads();
+        sum = 0.0;
+        top = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NT / 64; ++w) {
+            sum += red_sum[w];
+            top = fmaxf(top, red_max[w]);
+        }
+    }
 }
 
 struct RowScale {
@@ -99,6 +118,7 @@ struct NormArgs {
     u32x4* y;                // or null with codes
     uint2* q;
     float* s;
+    double inv_K;
     float eps;
     int M, K;
 };
@@ -106,20 +126,27 @@ struct NormArgs {
 // The squares are summed in fp64: rows near either end of bf16's range (1e30,
 // 1e-30) neither overflow nor vanish, and the result does not depend on how a
 // row is split over threads.  It costs nothing visible beside the row's bytes.
-__device__ __forceinline__ float rstd_of(double sum, int K, float eps) {
-    return (float)(1.0 / sqrt(sum / (double)K + (double)eps));   // eps > 0
+// 1 / sqrt in fp64 from the hardware's estimate and one Newton step, rounded once.
+__device__ __forceinline__ float rstd_of(double sum, double inv_K, float eps) {
+    const double v = fma(sum, inv_K, (double)eps);           // eps > 0
+    const double r = __builtin_amdgcn_rsq(v);
+    return (float)fma(r * 0.5, fma(-v * r, r, 1.0), r);
 }
 
+// The scale needs max |h rstd w|.  max |h w| is known before rstd, so both
+// reductions share one barrier, and the maximum is that times rstd; a row whose
+// |h w| leaves the middle of fp32's range reduces once more.
 template <class Fmt, int NT, int CPT>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs p) {
-    __shared__ double red_sum[NT < 256 ? 4 : NT / 64];
-    __shared__ float red_max[NT < 256 ? 4 : NT / 64];
+    constexpr int NW = NT < 256 ? 4 : NT / 64;
+    __shared__ double red_sum[NW];
+    __shared__ float red_max[2][NW];
     const int tid = threadIdx.x % NT;
     const int m = NT == 64 ? blockIdx.x * 4 + (int)(threadIdx.x >> 6) : (int)blockIdx.x;
     if (m >= p.M) return;                                    // whole waves (NT = 64) or workgroups
     const int chunks = p.K >> 3;
     const size_t row = (size_t)m * chunks;
-    u32x4 xv[CPT], rv[CPT];
+    u32x4 xv[CPT], rv[CPT], wv[CPT];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
         const int c = tid + i * NT;
@@ -132,8 +159,14 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
             rv[i] = c < chunks ? p.r[row + c] : u32x4{0u, 0u, 0u, 0u};
         }
     }
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        const int c = tid + i * NT;
+        wv[i] = c < chunks ? p.w[c] : u32x4{0u, 0u, 0u, 0u};
+    }
     float v[CPT][8];
     double sum = 0.0;
+    float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
         unpack8(xv[i], v[i]);
@@ -147,23 +180,37 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
         if (p.h && c < chunks) p.h[row + c] = pack8(v[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fma((double)v[i][j], (double)v[i][j], sum);
+        if constexpr (kCodes<Fmt>) {
+            float f[8];
+            unpack8(wv[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j] * f[j]));
+        }
     }
-    const float rstd = rstd_of(row_sum<NT>(sum, red_sum), p.K, p.eps);
-    float amax = 0.0f;
+    if constexpr (kCodes<Fmt>) row_sum_max<NT>(sum, top, red_sum, red_max[0]);
+    else sum = row_sum<NT>(sum, red_sum);
+    const float rstd = rstd_of(sum, p.inv_K, p.eps);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
         const int c = tid + i * NT;
         float f[8];
-        unpack8(c < chunks ? p.w[c] : u32x4{0u, 0u, 0u, 0u}, f);
+        unpack8(wv[i], f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[i][j] = v[i][j] * rstd * f[j];
-            amax = fmaxf(amax, fabsf(v[i][j]));
-        }
+        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * f[j];
         if (p.y && c < chunks) p.y[row + c] = pack8(v[i]);
     }
     if constexpr (kCodes<Fmt>) {
-        const RowScale sc = RowScale::of<Fmt>(row_max<NT>(amax, red_max));
+        if (top >= 0x1p-100f && top < __builtin_inff()) {    // uniform in the row
+            top *= rstd;
+        } else {
+            top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < CPT; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j]));
+            top = row_max<NT>(top, red_max[1]);
+        }
+        const RowScale sc = RowScale::of<Fmt>(top);
         if (tid == 0) p.s[m] = sc.s;
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
@@ -200,7 +247,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fma((double)v[j], (double)v[j], sum);
     }
-    const float rstd = rstd_of(row_sum<NT>(sum, red_sum), p.K, p.eps);
+    const float rstd = rstd_of(row_sum<NT>(sum, red_sum), p.inv_K, p.eps);
     auto norm = [&](int c, float* v) {
         float f[8];
         unpack8(p.w[c], f);
@@ -230,33 +277,45 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs p) {
     }
 }
 
+// Threads per row and chunks per thread of a row of `chunks` pieces: up to 128
+// pieces one wave; longer rows one workgroup.
+#ifndef QG_ROW_WIDE
+#define QG_ROW_WIDE 0
+#endif
+template <class Go>
+static bool with_row_shape(int M, int chunks, Go&& go) {
+    const bool wide = QG_ROW_WIDE;
+    (void)M;
+    if (chunks <= 64) go(ic<64>{}, ic<1>{});
+    else if (chunks <= 128) go(ic<64>{}, ic<2>{});
+    else if (chunks <= 256) go(ic<256>{}, ic<1>{});
+    else if (chunks <= 512) { if (wide) go(ic<512>{}, ic<1>{}); else go(ic<256>{}, ic<2>{}); }
+    else if (chunks <= 1024) { if (wide) go(ic<1024>{}, ic<1>{}); else go(ic<256>{}, ic<4>{}); }
+    else if (chunks <= 2048) { if (wide) go(ic<1024>{}, ic<2>{}); else go(ic<256>{}, ic<8>{}); }
+    else if (chunks <= 4096) { if (wide) go(ic<1024>{}, ic<4>{}); else go(ic<512>{}, ic<8>{}); }
+    else return false;
+    return true;
+}
+// workgroups and threads of M rows at NT threads a row
+template <int NT>
+static dim3 row_grid(int M) { return dim3(NT == 64 ? (M + 3) / 4 : M); }
+template <int NT>
+static dim3 row_block() { return dim3(NT == 64 ? 256 : NT); }
+
 template <class Fmt>
 static void launch_norm(const NormArgs& p, hipStream_t st) {
-    const int chunks = p.K / 8;
-    const dim3 rows(p.M);
-    if (chunks <= 64)
-        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 64, 1>), dim3((p.M + 3) / 4), dim3(256), 0, st, p);
-    else if (chunks <= 128)
-        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 64, 2>), dim3((p.M + 3) / 4), dim3(256), 0, st, p);
-    else if (chunks <= 256)
-        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 256, 1>), rows, dim3(256), 0, st, p);
-    else if (chunks <= 512)
-        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 256, 2>), rows, dim3(256), 0, st, p);
-    else if (chunks <= 1024)
-        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 256, 4>), rows, dim3(256), 0, st, p);
-    else if (chunks <= 2048)
-        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 512, 4>), rows, dim3(512), 0, st, p);
-    else if (chunks <= 4096)
-        hipLaunchKernelGGL((rms_norm_kernel<Fmt, 1024, 4>), rows, dim3(1024), 0, st, p);
-    else
-        hipLaunchKernelGGL(rms_norm_long_kernel<Fmt>, rows, dim3(1024), 0, st, p);
+    const bool done = with_row_shape(p.M, p.K / 8, [&](auto nt, auto cpt) {
+        constexpr int NT = decltype(nt)::value, CPT = decltype(cpt)::value;
+        hipLaunchKernelGGL((rms_norm_kernel<Fmt, NT, CPT>), row_grid<NT>(p.M), row_block<NT>(), 0, st, p);
+    });
+    if (!done) hipLaunchKernelGGL(rms_norm_long_kernel<Fmt>, dim3(p.M), dim3(1024), 0, st, p);
 }
 
 void launch_rms_norm(const uint16_t* x, const uint16_t* r, const uint16_t* w, float eps, int M, int K, uint16_t* h,
                      uint16_t* y, void* q, float* s, ActFormat fmt, hipStream_t st) {
     const NormArgs p{reinterpret_cast<const u32x4*>(x), reinterpret_cast<const u32x4*>(r),
                      reinterpret_cast<const u32x4*>(w), reinterpret_cast<u32x4*>(h), reinterpret_cast<u32x4*>(y),
-                     static_cast<uint2*>(q), s, eps, M, K};
+                     static_cast<uint2*>(q), s, 1.0 / K, eps, M, K};
     if (fmt == ActFormat::bf16) launch_norm<FmtNone>(p, st);
     else if (fmt == ActFormat::e4m3) launch_norm<FmtE4M3>(p, st);
     else launch_norm<FmtI8>(p, st);
@@ -376,24 +435,11 @@ __global__ __launch_bounds__(1024) void swiglu_quant_long_kernel(SwigluArgs p) {
 
 template <class Fmt>
 static void launch_swiglu_quant(const SwigluArgs& p, hipStream_t st) {
-    const int chunks = p.I / 8;
-    const dim3 rows(p.M);
-    if (chunks <= 64)
-        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 64, 1>), dim3((p.M + 3) / 4), dim3(256), 0, st, p);
-    else if (chunks <= 128)
-        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 64, 2>), dim3((p.M + 3) / 4), dim3(256), 0, st, p);
-    else if (chunks <= 256)
-        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 256, 1>), rows, dim3(256), 0, st, p);
-    else if (chunks <= 512)
-        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 256, 2>), rows, dim3(256), 0, st, p);
-    else if (chunks <= 1024)
-        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 256, 4>), rows, dim3(256), 0, st, p);
-    else if (chunks <= 2048)
-        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 512, 4>), rows, dim3(512), 0, st, p);
-    else if (chunks <= 4096)
-        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, 1024, 4>), rows, dim3(1024), 0, st, p);
-    else
-        hipLaunchKernelGGL(swiglu_quant_long_kernel<Fmt>, rows, dim3(1024), 0, st, p);
+    const bool done = with_row_shape(p.M, p.I / 8, [&](auto nt, auto cpt) {
+        constexpr int NT = decltype(nt)::value, CPT = decltype(cpt)::value;
+        hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, NT, CPT>), row_grid<NT>(p.M), row_block<NT>(), 0, st, p);
+    });
+    if (!done) hipLaunchKernelGGL(swiglu_quant_long_kernel<Fmt>, dim3(p.M), dim3(1024), 0, st, p);
 }
 
 void launch_swiglu(const uint16_t* gu, int M, int I, uint16_t* y, void* q, float* s, ActFormat fmt, hipStream_t st) {

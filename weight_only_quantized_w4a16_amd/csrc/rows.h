@@ -27,10 +27,55 @@ __device__ __forceinline__ u32x4 pack8(const float* f) {
     return u32x4{w[0], w[1], w[2], w[3]};
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
+// ---- wave reductions on DPP moves ------------------------------------------
+// Row shifts by 1, 2, 4, 8 and the row broadcasts 15 and 31 leave the result of
+// all 64 lanes in lane 63, a few cycles a step (a shuffle through LDS takes
+// about a hundred).  Lanes without a source keep `none`, the identity.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t none, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(dpp_u32<CTRL, ROWS>(0u, __float_as_uint(v)));
+}
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = dpp_u32<CTRL, ROWS>(0u, (uint32_t)u);
+    const uint64_t hi = dpp_u32<CTRL, ROWS>(0u, (uint32_t)(u >> 32));
+    return __builtin_bit_cast(double, lo | (hi << 32));
+}
+__device__ __forceinline__ float lane63(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double lane63(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    const uint64_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, lo | (hi << 32));
+}
+
+// The sum over the wave's lanes (float or double), in every lane.
+template <class T>
+__device__ __forceinline__ T wave_sum(T v) {
+    v += dpp<0x111>(v);
+    v += dpp<0x112>(v);
+    v += dpp<0x114>(v);
+    v += dpp<0x118>(v);
+    v += dpp<0x142, 0xa>(v);
+    v += dpp<0x143, 0xc>(v);
+    return lane63(v);
+}
+// The largest of non-negative values.
+__device__ __forceinline__ float wave_max_abs(float v) {
+    v = fmaxf(v, dpp<0x111>(v));
+    v = fmaxf(v, dpp<0x112>(v));
+    v = fmaxf(v, dpp<0x114>(v));
+    v = fmaxf(v, dpp<0x118>(v));
+    v = fmaxf(v, dpp<0x142, 0xa>(v));
+    v = fmaxf(v, dpp<0x143, 0xc>(v));
+    return lane63(v);
 }
 
 }  // namespace qg

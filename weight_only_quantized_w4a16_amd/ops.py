@@ -273,35 +273,42 @@ def qgemm_w4a8_fp8_grouped_dynamic(a_bf16, offsets_i32, packed, scales, y_bf16, 
 
 def _ptrs(*tensors):
     """Device addresses (None stays None) and the one device the tensors are on."""
-    dev = -1
+    dev = -2                                     # none yet; host tensors say -1
     out = []
     for t in tensors:
         if t is None:
             out.append(None)
             continue
-        if not t.is_cuda:
-            raise ValueError("tensor must be on the GPU")
-        if not t.is_contiguous():
-            raise ValueError("tensor must be contiguous")
         d = t.get_device()
         if d != dev:
+            if d < 0:
+                raise ValueError("tensor must be on the GPU")
             if dev >= 0:
                 raise ValueError("tensors must be on one device")
             dev = d
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
         out.append(t.data_ptr())
     if dev < 0:
         raise ValueError("no tensor was given")
     return out, dev
 
 
+# The current stream's handle and the current device without the Python objects
+# around them (1.2 and 0.1 us of a 6 us call), where this torch has these calls.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _launch(fn, dev, stream, *args):
     if stream is None:
-        raw = torch.cuda.current_stream(dev).cuda_stream
+        raw = _current_stream(dev)
     elif stream.device_index != dev:
         raise ValueError("the stream belongs to another device than the tensors")
     else:
         raw = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
