@@ -6,10 +6,12 @@ by DELTA, so it has to lie between the roundings of the fp64 value times
 
 DELTA = 2^-20 (16 fp32 roundings of 2^-24).  rms_norm: x + residual 1, the
 reciprocal root 1 (its sum is fp64), two products 2, the code's quotient 2.
-swiglu: the exponential 4 (product with its carry 1, hardware 2^t 2, sum 1),
-1 + e 1, g e 1, quotient 2, product with up 1, the code's quotient 2; below
--87 the exponential is a subnormal number that may vanish, an absolute error of
-2^-126 |g u| (|g| <= 256 below).
+swiglu: the hardware's 2^t 2, 1 + e 1, reciprocal 2, two products 2, the code's
+quotient 2.  The exponent t = -g log2 e is off by |t| (2^-24 + 2^-26) (its
+rounding, the constant's), which times ln 2 is a relative error of e of at most
+|g| 2^-23 and reaches the result as e / (1 + e) of that: less than 2^-24 for
+g >= 0, and |g| 2^-23 for g < 0.  Below -87 the reciprocal may vanish, an
+absolute error of 2^-126 |g u|.
 FLOOR = 2^-148 (two subnormal steps) bounds the absolute error of subnormal
 results.
 """
@@ -210,7 +212,7 @@ def test_swiglu(ops, M, I):
     gu = f32_to_bf16_bits(f)
     y64 = block.swiglu(f64(gu))
     gate, up = f64(gu)[:, :I], np.abs(f64(gu)[:, I:])
-    floor = FLOOR + np.where(gate < -87, 2.0 ** -126 * 256 * up, 0.0)
+    floor = FLOOR + np.where(gate < -87, 2.0 ** -126 * -gate * up, np.maximum(-gate, 0) * 2.0 ** -23 * np.abs(y64))
     what = f"M={M} I={I}"
     d = dev_bf16(gu)
     y, check_y = guarded((M, I), torch.bfloat16)

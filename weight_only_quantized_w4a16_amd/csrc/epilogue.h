@@ -1,8 +1,11 @@
 // What happens to a product's fp32 results before they are stored: nothing but
 // the rounding (NoEpilogue), or act(v + bias[n]) + residual[m, n] first.  A
-// kernel hands over the C results that a thread stores together, so that their
-// residuals are all requested before the first store (y may be the residual's
-// memory, and the compiler may not move a load over such a store).
+// kernel fetches the bias and residual of the results that a thread stores
+// together (an In) while other work is under way, and applies them before the
+// first store: y may be the residual's memory, so the compiler may not move a
+// load over such a store.  Measured at 1000 x 4096 x 14336 with a bias: 130 us
+// with the loads between the stores of each 32 x 32 block, against 118 us for
+// the plain product.
 #pragma once
 
 #include "device_common.h"
@@ -11,9 +14,17 @@ namespace qg {
 
 struct NoEpilogue {
     using out_ptr = uint16_t* __restrict__;
-    // v[i] becomes the value of row row(i), column col(i); only those with live(i) are read
-    template <int C, class V, class Live, class Row, class Col>
-    __device__ __forceinline__ void apply(V&, int, Live, Row, Col) const {}
+    static constexpr bool kActive = false;
+    template <int C>
+    struct In {};
+    __device__ __forceinline__ float bias_of(int) const { return 0.0f; }
+    // residuals (and with BIAS also biases) of the results i < C at row(i), col(i) for which live(i)
+    template <bool BIAS, int C, class Live, class Row, class Col>
+    __device__ __forceinline__ void fetch(In<C>&, int, Live, Row, Col) const {}
+    template <int C, class V>
+    __device__ __forceinline__ void apply(V&, const In<C>&) const {}
+    template <int C, class V>
+    __device__ __forceinline__ void apply(V&, const In<C>&, float) const {}
 };
 
 // qg_activation of include/qgemm.h
@@ -23,10 +34,9 @@ enum { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4
 // rounded to 8 bits of mantissa: hardware exp2 and reciprocal (1 unit in the
 // last place each; the exponent's own rounding adds |z| 2^-24).
 
-// x sigmoid(z) without overflow: exp(-|z|) <= 1
+// x sigmoid(z); far below zero the denominator is infinite and the result -0
 __device__ __forceinline__ float x_sigmoid(float x, float z) {
-    const float e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(z));
-    return (z < 0.0f ? x * e : x) * __builtin_amdgcn_rcpf(1.0f + e);
+    return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
 }
 
 // x Phi(x): the tail Phi(-|x|) = exp(-x^2 / 2) t P(t), t = 1 / (1 + 0.4 |x| /
@@ -77,23 +87,60 @@ __device__ __forceinline__ void activate(V& v, int act) {
 
 struct Epilogue {
     using out_ptr = uint16_t*;
+    static constexpr bool kActive = true;
     const uint16_t* bias;                        // [N] or null
     const uint16_t* residual;                    // [M, N] or null
     int act;
 
-    template <int C, class V, class Live, class Row, class Col>
-    __device__ __forceinline__ void apply(V& v, int N, Live live, Row row, Col col) const {
-        float r[C];
+    template <int C>
+    struct In {
+        uint32_t b[C], r[C];                     // bf16 bits
+    };
+    __device__ __forceinline__ float bias_of(int n) const { return bias ? bf16_to_f32(bias[n]) : 0.0f; }
+    // eight consecutive biases (n % 2 == 0; the pointer is 4-byte aligned)
+    __device__ __forceinline__ void bias8(float* b, int n) const {
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-            r[i] = residual && live(i) ? bf16_to_f32(residual[(size_t)row(i) * N + col(i)]) : 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = bias ? reinterpret_cast<const uint32_t*>(bias + n)[j] : 0u;
+            b[2 * j] = bf16_to_f32(w & 0xffffu);
+            b[2 * j + 1] = __uint_as_float(w & 0xffff0000u);
+        }
+    }
+    template <bool BIAS, int C, class Live, class Row, class Col>
+    __device__ __forceinline__ void fetch(In<C>& in, int N, Live live, Row row, Col col) const {
+        if (residual) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) in.r[i] = live(i) ? residual[(size_t)row(i) * N + col(i)] : 0u;
+        }
+        if (BIAS && bias) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) in.b[i] = live(i) ? bias[col(i)] : 0u;
+        }
+    }
+    template <int C, class V>
+    __device__ __forceinline__ void apply(V& v, const In<C>& in) const {
         if (bias) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) v[i] += live(i) ? bf16_to_f32(bias[col(i)]) : 0.0f;
+            for (int i = 0; i < C; ++i) v[i] += bf16_to_f32(in.b[i]);
         }
-        activate<C>(v, act);
+        finish<C>(v, in);
+    }
+    // results of one column, its bias already there
+    template <int C, class V>
+    __device__ __forceinline__ void apply(V& v, const In<C>& in, float b) const {
 #pragma unroll
-        for (int i = 0; i < C; ++i) v[i] += r[i];
+        for (int i = 0; i < C; ++i) v[i] += b;
+        finish<C>(v, in);
+    }
+
+private:
+    template <int C, class V>
+    __device__ __forceinline__ void finish(V& v, const In<C>& in) const {
+        activate<C>(v, act);
+        if (residual) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) v[i] += bf16_to_f32(in.r[i]);
+        }
     }
 };
 

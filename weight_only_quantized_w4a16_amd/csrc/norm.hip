@@ -24,20 +24,23 @@ namespace qg {
 
 struct FmtNone {                               // bf16 output only
     static constexpr float qmax = 1.0f;
-    __device__ static __forceinline__ uint32_t encode2(float, float) { return 0u; }
 };
 template <class Fmt>
 constexpr bool kCodes = !std::is_same<Fmt, FmtNone>::value;
 
-// The codes of eight values: quotients by the corrected reciprocal product
-// (three operations, within one unit in the last place of the IEEE quotient).
+// Four quotients -> four codes.  |q| exceeds q_max by roundings only (the scale
+// is the row's own maximum), so it rounds to the largest code without a clamp.
 template <class Fmt>
-__device__ __forceinline__ uint2 encode8(const float* y, float s, float r, bool fast) {
-    uint32_t b[4];
+__device__ __forceinline__ uint32_t encode4(const float* q) {
+    if constexpr (std::is_same<Fmt, FmtE4M3>::value) {
+        int c = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], c, true);
+    } else {
+        uint32_t c = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        b[j] = Fmt::encode2(dyn_quotient<Fmt>(y[2 * j], s, r, fast), dyn_quotient<Fmt>(y[2 * j + 1], s, r, fast));
-    return make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+        for (int j = 0; j < 4; ++j) c |= ((uint32_t)(int)rintf(q[j]) & 0xffu) << (8 * j);
+        return c;
+    }
 }
 
 // Reductions over the NT threads of a row (`red`: one LDS word per wave, used
@@ -87,6 +90,9 @@ __device__ __forceinline__ void row_sum_max(double& sum, float& top, double* red
     }
 }
 
+// The scale of a row and its codes: y times the rounded reciprocal of s (within
+// one unit in the last place of the IEEE quotient y / s); a scale too small for
+// a finite reciprocal divides.
 struct RowScale {
     float s, r;
     bool fast;
@@ -95,12 +101,21 @@ struct RowScale {
         RowScale q;
         q.s = amax / Fmt::qmax;                              // IEEE fp32 quotient
         q.r = 1.0f / q.s;
-        q.fast = q.s >= 0x1p-100f && q.s < __builtin_inff(); // a smaller one divides
+        q.fast = q.s >= 0x1p-100f;
         return q;
     }
     template <class Fmt>
     __device__ __forceinline__ uint2 codes(const float* y) const {
-        return s == 0.0f ? make_uint2(0u, 0u) : encode8<Fmt>(y, s, r, fast);
+        if (s == 0.0f) return make_uint2(0u, 0u);
+        float q[8];
+        if (fast) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = y[j] * r;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = y[j] / s;
+        }
+        return make_uint2(encode4<Fmt>(q), encode4<Fmt>(q + 4));
     }
 };
 
@@ -277,25 +292,28 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs p) {
     }
 }
 
-// Threads per row and chunks per thread of a row of `chunks` pieces: up to 128
-// pieces one wave; longer rows one workgroup.
-#ifndef QG_ROW_WIDE
-#define QG_ROW_WIDE 0
-#endif
+// Threads per row and chunks per thread of a row of `chunks` pieces: one wave up
+// to 128 pieces, else one workgroup with two to four chunks a thread (measured
+// against one chunk and 1024 threads, and against eight: norm to e4m3 at 8191 x
+// 8192 81 us, 93 and 83; swiglu to e4m3 at 8192 x 4096 30 us with 256 threads, 38
+// with 512).  `many` (coded rows, four a CU or more): one wave up to 256 pieces,
+// which saves the barriers (swiglu at 16384 / 256 x 2048 30 / 3.2 us against 37 /
+// 2.9; the bf16 norm, with one barrier, gains nothing).
 template <class Go>
-static bool with_row_shape(int M, int chunks, Go&& go) {
-    const bool wide = QG_ROW_WIDE;
-    (void)M;
+static bool with_row_shape(int chunks, bool many, Go&& go) {
     if (chunks <= 64) go(ic<64>{}, ic<1>{});
     else if (chunks <= 128) go(ic<64>{}, ic<2>{});
+    else if (chunks <= 192 && many) go(ic<64>{}, ic<3>{});
+    else if (chunks <= 256 && many) go(ic<64>{}, ic<4>{});
     else if (chunks <= 256) go(ic<256>{}, ic<1>{});
-    else if (chunks <= 512) { if (wide) go(ic<512>{}, ic<1>{}); else go(ic<256>{}, ic<2>{}); }
-    else if (chunks <= 1024) { if (wide) go(ic<1024>{}, ic<1>{}); else go(ic<256>{}, ic<4>{}); }
-    else if (chunks <= 2048) { if (wide) go(ic<1024>{}, ic<2>{}); else go(ic<256>{}, ic<8>{}); }
-    else if (chunks <= 4096) { if (wide) go(ic<1024>{}, ic<4>{}); else go(ic<512>{}, ic<8>{}); }
+    else if (chunks <= 512) go(ic<256>{}, ic<2>{});
+    else if (chunks <= 1024) go(ic<512>{}, ic<2>{});
+    else if (chunks <= 2048) go(ic<512>{}, ic<4>{});
+    else if (chunks <= 4096) go(ic<1024>{}, ic<4>{});
     else return false;
     return true;
 }
+static bool many_rows(int M) { return M >= 4 * device_cu_count(); }
 // workgroups and threads of M rows at NT threads a row
 template <int NT>
 static dim3 row_grid(int M) { return dim3(NT == 64 ? (M + 3) / 4 : M); }
@@ -304,7 +322,7 @@ static dim3 row_block() { return dim3(NT == 64 ? 256 : NT); }
 
 template <class Fmt>
 static void launch_norm(const NormArgs& p, hipStream_t st) {
-    const bool done = with_row_shape(p.M, p.K / 8, [&](auto nt, auto cpt) {
+    const bool done = with_row_shape(p.K / 8, kCodes<Fmt> && many_rows(p.M), [&](auto nt, auto cpt) {
         constexpr int NT = decltype(nt)::value, CPT = decltype(cpt)::value;
         hipLaunchKernelGGL((rms_norm_kernel<Fmt, NT, CPT>), row_grid<NT>(p.M), row_block<NT>(), 0, st, p);
     });
@@ -332,34 +350,18 @@ struct SwigluArgs {
     int M, I;
 };
 
-// exp(x) to about one unit in the last place: 2^(x log2 e) with the rounding
-// of the product carried into the result (the hardware's 2^t alone would be
-// off by |x| 2^-24).
-__device__ __forceinline__ float exp_f32(float x) {
-    constexpr float kLog2E = 1.44269504088896341f;
-    constexpr float kLog2ELo = 1.92596299e-8f;               // log2(e) - kLog2E
-    constexpr float kLn2 = 0.693147180559945309f;
-    const float t = x * kLog2E;
-    const float e = fmaf(x, kLog2ELo, fmaf(x, kLog2E, -t));
-    const float p = __builtin_amdgcn_exp2f(t);
-    return fmaf(p, e * kLn2, p);
-}
-
+// silu(g) u = g u / (1 + 2^(-g log2 e)) on the hardware's 2^t and reciprocal (one
+// unit in the last place each); the rounding of t adds |g| 2^-24 to the relative
+// error where the exponential dominates (g < 0).  A gate below -87 makes the
+// denominator infinite or its reciprocal vanish: the product is then -0, off by
+// less than 2^-126 |g u|.
 __device__ __forceinline__ void swiglu8(u32x4 gate, u32x4 up, float* y) {
     float g[8], u[8];
     unpack8(gate, g);
     unpack8(up, u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        // with e = exp(-|g|) <= 1 nothing overflows: the sigmoid is 1 / (1 + e)
-        // or e / (1 + e), and 1 + e lies in [1, 2]
-        const float e = exp_f32(-fabsf(g[j]));
-        const float n = g[j] < 0.0f ? g[j] * e : g[j];
-        const float d = 1.0f + e;
-        const float r = __builtin_amdgcn_rcpf(d);
-        const float a = n * r;
-        y[j] = fmaf(fmaf(-a, d, n), r, a) * u[j];
-    }
+    for (int j = 0; j < 8; ++j)
+        y[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g[j])) * u[j];
 }
 
 // no row reduction: the grid covers the chunks of all rows
@@ -435,7 +437,7 @@ __global__ __launch_bounds__(1024) void swiglu_quant_long_kernel(SwigluArgs p) {
 
 template <class Fmt>
 static void launch_swiglu_quant(const SwigluArgs& p, hipStream_t st) {
-    const bool done = with_row_shape(p.M, p.I / 8, [&](auto nt, auto cpt) {
+    const bool done = with_row_shape(p.I / 8, many_rows(p.M), [&](auto nt, auto cpt) {
         constexpr int NT = decltype(nt)::value, CPT = decltype(cpt)::value;
         hipLaunchKernelGGL((swiglu_quant_kernel<Fmt, NT, CPT>), row_grid<NT>(p.M), row_block<NT>(), 0, st, p);
     });

@@ -22,6 +22,7 @@
 #include "device_common.h"
 #include "epilogue.h"
 #include "launch.h"
+#include "rows.h"
 
 namespace qg {
 
@@ -239,6 +240,21 @@ __device__ __forceinline__ void small_m_tile(const uint16_t* __restrict__ a,
     const int nitems = (ng + U - 1) / U;          // the last item may be partial
     const Int4Unpacker unpack;
 
+    // output element o (of OUT) of this thread: (row, column) of the reduced tiles
+    constexpr int OUT = (CT * MT * 256 + NWAVE * 64 - 1) / (NWAVE * 64);
+    auto out_row = [&](int o) {
+        const int e = (int)threadIdx.x + o * NWAVE * 64;
+        return (e >> 8) % MT * 16 + 4 * (((e >> 2) & 63) >> 4) + (e & 3);
+    };
+    auto out_col = [&](int o) {
+        const int e = (int)threadIdx.x + o * NWAVE * 64;
+        return (nt0 + (e >> 8) / MT) * 16 + ((e >> 2) & 15);
+    };
+    auto out_live = [&](int o) { return (int)threadIdx.x + o * NWAVE * 64 < CT * MT * 256 && out_row(o) < M; };
+    typename EP::template In<OUT> ep_in;
+    // few outputs: their bias and residual wait in registers from the start
+    if constexpr (OUT <= 2) ep.template fetch<true>(ep_in, N, out_live, out_row, out_col);
+
     f32x4 total[CT][MT];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
@@ -355,6 +371,7 @@ __device__ __forceinline__ void small_m_tile(const uint16_t* __restrict__ a,
         }
     }
 
+    if constexpr (OUT > 2) ep.template fetch<true>(ep_in, N, out_live, out_row, out_col);
     __shared__ f32x4 red[NWAVE][CT][MT][64];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
@@ -362,22 +379,20 @@ __device__ __forceinline__ void small_m_tile(const uint16_t* __restrict__ a,
         for (int mt = 0; mt < MT; ++mt) red[wave][ct][mt][lane] = total[ct][mt];
     __syncthreads();
 
-    for (int e = threadIdx.x; e < CT * MT * 256; e += NWAVE * 64) {
-        const int i = e & 3;
-        const int l = (e >> 2) & 63;
-        const int cm = e >> 8;
-        const int mt = cm % MT;
-        const int ct = cm / MT;
-        const int m = mt * 16 + 4 * (l >> 4) + i;
-        if (m >= M) continue;
-        float sum = 0.0f;
+    float out[OUT];
 #pragma unroll
-        for (int w = 0; w < NWAVE; ++w) sum += red[w][ct][mt][l][i];
-        const int n = (nt0 + ct) * 16 + (l & 15);
-        float v[1] = {sum};
-        ep.template apply<1>(v, N, [](int) { return true; }, [&](int) { return m; }, [&](int) { return n; });
-        y[(size_t)m * N + n] = (uint16_t)f32_to_bf16_rne(v[0]);
+    for (int o = 0; o < OUT; ++o) {
+        out[o] = 0.0f;
+        if (!out_live(o)) continue;
+        const int e = (int)threadIdx.x + o * NWAVE * 64;
+        const int cm = e >> 8;
+#pragma unroll
+        for (int w = 0; w < NWAVE; ++w) out[o] += red[w][cm / MT][cm % MT][(e >> 2) & 63][e & 3];
     }
+    ep.template apply<OUT>(out, ep_in);
+#pragma unroll
+    for (int o = 0; o < OUT; ++o)
+        if (out_live(o)) y[(size_t)out_row(o) * N + out_col(o)] = (uint16_t)f32_to_bf16_rne(out[o]);
 }
 
 template <int MT, int CT, int NWAVE, int U, bool PIPE, class EP>
@@ -540,11 +555,21 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
     const bool direct = (KW == 1) && (S == 1);
     f32x4 total = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    // bias and residual of the tile under way, requested with its first chunk
+    typename EP::template In<4> ep_in;
+    float ep_bias = 0.0f;
+    auto ep_row = [&](int i) { return 4 * kq + i; };
+    auto ep_live = [&](int i) { return 4 * kq + i < M; };
+
     // ---- consume items in the same order
     int cp_chunk = 0, cp_tile = t0 + tslot;
     auto compute = [&](auto slot) {
         constexpr int sl = decltype(slot)::value;
         const int gl0 = gw0 + cp_chunk * U;      // group within the slice
+        if (EP::kActive && direct && cp_chunk == 0) {
+            ep_bias = ep.bias_of(cp_tile * 16 + col);
+            ep.template fetch<false>(ep_in, N, ep_live, ep_row, [&](int) { return cp_tile * 16 + col; });
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int g = gl0 + u;
@@ -567,8 +592,7 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
             const int tile = cp_tile;
             if (direct) {
                 const int n = tile * 16 + col;
-                ep.template apply<4>(total, N, [&](int i) { return 4 * kq + i < M; }, [&](int i) { return 4 * kq + i; },
-                                     [&](int) { return n; });
+                ep.template apply<4>(total, ep_in, ep_bias);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int m = 4 * kq + i;
@@ -592,6 +616,16 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
 
     // ---- reduction over the KW sub-ranges (LDS), then over the S slices
     const int T = t1 - t0;
+    // element e of the strip (tile e / 256, MFMA layout): its row and column
+    auto strip_row = [&](int e) { return 4 * (((e & 255) >> 2) >> 4) + (e & 3); };
+    auto strip_col = [&](int e) { return (t0 + (e >> 8)) * 16 + (((e & 255) >> 2) & 15); };
+    typename EP::template In<1> ep_one;
+    auto fetch_one = [&](int e) {                // whole K here: one element ahead
+        if (KW > 1 && S == 1)
+            ep.template fetch<true>(ep_one, N, [&](int) { return e < T * 256 && strip_row(e) < M; },
+                                    [&](int) { return strip_row(e); }, [&](int) { return strip_col(e); });
+    };
+    fetch_one(tid);
     if (KW > 1) __syncthreads();
     for (int e = tid; KW > 1 && e < T * 256; e += DK_NWAVE * 64) {
         const int tl = e >> 8;
@@ -603,7 +637,8 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
             const int m = 4 * ((r >> 2) >> 4) + (r & 3);
             const int n = (t0 + tl) * 16 + ((r >> 2) & 15);
             float o[1] = {v};
-            ep.template apply<1>(o, N, [&](int) { return m < M; }, [&](int) { return m; }, [&](int) { return n; });
+            ep.template apply<1>(o, ep_one);
+            fetch_one(e + DK_NWAVE * 64);        // another element than the one stored next
             if (m < M) y[(size_t)m * N + n] = (uint16_t)f32_to_bf16_rne(o[0]);
         } else {
             __hip_atomic_store(&part[((size_t)split * NT + t0 + tl) * 256 + r], v, __ATOMIC_RELAXED,
@@ -618,6 +653,12 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
     constexpr int EB = 4;
     for (int e0 = tid; e0 < T * 256; e0 += DK_NWAVE * 64 * EB) {
         float v[EB];
+        typename EP::template In<EB> ep_eb;
+        ep.template fetch<true>(ep_eb, N, [&](int b) {
+                const int e = e0 + b * DK_NWAVE * 64;
+                return e < T * 256 && strip_row(e) < M;
+            }, [&](int b) { return strip_row(e0 + b * DK_NWAVE * 64); },
+            [&](int b) { return strip_col(e0 + b * DK_NWAVE * 64); });
 #pragma unroll
         for (int b = 0; b < EB; ++b) v[b] = 0.0f;
         for (int k0 = 0; k0 < S; k0 += 8) {
@@ -638,12 +679,7 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[b] += pv[b][k];
         }
-        auto row = [&](int b) { const int r = (e0 + b * DK_NWAVE * 64) & 255; return 4 * ((r >> 2) >> 4) + (r & 3); };
-        auto column = [&](int b) {
-            const int e = e0 + b * DK_NWAVE * 64;
-            return (t0 + (e >> 8)) * 16 + (((e & 255) >> 2) & 15);
-        };
-        ep.template apply<EB>(v, N, [&](int b) { return e0 + b * DK_NWAVE * 64 < T * 256 && row(b) < M; }, row, column);
+        ep.template apply<EB>(v, ep_eb);
 #pragma unroll
         for (int b = 0; b < EB; ++b) {
             const int e = e0 + b * DK_NWAVE * 64;
@@ -729,6 +765,74 @@ constexpr int LM_BM = 128;
 #ifndef QG_LM_STAGGER              // 1: the two rows of waves scale their group sums half a step apart
 #define QG_LM_STAGGER 1
 #endif
+
+// The end of a whole-K tile with an epilogue.  The accumulators hold one column
+// per lane; handed over through LDS (the stages are free by then), every lane gets
+// eight consecutive columns of a row instead, so bias, residual and output move
+// 16 bytes at a time and a result costs about five instructions beside its
+// activation.  No other work covers a tile's end (LDS holds one workgroup per
+// CU), so its instructions count: 1000 x 4096 x 14336 with a bias took 126 us with
+// the per-column stores of the plain product's end, for which see below.
+// region(w): wave w's WROWS x (32 NBW) floats.
+template <int WROWS, int NBW, class EP, class Region>
+__device__ __forceinline__ void large_m_finish(const f32x16 (&total)[WROWS / 32][NBW], Region region, int m_first,
+                                               int n_first, uint16_t* y, int M, int N, const EP& ep) {
+    constexpr int TW = 32 * NBW;                 // columns of the wave
+    constexpr int PPR = TW / 8;                  // pieces of eight columns per row
+    constexpr int P = WROWS * PPR / 64;          // pieces per lane: rows r0 + p * (64 / PPR)
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r0 = lane / PPR;
+    const int n = n_first + (lane % PPR) * 8;
+    const bool in_n = n < N;                     // N % 16 == 0: a piece is inside or outside
+    float bias[8];
+    ep.bias8(bias, in_n ? n : 0);
+    u32x4 res[P];
+    if (ep.residual) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int m = min(m_first + r0 + p * (64 / PPR), M - 1);
+            res[p] = *reinterpret_cast<const u32x4*>(ep.residual + (size_t)m * N + (in_n ? n : 0));
+        }
+    }
+    // every copy into the stages has landed and every wave is past its reads
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    float* t = region(wave);
+    // rows r and r + 4 are written together: in 64-column rows their halves swap
+    // so that the two land in different banks
+    auto at = [](int r, int c) { return r * TW + (NBW == 2 ? c ^ ((r & 4) << 3) : c); };
+#pragma unroll
+    for (int mi = 0; mi < WROWS / 32; ++mi)
+#pragma unroll
+        for (int bb = 0; bb < NBW; ++bb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                t[at(mi * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3), bb * 32 + (lane & 31))] = total[mi][bb][i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the wave's own region: its LDS accesses are in order
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int r = r0 + p * (64 / PPR);
+        const float* src = t + at(r, (lane % PPR) * 8);
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = lo[j] + bias[j];
+            v[4 + j] = hi[j] + bias[4 + j];
+        }
+        activate<8>(v, ep.act);
+        if (ep.residual) {
+            float f[8];
+            unpack8(res[p], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += f[j];
+        }
+        const int m = m_first + r;
+        if (in_n && m < M) *reinterpret_cast<u32x4*>(y + (size_t)m * N + n) = pack8(v);
+    }
+}
 
 // The work of one workgroup: output tile `tile` (of `tiles`) of K slice `split`.
 // BM = 128 rows (two 32-row blocks per wave) or 64 (one block per wave: half
@@ -961,7 +1065,18 @@ __device__ __forceinline__ void large_m_tile(
         static_for<NS>([&](auto s) { step(s, rows_live && g + decltype(s)::value < G); });
     if (STAGGER && pend) scale_into_total(sprev);
 
-    if (S == 1) {
+    if constexpr (EP::kActive) {
+      if (S == 1) {
+        large_m_finish<WROWS, NBW, EP>(total, [&](int w) {
+            // the waves' fp32 sub-tiles over the stages: as many as fit into each
+            constexpr int per = sizeof(Stage) / (WROWS * 32 * NBW * sizeof(float));
+            static_assert(3 * per >= 8 && NS == 3, "sub-tiles fit into the stages");
+            Stage* st = w < per ? &S0 : w < 2 * per ? &S1 : &S2x[0];
+            return reinterpret_cast<float*>(st) + (w % per) * (WROWS * 32 * NBW);
+        }, m0 + wm * WROWS, nt0 * 16 + wn * 32 * NBW, y, M, N, ep);
+        return;
+      }
+    } else if (S == 1) {
 #pragma unroll
         for (int bb = 0; bb < NBW; ++bb) {
             const int nt = nt0 + wn * 2 * NBW + 2 * bb + ((lane & 31) >> 4);
@@ -969,11 +1084,9 @@ __device__ __forceinline__ void large_m_tile(
             const int n = nt * 16 + (lane & 15);
 #pragma unroll
             for (int mi = 0; mi < MI; ++mi) {
-                auto row = [&](int i) { return m0 + wm * WROWS + mi * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); };
-                ep.template apply<16>(total[mi][bb], N, [&](int i) { return row(i) < M; }, row, [&](int) { return n; });
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int m = row(i);
+                    const int m = m0 + wm * WROWS + mi * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
                     if (m < M) y[(size_t)m * N + n] = (uint16_t)f32_to_bf16_rne(total[mi][bb][i]);
                 }
             }
@@ -1011,6 +1124,11 @@ __device__ __forceinline__ void large_m_tile(
     constexpr int EB = 8;
     for (int e0 = tid; e0 < BM * BN; e0 += 512 * EB) {
         float v[EB];
+        typename EP::template In<EB> ep_eb;
+        auto row = [&](int b) { return m0 + (e0 + b * 512) / BN; };
+        auto column = [&](int b) { return n0 + (e0 + b * 512) % BN; };
+        ep.template fetch<true>(ep_eb, N, [&](int b) { return e0 + b * 512 < BM * BN && row(b) < M && column(b) < N; }, row,
+                                column);
 #pragma unroll
         for (int b = 0; b < EB; ++b) v[b] = 0.0f;
         for (int k0 = 0; k0 < S; k0 += 4) {
@@ -1033,9 +1151,7 @@ __device__ __forceinline__ void large_m_tile(
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[b] += pv[b][k];
         }
-        auto row = [&](int b) { return m0 + (e0 + b * 512) / BN; };
-        auto column = [&](int b) { return n0 + (e0 + b * 512) % BN; };
-        ep.template apply<EB>(v, N, [&](int b) { return e0 + b * 512 < BM * BN && row(b) < M && column(b) < N; }, row, column);
+        ep.template apply<EB>(v, ep_eb);
 #pragma unroll
         for (int b = 0; b < EB; ++b) {
             const int e = e0 + b * 512;
