@@ -17,14 +17,15 @@ struct NoEpilogue {
     static constexpr bool kActive = false;
     template <int C>
     struct In {};
-    __device__ __forceinline__ float bias_of(int) const { return 0.0f; }
-    // residuals (and with BIAS also biases) of the results i < C at row(i), col(i) for which live(i)
-    template <bool BIAS, int C, class Live, class Row, class Col>
-    __device__ __forceinline__ void fetch(In<C>&, int, Live, Row, Col) const {}
+    __device__ __forceinline__ uint32_t bias_bits(int) const { return 0u; }
+    // residuals (and with BIAS also biases) of the results i < C at row(i), col(i); results
+    // outside M x N get the nearest one's, which saves a branch each
+    template <bool BIAS, int C, class Row, class Col>
+    __device__ __forceinline__ void fetch(In<C>&, int, int, Row, Col) const {}
     template <int C, class V>
     __device__ __forceinline__ void apply(V&, const In<C>&) const {}
     template <int C, class V>
-    __device__ __forceinline__ void apply(V&, const In<C>&, float) const {}
+    __device__ __forceinline__ void apply(V&, const In<C>&, uint32_t) const {}
 };
 
 // qg_activation of include/qgemm.h
@@ -96,7 +97,8 @@ struct Epilogue {
     struct In {
         uint32_t b[C], r[C];                     // bf16 bits
     };
-    __device__ __forceinline__ float bias_of(int n) const { return bias ? bf16_to_f32(bias[n]) : 0.0f; }
+    // the bits as loaded: nothing waits for them before they are used
+    __device__ __forceinline__ uint32_t bias_bits(int n) const { return bias ? bias[n] : 0u; }
     // eight consecutive biases (n % 2 == 0; the pointer is 4-byte aligned)
     __device__ __forceinline__ void bias8(float* b, int n) const {
 #pragma unroll
@@ -106,15 +108,15 @@ struct Epilogue {
             b[2 * j + 1] = __uint_as_float(w & 0xffff0000u);
         }
     }
-    template <bool BIAS, int C, class Live, class Row, class Col>
-    __device__ __forceinline__ void fetch(In<C>& in, int N, Live live, Row row, Col col) const {
+    template <bool BIAS, int C, class Row, class Col>
+    __device__ __forceinline__ void fetch(In<C>& in, int M, int N, Row row, Col col) const {
         if (residual) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) in.r[i] = live(i) ? residual[(size_t)row(i) * N + col(i)] : 0u;
+            for (int i = 0; i < C; ++i) in.r[i] = residual[(size_t)min(row(i), M - 1) * N + min(col(i), N - 1)];
         }
         if (BIAS && bias) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) in.b[i] = live(i) ? bias[col(i)] : 0u;
+            for (int i = 0; i < C; ++i) in.b[i] = bias[min(col(i), N - 1)];
         }
     }
     template <int C, class V>
@@ -125,9 +127,10 @@ struct Epilogue {
         }
         finish<C>(v, in);
     }
-    // results of one column, its bias already there
+    // results of one column, its bias bits already there
     template <int C, class V>
-    __device__ __forceinline__ void apply(V& v, const In<C>& in, float b) const {
+    __device__ __forceinline__ void apply(V& v, const In<C>& in, uint32_t bits) const {
+        const float b = bf16_to_f32(bits);
 #pragma unroll
         for (int i = 0; i < C; ++i) v[i] += b;
         finish<C>(v, in);

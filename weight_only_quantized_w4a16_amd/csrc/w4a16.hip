@@ -253,7 +253,7 @@ __device__ __forceinline__ void small_m_tile(const uint16_t* __restrict__ a,
     auto out_live = [&](int o) { return (int)threadIdx.x + o * NWAVE * 64 < CT * MT * 256 && out_row(o) < M; };
     typename EP::template In<OUT> ep_in;
     // few outputs: their bias and residual wait in registers from the start
-    if constexpr (OUT <= 2) ep.template fetch<true>(ep_in, N, out_live, out_row, out_col);
+    if constexpr (OUT <= 2) ep.template fetch<true>(ep_in, M, N, out_row, out_col);
 
     f32x4 total[CT][MT];
 #pragma unroll
@@ -371,7 +371,7 @@ __device__ __forceinline__ void small_m_tile(const uint16_t* __restrict__ a,
         }
     }
 
-    if constexpr (OUT > 2) ep.template fetch<true>(ep_in, N, out_live, out_row, out_col);
+    if constexpr (OUT > 2) ep.template fetch<true>(ep_in, M, N, out_row, out_col);
     __shared__ f32x4 red[NWAVE][CT][MT][64];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
@@ -509,6 +509,18 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
         ++ld_item;
         if (++ld_chunk == nchunk) { ld_chunk = 0; ld_tile += TW; }
     };
+    // bias and residual of the wave's next whole tile, requested before the
+    // weights that they would otherwise wait for
+    const bool direct = (KW == 1) && (S == 1);
+    typename EP::template In<4> ep_in;
+    uint32_t ep_bias = 0u;
+    auto fetch_tile = [&](int tile) {
+        if (EP::kActive && direct && tile < t1) {
+            ep_bias = ep.bias_bits(tile * 16 + col);
+            ep.template fetch<false>(ep_in, M, N, [&](int i) { return 4 * kq + i; }, [&](int) { return tile * 16 + col; });
+        }
+    };
+    fetch_tile(t0 + tslot);
     // ---- stage the activation slice, with the first weight requests in flight
     const int cpr = Gs * 16;                     // 16-byte chunks per staged row
     if (cpr % 64 == 0) {
@@ -552,24 +564,13 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
     const float* crow = corr + 4 * kq;
     const int sidx = (col >> 1) << 2;            // ds_bpermute byte address of lane col/2
     const int shalf = (col & 1) << 4;
-    const bool direct = (KW == 1) && (S == 1);
     f32x4 total = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    // bias and residual of the tile under way, requested with its first chunk
-    typename EP::template In<4> ep_in;
-    float ep_bias = 0.0f;
-    auto ep_row = [&](int i) { return 4 * kq + i; };
-    auto ep_live = [&](int i) { return 4 * kq + i < M; };
 
     // ---- consume items in the same order
     int cp_chunk = 0, cp_tile = t0 + tslot;
     auto compute = [&](auto slot) {
         constexpr int sl = decltype(slot)::value;
         const int gl0 = gw0 + cp_chunk * U;      // group within the slice
-        if (EP::kActive && direct && cp_chunk == 0) {
-            ep_bias = ep.bias_of(cp_tile * 16 + col);
-            ep.template fetch<false>(ep_in, N, ep_live, ep_row, [&](int) { return cp_tile * 16 + col; });
-        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int g = gl0 + u;
@@ -598,6 +599,7 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
                     const int m = 4 * kq + i;
                     if (m < M) y[(size_t)m * N + n] = (uint16_t)f32_to_bf16_rne(total[i]);
                 }
+                fetch_tile(tile + TW);
             } else if (KW == 1) {                // whole tile in this wave: publish the slot
                 float* dst = part + ((size_t)split * NT + tile) * 256 + lane * 4;
 #pragma unroll
@@ -622,8 +624,7 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
     typename EP::template In<1> ep_one;
     auto fetch_one = [&](int e) {                // whole K here: one element ahead
         if (KW > 1 && S == 1)
-            ep.template fetch<true>(ep_one, N, [&](int) { return e < T * 256 && strip_row(e) < M; },
-                                    [&](int) { return strip_row(e); }, [&](int) { return strip_col(e); });
+            ep.template fetch<true>(ep_one, M, N, [&](int) { return strip_row(e); }, [&](int) { return strip_col(e); });
     };
     fetch_one(tid);
     if (KW > 1) __syncthreads();
@@ -654,11 +655,8 @@ __global__ __launch_bounds__(DK_NWAVE * 64) void w4a16_decode_kernel(
     for (int e0 = tid; e0 < T * 256; e0 += DK_NWAVE * 64 * EB) {
         float v[EB];
         typename EP::template In<EB> ep_eb;
-        ep.template fetch<true>(ep_eb, N, [&](int b) {
-                const int e = e0 + b * DK_NWAVE * 64;
-                return e < T * 256 && strip_row(e) < M;
-            }, [&](int b) { return strip_row(e0 + b * DK_NWAVE * 64); },
-            [&](int b) { return strip_col(e0 + b * DK_NWAVE * 64); });
+        ep.template fetch<true>(ep_eb, M, N, [&](int b) { return strip_row(e0 + b * DK_NWAVE * 64); },
+                                [&](int b) { return strip_col(e0 + b * DK_NWAVE * 64); });
 #pragma unroll
         for (int b = 0; b < EB; ++b) v[b] = 0.0f;
         for (int k0 = 0; k0 < S; k0 += 8) {
@@ -1127,8 +1125,7 @@ __device__ __forceinline__ void large_m_tile(
         typename EP::template In<EB> ep_eb;
         auto row = [&](int b) { return m0 + (e0 + b * 512) / BN; };
         auto column = [&](int b) { return n0 + (e0 + b * 512) % BN; };
-        ep.template fetch<true>(ep_eb, N, [&](int b) { return e0 + b * 512 < BM * BN && row(b) < M && column(b) < N; }, row,
-                                column);
+        ep.template fetch<true>(ep_eb, M, N, row, column);
 #pragma unroll
         for (int b = 0; b < EB; ++b) v[b] = 0.0f;
         for (int k0 = 0; k0 < S; k0 += 4) {
