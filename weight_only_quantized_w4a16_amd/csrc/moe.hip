@@ -390,6 +390,9 @@ void launch_moe_dispatch(const int* ids, const void* rows, const float* scale, i
     if (rows) launch_moe_gather(rows, scale, row_of_slot, B, k, row_bytes, out, scale_out, st);
 }
 
+// STREAM: the experts' rows, dead after this, pass the caches by (8192 tokens of
+// top-8, 2048 bf16, 57 us without, 52 with; 4096 of top-2, 4096 bf16, 26.5 and 22).
+template <bool STREAM>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const u32x4* __restrict__ rows,
                                                           const int* __restrict__ row_of_slot,
                                                           const float* __restrict__ weights, const u32x4* residual, int B,
@@ -415,7 +418,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const u32x4* __restric
         }
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j)
-            if ((unsigned)r[j] < (unsigned)T) v[j] = rows[(size_t)r[j] * chunks + c];
+            if ((unsigned)r[j] < (unsigned)T) v[j] = load_row<STREAM>(rows + (size_t)r[j] * chunks + c);
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
             if ((unsigned)r[j] >= (unsigned)T) continue;
@@ -438,9 +441,14 @@ void launch_moe_combine(const uint16_t* rows, const int* row_of_slot, const floa
                         int B, int k, int K, uint16_t* y, hipStream_t st) {
     const int chunks = K / 8;
     const TokenGrid g = token_grid(B, chunks);
-    hipLaunchKernelGGL(moe_combine_kernel, dim3(g.blocks), dim3(256), 0, st, reinterpret_cast<const u32x4*>(rows),
-                       row_of_slot, weights, reinterpret_cast<const u32x4*>(residual), B, k, chunks, g.span_log2,
-                       g.parts, reinterpret_cast<u32x4*>(y));
+    auto go = [&](auto stream) {
+        hipLaunchKernelGGL(moe_combine_kernel<decltype(stream)::value>, dim3(g.blocks), dim3(256), 0, st,
+                           reinterpret_cast<const u32x4*>(rows), row_of_slot, weights,
+                           reinterpret_cast<const u32x4*>(residual), B, k, chunks, g.span_log2, g.parts,
+                           reinterpret_cast<u32x4*>(y));
+    };
+    if ((size_t)B * k * K * 2 > kStreamBytes) go(std::true_type{});
+    else go(std::false_type{});
 }
 
 // One workgroup per token: its threads hold the pieces of dy, and the slots'
@@ -481,7 +489,7 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
                     float d[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) d[i] = w[j] * g[i];
-                    drows[at] = pack8(d);
+                    __builtin_nontemporal_store(pack8(d), drows + at);
                 }
             }
         }

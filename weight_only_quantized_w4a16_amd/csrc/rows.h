@@ -27,6 +27,23 @@ __device__ __forceinline__ u32x4 pack8(const float* f) {
     return u32x4{w[0], w[1], w[2], w[3]};
 }
 
+// ---- streamed rows -----------------------------------------------------------
+// Bytes that nothing reads again soon (an input at its last use, an output that
+// the caches cannot hold until its reader comes) go past the caches with the
+// non-temporal hint, which leaves them to what is read again.
+template <bool STREAM, class T>
+__device__ __forceinline__ T load_row(const T* p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool STREAM, class T>
+__device__ __forceinline__ void store_row(T* p, T v) {
+    if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+// rows that count as such: more than the XCDs' L2s hold together
+constexpr size_t kStreamBytes = size_t(32) << 20;
+
 // ---- wave reductions on DPP moves ------------------------------------------
 // Row shifts by 1, 2, 4, 8 and the row broadcasts 15 and 31 leave the result of
 // all 64 lanes in lane 63, a few cycles a step (a shuffle through LDS takes
