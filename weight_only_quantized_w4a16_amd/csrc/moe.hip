@@ -27,11 +27,14 @@ namespace qg {
 // slots (one workgroup, `seg` slots) counts its experts into hist[i][e]; then
 // every segment derives the first row of each expert (totals over all segments)
 // and of its own share (totals over the segments before it), and numbers its
-// slots in order.  Few large segments: the work is latency, not bandwidth.
+// slots in order.  Few large segments: the work is latency, not bandwidth.  Up to
+// SORT_MAX_SEGS segments hold SORT_NT * SORT_REG slots, which the threads keep in
+// registers (REG); beyond, segments grow and are read twice.
 // ---------------------------------------------------------------------------
 constexpr int SORT_WAVES = 16;
 constexpr int SORT_NT = SORT_WAVES * 64;
-constexpr int SORT_MIN_SEG = 4 * SORT_NT;
+constexpr int SORT_REG = 4;
+constexpr int SORT_MIN_SEG = SORT_REG * SORT_NT;
 constexpr int SORT_MAX_SEGS = 256;
 
 // slots per segment, a multiple of SORT_NT
@@ -47,9 +50,13 @@ __global__ __launch_bounds__(SORT_NT) void moe_count_kernel(const int* __restric
     __syncthreads();
     const int s0 = blockIdx.x * seg;
     const int s1 = min(s0 + seg, T);
-    for (int s = s0 + (int)threadIdx.x; s < s1; s += SORT_NT) {
-        const int e = ids[s];
-        if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+    for (int s = s0 + (int)threadIdx.x; s < s1; s += SORT_REG * SORT_NT) {
+        int e[SORT_REG];
+#pragma unroll
+        for (int i = 0; i < SORT_REG; ++i) e[i] = s + i * SORT_NT < s1 ? ids[s + i * SORT_NT] : -1;
+#pragma unroll
+        for (int i = 0; i < SORT_REG; ++i)
+            if (e[i] >= 0 && e[i] < E) atomicAdd(&count[e[i]], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += SORT_NT) hist[(size_t)blockIdx.x * E + e] = count[e];
@@ -100,6 +107,7 @@ __device__ __forceinline__ void scan_experts(const int* all, int E, int* first, 
 // LDS words of moe_place_kernel
 static int place_words(int E) { return (2 + SORT_WAVES) * E; }
 
+template <bool REG>
 __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restrict__ ids, int T, int E, int bits, int seg,
                                                             const int* __restrict__ hist, int* __restrict__ offsets,
                                                             int* __restrict__ row_of_slot) {
@@ -113,6 +121,16 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
     const int wave = tid >> 6;
     const int nseg = gridDim.x;
     const int mine = blockIdx.x;
+
+    // each wave numbers a contiguous part of the segment, 64 slots at a time
+    const int per = seg / SORT_WAVES;
+    const int s0 = mine * seg + wave * per;
+    const int s1 = min(s0 + per, T);
+    int held[SORT_REG];
+    if constexpr (REG) {
+#pragma unroll
+        for (int i = 0; i < SORT_REG; ++i) held[i] = s0 + i * 64 + lane < s1 ? ids[s0 + i * 64 + lane] : -1;
+    }
 
     // totals over the segments: SORT_NT / 2^bits threads share an expert's column
     // (up to 2^10 experts: one thread each at least)
@@ -135,14 +153,16 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
             atomicAdd(&first[e], before);
         }
     }
-    // meanwhile each wave counts its contiguous part of the segment
-    const int per = seg / SORT_WAVES;
-    const int s0 = mine * seg + wave * per;
-    const int s1 = min(s0 + per, T);
+    // meanwhile each wave counts its part
     int* cnt = next + wave * E;
-    for (int s = s0 + lane; s < s1; s += 64) {
-        const int e = ids[s];
+    auto count = [&](int e) {
         if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+    };
+    if constexpr (REG) {
+#pragma unroll
+        for (int i = 0; i < SORT_REG; ++i) count(held[i]);
+    } else {
+        for (int s = s0 + lane; s < s1; s += 64) count(ids[s]);
     }
     __syncthreads();
     // counts become the first row of each (expert, wave)
@@ -156,9 +176,7 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
     }
     __syncthreads();
     scan_experts<SORT_WAVES>(all, E, first, mine == 0 ? offsets : nullptr, wave_total);
-    for (int s = s0; s < s1; s += 64) {          // uniform in the wave
-        const bool in = s + lane < s1;
-        const int e = in ? ids[s + lane] : -1;
+    auto number = [&](int s, int e) {            // all lanes of the wave; s: the first lane's slot
         const bool kept = e >= 0 && e < E;
         const uint64_t live = __ballot(kept);
         const uint64_t m = same_key(kept ? e : 0, bits, live);
@@ -171,7 +189,13 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
         __builtin_amdgcn_wave_barrier();         // every lane has read before one writes
         if (kept && (m >> lane) == 1ull) cnt[e] = at + __popcll(m);   // the last lane of each key
         __builtin_amdgcn_wave_barrier();
-        if (in) row_of_slot[s + lane] = row;
+        if (s + lane < s1) row_of_slot[s + lane] = row;
+    };
+    if constexpr (REG) {
+#pragma unroll
+        for (int i = 0; i < SORT_REG; ++i) number(s0 + i * 64, held[i]);
+    } else {
+        for (int s = s0; s < s1; s += 64) number(s, s + lane < s1 ? ids[s + lane] : -1);   // uniform bounds
     }
 }
 
@@ -186,13 +210,18 @@ static void launch_sort(const int* ids, int T, int E, int* offsets, int* row_of_
     const int nseg = (T + seg - 1) / seg;
     int* hist = static_cast<int*>(ws);
     hipLaunchKernelGGL(moe_count_kernel, dim3(nseg), dim3(SORT_NT), E * sizeof(int), st, ids, T, E, seg, hist);
-    static std::atomic<uint64_t> lds_set{0};
     const int bytes = place_words(E) * (int)sizeof(int);
-    if (bytes > 60 * 1024)                       // beside the static words, over the default limit of 64 KiB
-        allow_dynamic_lds(reinterpret_cast<const void*>(&moe_place_kernel), place_words(kGroupedMaxExperts) * (int)sizeof(int),
-                          lds_set);
-    hipLaunchKernelGGL(moe_place_kernel, dim3(nseg), dim3(SORT_NT), bytes, st, ids, T, E, bits_of(E), seg, hist, offsets,
-                       row_of_slot);
+    auto place = [&](auto reg) {
+        constexpr bool REG = decltype(reg)::value;
+        static std::atomic<uint64_t> lds_set{0};
+        if (bytes > 60 * 1024)                   // with the static words, over the default limit of 64 KiB
+            allow_dynamic_lds(reinterpret_cast<const void*>(&moe_place_kernel<REG>),
+                              place_words(kGroupedMaxExperts) * (int)sizeof(int), lds_set);
+        hipLaunchKernelGGL(moe_place_kernel<REG>, dim3(nseg), dim3(SORT_NT), bytes, st, ids, T, E, bits_of(E), seg, hist,
+                           offsets, row_of_slot);
+    };
+    if (seg == SORT_MIN_SEG) place(std::true_type{});
+    else place(std::false_type{});
 }
 
 // offsets of a call without slots
@@ -452,11 +481,16 @@ void launch_moe_combine(const uint16_t* rows, const int* row_of_slot, const floa
 }
 
 // One workgroup per token: its threads hold the pieces of dy, and the slots'
-// products <dy, row> are reduced over the workgroup, J slots at a time.
-template <int J>
+// products <dy, row> are reduced over the workgroup, J slots and SLOTS / J pieces a
+// thread at a time (J = 2, 4 or 8, the least that covers k: with 8 alone, 4096
+// tokens of top-2, 4096 bf16, took 37 us).
+// STREAM: drows, more than the caches hold until its reader comes, passes them by
+// (8192 / 4099 tokens of top-8, 2048 bf16, 112 / 59 us without, 91 / 49 with).
+template <int J, bool STREAM>
 __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
     const u32x4* __restrict__ dy, const u32x4* __restrict__ rows, const int* __restrict__ row_of_slot,
     const float* __restrict__ weights, int B, int k, int chunks, u32x4* __restrict__ drows, float* __restrict__ dweights) {
+    constexpr int U = SLOTS / J;
     __shared__ float red[4][J];
     const int b = blockIdx.x;
     const int T = B * k;
@@ -472,24 +506,39 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
             w[j] = in && weights ? weights[b * k + j0 + j] : 1.0f;
             dot[j] = 0.0f;
         }
-        for (int c = tid; c < chunks; c += 256) {
-            float g[8];
-            unpack8(dy[(size_t)b * chunks + c], g);
+        for (int c0 = tid; c0 < chunks; c0 += 256 * U) {
+            u32x4 d[U], v[U][J];
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                if (r[j] < 0) continue;
-                const size_t at = (size_t)r[j] * chunks + c;
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * 256;
+                if (c >= chunks) continue;
+                d[u] = dy[(size_t)b * chunks + c];
                 if (dweights) {
-                    float v[8];
-                    unpack8(rows[at], v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], v[i], dot[j]);
+                    for (int j = 0; j < J; ++j)
+                        if (r[j] >= 0) v[u][j] = rows[(size_t)r[j] * chunks + c];
                 }
-                if (drows) {
-                    float d[8];
+            }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] = w[j] * g[i];
-                    __builtin_nontemporal_store(pack8(d), drows + at);
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * 256;
+                if (c >= chunks) continue;
+                float g[8];
+                unpack8(d[u], g);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if (r[j] < 0) continue;
+                    float f[8];
+                    if (drows) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = w[j] * g[i];
+                        store_row<STREAM>(drows + (size_t)r[j] * chunks + c, pack8(f));
+                    }
+                    if (dweights) {
+                        unpack8(v[u][j], f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
+                    }
                 }
             }
         }
@@ -509,9 +558,18 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
 
 void launch_moe_combine_backward(const uint16_t* dy, const uint16_t* rows, const int* row_of_slot, const float* weights,
                                  int B, int k, int K, uint16_t* drows, float* dweights, hipStream_t st) {
-    hipLaunchKernelGGL(moe_combine_backward_kernel<8>, dim3(B), dim3(256), 0, st, reinterpret_cast<const u32x4*>(dy),
-                       reinterpret_cast<const u32x4*>(rows), row_of_slot, weights, B, k, K / 8,
-                       reinterpret_cast<u32x4*>(drows), dweights);
+    auto go = [&](auto j, auto stream) {
+        hipLaunchKernelGGL((moe_combine_backward_kernel<decltype(j)::value, decltype(stream)::value>), dim3(B), dim3(256),
+                           0, st, reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(rows), row_of_slot,
+                           weights, B, k, K / 8, reinterpret_cast<u32x4*>(drows), dweights);
+    };
+    auto by_k = [&](auto stream) {
+        if (k <= 2) go(ic<2>{}, stream);
+        else if (k <= 4) go(ic<4>{}, stream);
+        else go(ic<8>{}, stream);
+    };
+    if ((size_t)B * k * K * 2 >= kStreamBytes) by_k(std::true_type{});
+    else by_k(std::false_type{});
 }
 
 }  // namespace qg
