@@ -83,7 +83,8 @@ def dispatch(ops, ids, E, rows=None, scale=None):
 
 
 SORTS = [(1, 1, 1), (1, 8, 128), (2, 3, 5), (4, 8, 128), (16, 8, 128), (31, 2, 1024), (64, 4, 60), (100, 5, 3),
-         (128, 8, 128), (257, 8, 128), (511, 4, 64), (1000, 3, 1024), (4099, 8, 256), (9000, 1, 7), (70001, 4, 65)]
+         (128, 8, 128), (257, 8, 128), (511, 4, 64), (1000, 3, 1024), (4099, 8, 256), (9000, 1, 7), (70001, 4, 65),
+         (300, 17, 40), (700, 9, 128), (1048577, 1, 64), (300000, 4, 1024)]
 
 
 @pytest.mark.parametrize("B,k,E", SORTS)
@@ -106,7 +107,7 @@ WIDTHS = [8, 16, 24, 768, 1032, 2048, 4096, 4104, 8192, 28672]
 
 @pytest.mark.parametrize("width", WIDTHS)
 @pytest.mark.parametrize("B,k,E,kind", [(1, 8, 128, "uniform"), (5, 3, 4, "dropped"), (33, 8, 16, "dropped"),
-                                        (700, 2, 60, "uniform")])
+                                        (700, 2, 60, "uniform"), (500, 8, 128, "dropped"), (600, 8, 128, "uniform")])
 def test_dispatch_rows(ops, width, B, k, E, kind):
     announce(f"moe_dispatch rows width={width} B={B} k={k} E={E} {kind}")
     rng = np.random.default_rng(width + B)

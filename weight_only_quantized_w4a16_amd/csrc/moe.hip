@@ -312,13 +312,20 @@ void launch_moe_gather(const void* rows, const float* scale, const int* row_of_s
 // is the number of slots before it in (expert, slot) order, so each token's
 // workgroups count that over all T ids for their k slots (a ballot per 64 ids and
 // slot) while the token's row is on its way from memory; one more workgroup
-// writes the offsets.  The work grows with T per token, so this serves up to
-// DIRECT_MAX_T slots.
+// writes the offsets.  The work grows with the workgroups times T: DIRECT_MAX_WORK
+// bounds it (top-8 of 128, e4m3 rows of 2048, this / the two-launch sort and the
+// copy, us: 256 tokens 7.4 / 10.1, 512 11.1 / 11.1, 768 15.2 / 12.6; top-2 of 8, rows
+// of 4096: 1024 8.5 / 10.7, 2048 20.0 / 13.8).
 // ---------------------------------------------------------------------------
-#ifndef QG_MOE_DIRECT_MAX_T
-#define QG_MOE_DIRECT_MAX_T 4096
+#ifndef QG_MOE_DIRECT_MAX_WORK
+#define QG_MOE_DIRECT_MAX_WORK (1 << 21)
 #endif
-constexpr int DIRECT_MAX_T = QG_MOE_DIRECT_MAX_T;
+
+// work of `parts` workgroups per token
+static int64_t direct_work(int B, int k, int parts) {
+    return (int64_t)B * parts * ((k + SLOTS - 1) / SLOTS) * B * k;
+}
+static bool direct_sort(int B, int k) { return direct_work(B, k, 1) <= QG_MOE_DIRECT_MAX_WORK; }
 
 template <class V>
 __global__ __launch_bounds__(256) void moe_dispatch_direct_kernel(const int* __restrict__ ids, const V* __restrict__ rows,
@@ -351,7 +358,7 @@ __global__ __launch_bounds__(256) void moe_dispatch_direct_kernel(const int* __r
     if (c < chunks) v = rows[(size_t)b * chunks + c];
     const float s = scale && c == 0 ? scale[b] : 0.0f;
     for (int j0 = 0; j0 < k; j0 += SLOTS) {
-        // (expert, slot) as one number: E T <= 2^10 DIRECT_MAX_T fits 32 bits
+        // (expert, slot) as one number: T <= DIRECT_MAX_WORK and E <= 2^10 fit 32 bits
         unsigned key[SLOTS];
         int n[SLOTS];
 #pragma unroll
@@ -390,8 +397,8 @@ __global__ __launch_bounds__(256) void moe_dispatch_direct_kernel(const int* __r
 }
 
 size_t moe_dispatch_workspace_bytes(int B, int k, int E) {
+    if (B == 0 || direct_sort(B, k)) return 0;
     const int T = B * k;
-    if (T <= DIRECT_MAX_T) return 0;
     const int seg = sort_seg(T);
     return (size_t)((T + seg - 1) / seg) * E * sizeof(int);
 }
@@ -402,17 +409,25 @@ void launch_moe_dispatch(const int* ids, const void* rows, const float* scale, i
         hipLaunchKernelGGL(moe_no_rows_kernel, dim3(1), dim3(256), 0, st, E, offsets);
         return;
     }
-    if (B * k <= DIRECT_MAX_T) {
-        auto go = [&](auto* piece) {
+    if (direct_sort(B, k)) {
+        auto go = [&](auto* piece, const void* in, int chunks, int parts) {
             using V = std::remove_pointer_t<decltype(piece)>;
-            const int chunks = rows ? row_bytes / (int)sizeof(V) : 0;
-            const int parts = std::max(1, (chunks + 255) / 256);
             hipLaunchKernelGGL(moe_dispatch_direct_kernel<V>, dim3((unsigned)(B * parts + 1)), dim3(256), 0, st, ids,
-                               static_cast<const V*>(rows), scale, B, k, E, chunks, parts, offsets, row_of_slot,
-                               static_cast<V*>(out), scale_out);
+                               static_cast<const V*>(in), in ? scale : nullptr, B, k, E, chunks, parts, offsets,
+                               row_of_slot, static_cast<V*>(out), scale_out);
         };
-        if (row_bytes % 16 == 0) go((u32x4*)nullptr);
-        else go((uint2*)nullptr);
+        const int piece = row_bytes % 16 == 0 ? 16 : 8;
+        const int chunks = rows ? row_bytes / piece : 0;
+        const int parts = std::max(1, (chunks + 255) / 256);
+        // every part of a long row would count again: sort first, then copy
+        if (parts > 1 && direct_work(B, k, parts) > QG_MOE_DIRECT_MAX_WORK) {
+            go((u32x4*)nullptr, nullptr, 0, 1);
+            launch_moe_gather(rows, scale, row_of_slot, B, k, row_bytes, out, scale_out, st);
+        } else if (piece == 16) {
+            go((u32x4*)nullptr, rows, chunks, parts);
+        } else {
+            go((uint2*)nullptr, rows, chunks, parts);
+        }
         return;
     }
     launch_sort(ids, B * k, E, offsets, row_of_slot, ws, st);
