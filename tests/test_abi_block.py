@@ -95,11 +95,11 @@ def test_moe_shapes(ops):
 
 def test_moe_pointers(ops):
     for p in ("ids", "offsets", "row", "ws"):
-        assert call(ops, "moe_dispatch", DISPATCH, B=4096, **{p: None}) == QG_ERR_NULL, p
+        assert call(ops, "moe_dispatch", DISPATCH, B=65536, **{p: None}) == QG_ERR_NULL, p
     # rows and their destination come together, and so do scales; scales need rows
     for changed in (dict(rows=None), dict(out=None), dict(rs=None), dict(so=None), dict(rows=None, out=None)):
         assert call(ops, "moe_dispatch", DISPATCH, **changed) == QG_ERR_NULL, changed
-    assert call(ops, "moe_dispatch", DISPATCH, B=4096, wsb=3) == QG_ERR_WORKSPACE
+    assert call(ops, "moe_dispatch", DISPATCH, B=65536, wsb=3) == QG_ERR_WORKSPACE
     assert call(ops, "moe_dispatch", DISPATCH, B=0, offsets=None) == QG_ERR_NULL
     for p in ("rows", "row", "out", "rs", "so"):
         assert call(ops, "moe_gather", GATHER, **{p: None}) == QG_ERR_NULL, p
@@ -113,7 +113,7 @@ def test_moe_pointers(ops):
         for p, v in base.items():
             if v == FAKE and not (name == "moe_dispatch" and p == "ws"):
                 assert call(ops, name, base, **{p: FAKE + 2}) == QG_ERR_ALIGN, (name, p)
-    assert call(ops, "moe_dispatch", DISPATCH, B=4096, ws=FAKE + 2) == QG_ERR_ALIGN
+    assert call(ops, "moe_dispatch", DISPATCH, B=65536, ws=FAKE + 2) == QG_ERR_ALIGN
     for name, base in (("moe_gather", GATHER), ("moe_combine", COMBINE), ("moe_combine_backward", BACKWARD)):
         assert call(ops, name, base, B=0, row=None) == QG_OK
 

@@ -27,19 +27,18 @@ namespace qg {
 // slots (one workgroup, `seg` slots) counts its experts into hist[i][e]; then
 // every segment derives the first row of each expert (totals over all segments)
 // and of its own share (totals over the segments before it), and numbers its
-// slots in order.  Few large segments: the work is latency, not bandwidth.  Up to
-// SORT_MAX_SEGS segments hold SORT_NT * SORT_REG slots, which the threads keep in
-// registers (REG); beyond, segments grow and are read twice.
+// slots in order.  The work is latency, not bandwidth: up to SORT_MAX_SEGS segments
+// hold one slot per thread (REG), beyond that they grow and are read twice
+// (measured, one / two / four slots per thread, 128 experts, us: 8192 slots 6.3 /
+// 7.1 / 8.2, 65536 6.9 / 8.2 / 9.1, 262144 9.3 / 8.6 / 9.3).
 // ---------------------------------------------------------------------------
 constexpr int SORT_WAVES = 16;
 constexpr int SORT_NT = SORT_WAVES * 64;
-constexpr int SORT_REG = 4;
-constexpr int SORT_MIN_SEG = SORT_REG * SORT_NT;
 constexpr int SORT_MAX_SEGS = 256;
 
 // slots per segment, a multiple of SORT_NT
 static int sort_seg(int T) {
-    const int seg = std::max(SORT_MIN_SEG, (T + SORT_MAX_SEGS - 1) / SORT_MAX_SEGS);
+    const int seg = (T + SORT_MAX_SEGS - 1) / SORT_MAX_SEGS;
     return (seg + SORT_NT - 1) / SORT_NT * SORT_NT;
 }
 
@@ -50,13 +49,9 @@ __global__ __launch_bounds__(SORT_NT) void moe_count_kernel(const int* __restric
     __syncthreads();
     const int s0 = blockIdx.x * seg;
     const int s1 = min(s0 + seg, T);
-    for (int s = s0 + (int)threadIdx.x; s < s1; s += SORT_REG * SORT_NT) {
-        int e[SORT_REG];
-#pragma unroll
-        for (int i = 0; i < SORT_REG; ++i) e[i] = s + i * SORT_NT < s1 ? ids[s + i * SORT_NT] : -1;
-#pragma unroll
-        for (int i = 0; i < SORT_REG; ++i)
-            if (e[i] >= 0 && e[i] < E) atomicAdd(&count[e[i]], 1);
+    for (int s = s0 + (int)threadIdx.x; s < s1; s += SORT_NT) {
+        const int e = ids[s];
+        if (e >= 0 && e < E) atomicAdd(&count[e], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += SORT_NT) hist[(size_t)blockIdx.x * E + e] = count[e];
@@ -126,11 +121,7 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
     const int per = seg / SORT_WAVES;
     const int s0 = mine * seg + wave * per;
     const int s1 = min(s0 + per, T);
-    int held[SORT_REG];
-    if constexpr (REG) {
-#pragma unroll
-        for (int i = 0; i < SORT_REG; ++i) held[i] = s0 + i * 64 + lane < s1 ? ids[s0 + i * 64 + lane] : -1;
-    }
+    const int held = REG && s0 + lane < s1 ? ids[s0 + lane] : -1;
 
     // totals over the segments: SORT_NT / 2^bits threads share an expert's column
     // (up to 2^10 experts: one thread each at least)
@@ -159,8 +150,7 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
         if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
     };
     if constexpr (REG) {
-#pragma unroll
-        for (int i = 0; i < SORT_REG; ++i) count(held[i]);
+        count(held);
     } else {
         for (int s = s0 + lane; s < s1; s += 64) count(ids[s]);
     }
@@ -192,10 +182,9 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
         if (s + lane < s1) row_of_slot[s + lane] = row;
     };
     if constexpr (REG) {
-#pragma unroll
-        for (int i = 0; i < SORT_REG; ++i) number(s0 + i * 64, held[i]);
+        number(s0, held);
     } else {
-        for (int s = s0; s < s1; s += 64) number(s, s + lane < s1 ? ids[s + lane] : -1);   // uniform bounds
+        for (int s = s0; s < s1; s += 64) number(s, s + lane < s1 ? ids[s + lane] : -1);   // uniform in the wave
     }
 }
 
@@ -206,21 +195,21 @@ static int bits_of(int E) {
 }
 
 static void launch_sort(const int* ids, int T, int E, int* offsets, int* row_of_slot, void* ws, hipStream_t st) {
-    const int seg = sort_seg(T);
-    const int nseg = (T + seg - 1) / seg;
     int* hist = static_cast<int*>(ws);
-    hipLaunchKernelGGL(moe_count_kernel, dim3(nseg), dim3(SORT_NT), E * sizeof(int), st, ids, T, E, seg, hist);
     const int bytes = place_words(E) * (int)sizeof(int);
+    const int seg = sort_seg(T);
     auto place = [&](auto reg) {
         constexpr bool REG = decltype(reg)::value;
         static std::atomic<uint64_t> lds_set{0};
         if (bytes > 60 * 1024)                   // with the static words, over the default limit of 64 KiB
             allow_dynamic_lds(reinterpret_cast<const void*>(&moe_place_kernel<REG>),
                               place_words(kGroupedMaxExperts) * (int)sizeof(int), lds_set);
-        hipLaunchKernelGGL(moe_place_kernel<REG>, dim3(nseg), dim3(SORT_NT), bytes, st, ids, T, E, bits_of(E), seg, hist,
-                           offsets, row_of_slot);
+        hipLaunchKernelGGL(moe_place_kernel<REG>, dim3((T + seg - 1) / seg), dim3(SORT_NT), bytes, st, ids, T, E,
+                           bits_of(E), seg, hist, offsets, row_of_slot);
     };
-    if (seg == SORT_MIN_SEG) place(std::true_type{});
+    hipLaunchKernelGGL(moe_count_kernel, dim3((T + seg - 1) / seg), dim3(SORT_NT), E * sizeof(int), st, ids, T, E, seg,
+                       hist);
+    if (seg == SORT_NT) place(std::true_type{});
     else place(std::false_type{});
 }
 
@@ -314,11 +303,11 @@ void launch_moe_gather(const void* rows, const float* scale, const int* row_of_s
 // slot) while the token's row is on its way from memory; one more workgroup
 // writes the offsets.  The work grows with the workgroups times T: DIRECT_MAX_WORK
 // bounds it (top-8 of 128, e4m3 rows of 2048, this / the two-launch sort and the
-// copy, us: 256 tokens 7.4 / 10.1, 512 11.1 / 11.1, 768 15.2 / 12.6; top-2 of 8, rows
-// of 4096: 1024 8.5 / 10.7, 2048 20.0 / 13.8).
+// copy, us: 128 tokens 5.8 / 8.0, 256 7.4 / 8.6, 512 11.1 / 9.6; top-2 of 8, rows of
+// 4096: 512 5.0 / 7.9, 1024 8.5 / 9.4).
 // ---------------------------------------------------------------------------
 #ifndef QG_MOE_DIRECT_MAX_WORK
-#define QG_MOE_DIRECT_MAX_WORK (1 << 21)
+#define QG_MOE_DIRECT_MAX_WORK (1 << 20)
 #endif
 
 // work of `parts` workgroups per token

@@ -36,10 +36,11 @@ __device__ __forceinline__ uint32_t encode4(const float* q) {
         int c = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
         return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], c, true);
     } else {
-        uint32_t c = 0;
+        // q + 1.5 2^23 has the half-even rounding of q in its lowest byte
+        uint32_t c[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c |= ((uint32_t)(int)rintf(q[j]) & 0xffu) << (8 * j);
-        return c;
+        for (int j = 0; j < 4; ++j) c[j] = __float_as_uint(q[j] + 12582912.0f);
+        return __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u) | __builtin_amdgcn_perm(c[3], c[2], 0x04000c0cu);
     }
 }
 
