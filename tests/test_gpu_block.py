@@ -225,3 +225,31 @@ def test_stream_argument(ops):
     st.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_memory_of_an_explicit_stream(ops):
+    """A helper's workspace, freed when the helper returns, is not handed to the
+    current stream while the given stream still has to use it."""
+    announce("workspace of an explicit stream")
+    B, k, n_exp = 4096, 8, 64
+    rng = np.random.default_rng(3)
+    ids_h = rng.integers(0, n_exp, (B, k)).astype(np.int32)
+    ids = torch.from_numpy(ids_h).cuda()
+    need = ops.moe_dispatch_workspace_bytes(B, k, n_exp)
+    assert need > 0
+    a = torch.randn((4096, 4096), device="cuda:0")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(8):                                    # a few milliseconds ahead of the dispatch
+            a = torch.sin(a @ a)
+    r, _, _ = ops.MoeRouting.dispatch(ids, n_exp, stream=st)
+    spoil = [torch.full((need,), 0x7F, dtype=torch.uint8, device="cuda:0") for _ in range(64)]
+    torch.cuda.synchronize()
+    off, row = r.offsets.cpu().numpy(), r.row_of_slot.cpu().numpy()
+    del spoil
+    order = np.argsort(ids_h.reshape(-1), kind="stable")
+    want = np.empty(B * k, np.int32)
+    want[order] = np.arange(B * k)
+    assert np.array_equal(row.reshape(-1), want)
+    assert np.array_equal(off, np.searchsorted(np.sort(ids_h.reshape(-1)), np.arange(n_exp + 1)))

@@ -670,6 +670,14 @@ def _is(t, dtypes, shape, what):
 
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _on(stream, t):
+    """Context in which `stream` is the current stream (None: no change): what a helper
+    allocates then belongs to the stream that writes it, and may be freed while it runs."""
+    if stream is not None and stream.device_index != t.get_device():
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)
 _CODES = {"e4m3": torch.uint8, "int8": torch.int8}
 
 
@@ -697,18 +705,20 @@ class RMSNorm:
 
     def __call__(self, x, residual=None, stream=None):
         """(y, h): the bf16 norm and the new residual stream (x itself without a residual)."""
-        M, K, h = self._inputs(x, residual)
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
-        rms_norm(x, residual, self.weight, self.eps, M, K, h, y, stream)
+        with _on(stream, x):
+            M, K, h = self._inputs(x, residual)
+            y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+            rms_norm(x, residual, self.weight, self.eps, M, K, h, y)
         return y, x if h is None else h
 
     def quantized(self, x, residual=None, fmt="e4m3", with_bf16=False, stream=None):
         """(q, s, h): per-token codes and scales of the norm; with_bf16: (q, s, h, y)."""
-        M, K, h = self._inputs(x, residual)
-        q, s = _codes(M, K, fmt, x.device)
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if with_bf16 else None
-        call = rms_norm_quant if fmt == "e4m3" else rms_norm_quant_int8
-        call(x, residual, self.weight, self.eps, M, K, h, y, q, s, stream)
+        with _on(stream, x):
+            M, K, h = self._inputs(x, residual)
+            q, s = _codes(M, K, fmt, x.device)
+            y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if with_bf16 else None
+            call = rms_norm_quant if fmt == "e4m3" else rms_norm_quant_int8
+            call(x, residual, self.weight, self.eps, M, K, h, y, q, s)
         out = (q, s, x if h is None else h)
         return out + (y,) if with_bf16 else out
 
@@ -719,8 +729,9 @@ def gated_silu(gate_up, stream=None):
     if n % 2:
         raise ValueError("gate_up: the gate and up halves need an even number of columns")
     _is(gate_up, _BF16, (M, n), "gate_up")
-    y = torch.empty((M, n // 2), dtype=torch.bfloat16, device=gate_up.device)
-    swiglu(gate_up, M, n // 2, y, stream)
+    with _on(stream, gate_up):
+        y = torch.empty((M, n // 2), dtype=torch.bfloat16, device=gate_up.device)
+        swiglu(gate_up, M, n // 2, y)
     return y
 
 
@@ -730,8 +741,9 @@ def gated_silu_quantized(gate_up, fmt="e4m3", stream=None):
     if n % 2:
         raise ValueError("gate_up: the gate and up halves need an even number of columns")
     _is(gate_up, _BF16, (M, n), "gate_up")
-    q, s = _codes(M, n // 2, fmt, gate_up.device)
-    (swiglu_quant if fmt == "e4m3" else swiglu_quant_int8)(gate_up, M, n // 2, q, s, stream)
+    with _on(stream, gate_up):
+        q, s = _codes(M, n // 2, fmt, gate_up.device)
+        (swiglu_quant if fmt == "e4m3" else swiglu_quant_int8)(gate_up, M, n // 2, q, s)
     return q, s
 
 
@@ -750,13 +762,16 @@ class MoeRouting:
         Rows from offsets[E] on belong to no expert and are not written."""
         B, k = expert_ids.shape
         _is(expert_ids, (torch.int32,), (B, k), "expert_ids")
+        if E < 1:
+            raise ValueError(f"E must be positive, got {E}")
         dev = expert_ids.device
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        row = torch.empty((B, k), dtype=torch.int32, device=dev)
-        out, scale_out, width = cls._rows_out(rows, row_scale, B, k)
-        need = moe_dispatch_workspace_bytes(B, k, E)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        moe_dispatch(expert_ids, rows, row_scale, B, k, E, width, offsets, row, out, scale_out, ws, need, stream)
+        with _on(stream, expert_ids):
+            offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+            row = torch.empty((B, k), dtype=torch.int32, device=dev)
+            out, scale_out, width = cls._rows_out(rows, row_scale, B, k)
+            need = moe_dispatch_workspace_bytes(B, k, E)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+            moe_dispatch(expert_ids, rows, row_scale, B, k, E, width, offsets, row, out, scale_out, ws, need)
         return cls(offsets, row), out, scale_out
 
     @staticmethod
@@ -776,8 +791,9 @@ class MoeRouting:
 
     def gather(self, rows, row_scale=None, stream=None):
         """(rows [B k, K], scales or None): another tensor's rows in the routed order."""
-        out, scale_out, width = self._rows_out(rows, row_scale, self.B, self.k)
-        moe_gather(rows, row_scale, self.row_of_slot, self.B, self.k, width, out, scale_out, stream)
+        with _on(stream, rows):
+            out, scale_out, width = self._rows_out(rows, row_scale, self.B, self.k)
+            moe_gather(rows, row_scale, self.row_of_slot, self.B, self.k, width, out, scale_out)
         return out, scale_out
 
     def _weights(self, weights):
@@ -790,9 +806,10 @@ class MoeRouting:
         _is(rows, _BF16, (self.B * self.k, K), "rows")
         if residual is not None:
             _is(residual, _BF16, (self.B, K), "residual")
-        y = _is(out, _BF16, (self.B, K), "out") if out is not None else \
-            torch.empty((self.B, K), dtype=torch.bfloat16, device=rows.device)
-        moe_combine(rows, self.row_of_slot, self._weights(weights), residual, self.B, self.k, K, y, stream)
+        with _on(stream, rows):
+            y = _is(out, _BF16, (self.B, K), "out") if out is not None else \
+                torch.empty((self.B, K), dtype=torch.bfloat16, device=rows.device)
+            moe_combine(rows, self.row_of_slot, self._weights(weights), residual, self.B, self.k, K, y)
         return y
 
     def combine_backward(self, dy, rows, weights=None, stream=None):
@@ -800,7 +817,8 @@ class MoeRouting:
         K = dy.shape[1]
         _is(dy, _BF16, (self.B, K), "dy")
         _is(rows, _BF16, (self.B * self.k, K), "rows")
-        drows = torch.empty((self.B * self.k, K), dtype=torch.bfloat16, device=dy.device)
-        dw = torch.empty((self.B, self.k), dtype=torch.float32, device=dy.device)
-        moe_combine_backward(dy, rows, self.row_of_slot, self._weights(weights), self.B, self.k, K, drows, dw, stream)
+        with _on(stream, dy):
+            drows = torch.empty((self.B * self.k, K), dtype=torch.bfloat16, device=dy.device)
+            dw = torch.empty((self.B, self.k), dtype=torch.float32, device=dy.device)
+            moe_combine_backward(dy, rows, self.row_of_slot, self._weights(weights), self.B, self.k, K, drows, dw)
         return drows, dw
