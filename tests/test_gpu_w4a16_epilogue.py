@@ -158,3 +158,56 @@ def test_refusals(ops):
         ops.W4A16Linear(wt)(a, residual=torch.zeros((3, 512), dtype=torch.bfloat16, device="cuda:0"))
     with pytest.raises(ops.QGemmError):
         ops.qgemm_w4a16_epilogue(a, wt.packed, wt.scales, None, 5, None, torch.empty_like(a), 4, 512, 512)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_bias_at_any_word(ops, M, N, K):
+    """A bias that starts at any 4-byte word gives the bits of an aligned one; at a
+    half word it is refused."""
+    announce(f"bias alignment M={M} N={N} K={K}")
+    wt, _ = weight(ops, K, N)
+    a = dev_bf16(synth.activations(M, K, seed=1))
+    room = torch.zeros(N + 16, dtype=torch.bfloat16, device="cuda:0")
+    bias = dev_bf16(synth.normal_bf16((N,), 2))
+    want = ops.W4A16Linear(wt, bias, "silu")(a)
+    for off in (2, 6):
+        part = room[off:off + N]
+        part.copy_(bias)
+        got = ops.W4A16Linear(wt, part, "silu")(a)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), off
+    with pytest.raises(ops.QGemmError):
+        ops.W4A16Linear(wt, room[1:1 + N], "silu")(a)
+
+
+@pytest.mark.parametrize("M,N,K", [s for s in SHAPES if s in ((16, 1024, 14336), (12, 272, 16384), (100, 4096, 4096),
+                                                              (130, 8192, 8192))])
+def test_split_slots_are_written_before_they_are_read(ops, M, N, K):
+    """K splits: the partial sums' memory holds NaN before every call, the inputs
+    alternate, and one workspace serves the plain product and the epilogue in turn."""
+    announce(f"epilogue on a spoilt workspace M={M} N={N} K={K}")
+    assert not ops.w4a16_kernel_for(M, N, K).endswith("S=1")
+    wt, _ = weight(ops, K, N)
+    bias, res = dev_bf16(synth.normal_bf16((N,), 2)), dev_bf16(synth.normal_bf16((M, N), 3))
+    ins = [dev_bf16(synth.activations(M, K, seed=s)) for s in (1, 2)]
+    lin = ops.W4A16Linear(wt)
+    ws, need = lin.workspace(M)
+    want = {}
+    for turn in range(6):
+        i = turn % 2
+        ws[64 * 1024:].fill_(0xFF)
+        y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda:0")
+        ops.qgemm_w4a16_epilogue(ins[i], wt.packed, wt.scales, bias, "gelu", res, y, M, N, K, ws, need)
+        p = lin(ins[i])
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(y).all()) and not bool(ws[:64 * 1024].any())
+        if i in want:
+            assert torch.equal(y, want[i][0]) and torch.equal(p, want[i][1])
+        want[i] = (y, p)
+
+
+def test_no_rows(ops):
+    announce("epilogue M=0")
+    wt, _ = weight(ops, 512, 512)
+    empty = torch.empty((0, 512), dtype=torch.bfloat16, device="cuda:0")
+    assert ops.W4A16Linear(wt, activation="relu")(empty, residual=empty).shape == (0, 512)

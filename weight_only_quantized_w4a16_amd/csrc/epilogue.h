@@ -3,9 +3,9 @@
 // kernel fetches the bias and residual of the results that a thread stores
 // together (an In) while other work is under way, and applies them before the
 // first store: y may be the residual's memory, so the compiler may not move a
-// load over such a store.  Measured at 1000 x 4096 x 14336 with a bias: 130 us
-// with the loads between the stores of each 32 x 32 block, against 118 us for
-// the plain product.
+// load over such a store.  Loaded bits stay as they are until then: a conversion
+// next to the load would wait for it (1 x 4096 x 28672 with a bias 14.4 us so, 13.9
+// otherwise, 13.0 for the plain product).
 #pragma once
 
 #include "device_common.h"

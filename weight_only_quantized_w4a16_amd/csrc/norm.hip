@@ -11,7 +11,10 @@
 // fp64): y is rounded once, to bf16 or to its code, and h (stored as bf16)
 // enters the norm unrounded.
 // Both are bound by memory: a row is read once and stays in registers between
-// the reductions and the encoding.
+// the reductions and the encoding.  Graph-timed: norm with residual at 8191 x 8192
+// to bf16 / e4m3 79 / 73 us (6.8 / 6.4 TB/s), at 1 x 4096 2.6 / 2.9 us; swiglu at 8192
+// x 14336 103 / 94 us (6.9 / 6.3 TB/s), at 16 x 14336 2.3 / 3.9 us (an empty launch
+// takes about 2).
 
 #include <algorithm>
 
