@@ -1,24 +1,30 @@
-"""Build libqgemm.so in-tree with hipcc for gfx950.
+"""Build libqgemm.so in-tree with hipcc for gfx950, and _calls.so, the binding's
+call marshalling (host code against the installed torch's headers).
 
     python -m weight_only_quantized_w4a16_amd.build
 
 Every call compiles from source (no staleness check): the object files go to
-csrc/_build/, the library to the package directory.
+csrc/_build/, the libraries to the package directory.
 """
 import concurrent.futures
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(CSRC, "_build")
 LIB = os.path.join(PKG, "libqgemm.so")
+CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["abi.cpp", "abi_block.cpp", "w4a16.hip", "fp8.hip", "w4a8.hip", "norm.hip", "moe.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
+ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
@@ -41,10 +47,27 @@ def _compile(src):
     return obj, warn
 
 
+def _build_calls():
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    lib = os.path.join(torch, "lib")
+    tmp = CALLS + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-I", os.path.join(torch, "include"), "-I", os.path.join(ROCM, "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "calls.cpp"),
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+           "-L", os.path.join(ROCM, "lib"), "-lamdhip64", "-Wl,-rpath," + lib, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for calls.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose=True):
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        calls = ex.submit(_build_calls)
         results = list(ex.map(_compile, SOURCES))
+        calls.result()
     objs = [o for o, _ in results]
     if verbose:
         for (_, w), src in zip(results, SOURCES):
@@ -58,6 +81,7 @@ def build(verbose=True):
     os.replace(tmp, LIB)
     if verbose:
         print(f"built {LIB}")
+        print(f"built {CALLS}")
     return LIB
 
 

@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the computation runs in the HIP
 library.  Functions take torch tensors on the GPU, pass their device pointers
 and torch's current HIP stream, and raise QGemmError on a non-zero status.
-There is no fallback: if libqgemm.so is missing, importing this module raises.
+There is no fallback: if libqgemm.so or _calls.so (the compiled marshalling of
+the block operators' calls) is missing, importing this module raises.
 
 bf16 data travels as torch.bfloat16 (or int16 / uint16 bit patterns) tensors;
 e4m3 codes as torch.uint8 (or torch.float8_e4m3fn) tensors.
@@ -16,12 +17,15 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqgemm.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(
-        f"{LIB_PATH} is not built; run `python -m weight_only_quantized_w4a16_amd.build` "
-        "(hipcc, gfx950)")
+for _path in (LIB_PATH, os.path.join(_PKG, "_calls.so")):
+    if not os.path.exists(_path):
+        raise ImportError(
+            f"{_path} is not built; run `python -m weight_only_quantized_w4a16_amd.build` "
+            "(hipcc, gfx950)")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _calls  # noqa: E402  (call marshalling of the block operators; built beside the library)
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -80,6 +84,11 @@ for _name, (_res, _args) in _SIGS.items():
     _f.argtypes = _args
 
 EXPORTED = tuple(_SIGS)
+
+# the compiled marshalling calls the functions of the library loaded above
+for _name in dir(_calls):
+    if _name in _SIGS:
+        _calls.bind(_name, ctypes.cast(getattr(_lib, _name), ctypes.c_void_p).value)
 
 
 class QGemmError(RuntimeError):
@@ -269,82 +278,32 @@ def qgemm_w4a8_fp8_grouped_dynamic(a_bf16, offsets_i32, packed, scales, y_bf16, 
 
 # ---- the operators between two products: raw entry points ----------------------
 # They launch on the device their tensors are on, on that device's current
-# stream unless one is given.
-
-def _ptrs(*tensors):
-    """Device addresses (None stays None) and the one device the tensors are on."""
-    dev = -2                                     # none yet; host tensors say -1
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        d = t.get_device()
-        if d != dev:
-            if d < 0:
-                raise ValueError("tensor must be on the GPU")
-            if dev >= 0:
-                raise ValueError("tensors must be on one device")
-            dev = d
-        if not t.is_contiguous():
-            raise ValueError("tensor must be contiguous")
-        out.append(t.data_ptr())
-    if dev < 0:
-        raise ValueError("no tensor was given")
-    return out, dev
-
-
-# The current stream's handle and the current device without the Python objects
-# around them (1.2 and 0.1 us of a 6 us call), where this torch has these calls.
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
-def _launch(fn, dev, stream, *args):
-    if stream is None:
-        raw = _current_stream(dev)
-    elif stream.device_index != dev:
-        raise ValueError("the stream belongs to another device than the tensors")
-    else:
-        raw = stream.cuda_stream
-    if dev == _current_device():
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status != 0:
-        raise QGemmError(fn.__name__, status)
-
+# stream unless one is given.  The marshalling is compiled (_calls).
 
 def rms_norm(x_bf16, residual_bf16, weight_bf16, eps, M, K, h_bf16, y_bf16, stream=None):
-    (x, r, w, h, y), dev = _ptrs(x_bf16, residual_bf16, weight_bf16, h_bf16, y_bf16)
-    _launch(_lib.rms_norm, dev, stream, x, r, w, eps, M, K, h, y)
+    _check("rms_norm", _calls.rms_norm(x_bf16, residual_bf16, weight_bf16, eps, M, K, h_bf16, y_bf16, stream))
 
 
 def rms_norm_quant(x_bf16, residual_bf16, weight_bf16, eps, M, K, h_bf16, y_bf16, y_e4m3, y_scale, stream=None):
-    (x, r, w, h, y, q, s), dev = _ptrs(x_bf16, residual_bf16, weight_bf16, h_bf16, y_bf16, y_e4m3, y_scale)
-    _launch(_lib.rms_norm_quant, dev, stream, x, r, w, eps, M, K, h, y, q, s)
+    _check("rms_norm_quant", _calls.rms_norm_quant(x_bf16, residual_bf16, weight_bf16, eps, M, K, h_bf16, y_bf16, y_e4m3,
+                                                   y_scale, stream))
 
 
 def rms_norm_quant_int8(x_bf16, residual_bf16, weight_bf16, eps, M, K, h_bf16, y_bf16, y_i8, y_scale, stream=None):
-    (x, r, w, h, y, q, s), dev = _ptrs(x_bf16, residual_bf16, weight_bf16, h_bf16, y_bf16, y_i8, y_scale)
-    _launch(_lib.rms_norm_quant_int8, dev, stream, x, r, w, eps, M, K, h, y, q, s)
+    _check("rms_norm_quant_int8", _calls.rms_norm_quant_int8(x_bf16, residual_bf16, weight_bf16, eps, M, K, h_bf16, y_bf16,
+                                                             y_i8, y_scale, stream))
 
 
 def swiglu(gate_up_bf16, M, I, y_bf16, stream=None):
-    (g, y), dev = _ptrs(gate_up_bf16, y_bf16)
-    _launch(_lib.swiglu, dev, stream, g, M, I, y)
+    _check("swiglu", _calls.swiglu(gate_up_bf16, M, I, y_bf16, stream))
 
 
 def swiglu_quant(gate_up_bf16, M, I, y_e4m3, y_scale, stream=None):
-    (g, q, s), dev = _ptrs(gate_up_bf16, y_e4m3, y_scale)
-    _launch(_lib.swiglu_quant, dev, stream, g, M, I, q, s)
+    _check("swiglu_quant", _calls.swiglu_quant(gate_up_bf16, M, I, y_e4m3, y_scale, stream))
 
 
 def swiglu_quant_int8(gate_up_bf16, M, I, y_i8, y_scale, stream=None):
-    (g, q, s), dev = _ptrs(gate_up_bf16, y_i8, y_scale)
-    _launch(_lib.swiglu_quant_int8, dev, stream, g, M, I, q, s)
+    _check("swiglu_quant_int8", _calls.swiglu_quant_int8(gate_up_bf16, M, I, y_i8, y_scale, stream))
 
 
 # qg_activation of include/qgemm.h
@@ -354,12 +313,11 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 def qgemm_w4a16_epilogue(a_bf16, packed, scales, bias_bf16, activation, residual_bf16, y_bf16, M, N, K, workspace=None,
                          workspace_bytes=0, stream=None):
     """activation: a name of ACTIVATIONS or its qg_activation code."""
-    (a, w, sc, b, r, y, ws), dev = _ptrs(a_bf16, packed, scales, bias_bf16, residual_bf16, y_bf16, workspace)
-    if not isinstance(activation, int):
-        if activation not in ACTIVATIONS:
-            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
-        activation = ACTIVATIONS[activation]
-    _launch(_lib.qgemm_w4a16_epilogue, dev, stream, a, w, sc, b, activation, r, y, M, N, K, ws, workspace_bytes)
+    code = ACTIVATIONS.get(activation, activation)
+    if not isinstance(code, int):
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    _check("qgemm_w4a16_epilogue", _calls.qgemm_w4a16_epilogue(a_bf16, packed, scales, bias_bf16, code, residual_bf16, y_bf16,
+                                                               M, N, K, workspace, workspace_bytes, stream))
 
 
 def moe_dispatch_workspace_bytes(B, k, E):
@@ -368,24 +326,21 @@ def moe_dispatch_workspace_bytes(B, k, E):
 
 def moe_dispatch(expert_ids, rows, row_scale, B, k, E, row_bytes, offsets, row_of_slot, rows_out, row_scale_out,
                  workspace=None, workspace_bytes=0, stream=None):
-    (i, r, s, o, ros, ro, so, ws), dev = _ptrs(expert_ids, rows, row_scale, offsets, row_of_slot, rows_out, row_scale_out,
-                                               workspace)
-    _launch(_lib.moe_dispatch, dev, stream, i, r, s, B, k, E, row_bytes, o, ros, ro, so, ws, workspace_bytes)
+    _check("moe_dispatch", _calls.moe_dispatch(expert_ids, rows, row_scale, B, k, E, row_bytes, offsets, row_of_slot, rows_out,
+                                               row_scale_out, workspace, workspace_bytes, stream))
 
 
 def moe_gather(rows, row_scale, row_of_slot, B, k, row_bytes, rows_out, row_scale_out, stream=None):
-    (r, s, ros, ro, so), dev = _ptrs(rows, row_scale, row_of_slot, rows_out, row_scale_out)
-    _launch(_lib.moe_gather, dev, stream, r, s, ros, B, k, row_bytes, ro, so)
+    _check("moe_gather", _calls.moe_gather(rows, row_scale, row_of_slot, B, k, row_bytes, rows_out, row_scale_out, stream))
 
 
 def moe_combine(rows_bf16, row_of_slot, weights, residual_bf16, B, k, K, y_bf16, stream=None):
-    (r, ros, w, res, y), dev = _ptrs(rows_bf16, row_of_slot, weights, residual_bf16, y_bf16)
-    _launch(_lib.moe_combine, dev, stream, r, ros, w, res, B, k, K, y)
+    _check("moe_combine", _calls.moe_combine(rows_bf16, row_of_slot, weights, residual_bf16, B, k, K, y_bf16, stream))
 
 
 def moe_combine_backward(dy_bf16, rows_bf16, row_of_slot, weights, B, k, K, drows_bf16, dweights, stream=None):
-    (d, r, ros, w, dr, dw), dev = _ptrs(dy_bf16, rows_bf16, row_of_slot, weights, drows_bf16, dweights)
-    _launch(_lib.moe_combine_backward, dev, stream, d, r, ros, w, B, k, K, dr, dw)
+    _check("moe_combine_backward", _calls.moe_combine_backward(dy_bf16, rows_bf16, row_of_slot, weights, B, k, K, drows_bf16,
+                                                               dweights, stream))
 
 
 # ---- tensor-level helpers (allocate outputs with torch, then call the above) --
