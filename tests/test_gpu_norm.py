@@ -100,9 +100,9 @@ def assert_codes(q, s, ref, fmt, what, floor=FLOOR):
     assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} codes, first {np.argwhere(bad)[0]}"
 
 
-# every launch: a wave a row (K <= 1024), 256 to 1024 threads a row, the long kernel (K > 32768)
-NORM_SHAPES = [(1, 8), (5, 64), (7, 512), (6, 520), (9, 1024), (5, 1032), (1, 2048), (6, 2056), (1, 4096), (5, 4104),
-               (6, 8192), (3, 8200), (5, 16384), (2, 16392), (5, 32768), (5, 32776), (2, 65536), (300, 768)]
+# every launch: parts of a wave (K <= 256), a wave a row (K <= 1024, or 2048 when many), 256 to 1024 threads a row, the long kernel (K > 32768)
+NORM_SHAPES = [(1, 8), (5, 64), (70, 8), (37, 72), (41, 128), (19, 136), (9, 256), (6, 264), (7, 512), (6, 520), (9, 1024), (5, 1032), (1, 2048), (6, 2056), (1, 4096), (5, 4104),
+               (6, 8192), (3, 8200), (5, 16384), (2, 16392), (5, 32768), (5, 32776), (2, 65536), (300, 768), (1100, 1536), (1030, 2048)]
 
 
 @pytest.mark.parametrize("M,K", NORM_SHAPES)
@@ -192,8 +192,8 @@ def test_rms_norm_rows_do_not_depend_on_each_other(ops):
     assert torch.equal(q3[0], q[3]) and torch.equal(s3[0], s[3]) and torch.equal(y3[0], y[3])
 
 
-SWIGLU_SHAPES = [(1, 8), (5, 64), (7, 512), (6, 520), (9, 1024), (5, 1032), (3, 2048), (6, 2056), (1, 4096), (4, 4104),
-                 (6, 8192), (1, 14336), (5, 16384), (2, 16392), (5, 32768), (5, 32776), (300, 768)]
+SWIGLU_SHAPES = [(1, 8), (5, 64), (70, 8), (37, 72), (41, 128), (19, 136), (9, 256), (6, 264), (7, 512), (6, 520), (9, 1024), (5, 1032), (3, 2048), (6, 2056), (1, 4096), (4, 4104),
+                 (6, 8192), (1, 14336), (5, 16384), (2, 16392), (5, 32768), (5, 32776), (300, 768), (1100, 1536), (1030, 2048)]
 
 
 @pytest.mark.parametrize("M,I", SWIGLU_SHAPES)

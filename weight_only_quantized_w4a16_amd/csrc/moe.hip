@@ -487,21 +487,26 @@ void launch_moe_combine(const uint16_t* rows, const int* row_of_slot, const floa
     else go(std::false_type{});
 }
 
-// One workgroup per token: its threads hold the pieces of dy, and the slots'
-// products <dy, row> are reduced over the workgroup, J slots and SLOTS / J pieces a
-// thread at a time (J = 2, 4 or 8, the least that covers k: with 8 alone, 4096
+// NT threads per token, a workgroup or (rows of up to 64 pieces) a wave: 16384 tokens
+// of top-4, 128 / 512 bf16, 12.3 / 29.1 us with a wave, 21.7 / 30.2 with a workgroup; 1000
+// of top-8, 1024, 8.9 and 8.6.  They hold the pieces of dy, and the slots' products
+// <dy, row> are reduced over them, J slots and SLOTS / J pieces a thread at a time (J = 2, 4 or 8, the least that covers k: with 8 alone, 4096
 // tokens of top-2, 4096 bf16, took 37 us).
-// STREAM: drows, more than the caches hold until its reader comes, passes them by
-// (8192 / 4099 tokens of top-8, 2048 bf16, 112 / 59 us without, 91 / 49 with).
-template <int J, bool STREAM>
+// drows passes the caches by, which then keep the rows (4099 / 1000 / 256 tokens of
+// top-8, 2048 bf16, 59 / 17.0 / 6.3 us without, 49 / 12.7 / 5.6 with).
+#ifndef QG_MOE_BWD_WAVE_K          // longest row of one wave per token
+#define QG_MOE_BWD_WAVE_K 512
+#endif
+template <int NT, int J>
 __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
     const u32x4* __restrict__ dy, const u32x4* __restrict__ rows, const int* __restrict__ row_of_slot,
     const float* __restrict__ weights, int B, int k, int chunks, u32x4* __restrict__ drows, float* __restrict__ dweights) {
     constexpr int U = SLOTS / J;
     __shared__ float red[4][J];
-    const int b = blockIdx.x;
+    const int b = NT == 64 ? (int)(blockIdx.x * 4 + (threadIdx.x >> 6)) : (int)blockIdx.x;
+    if (b >= B) return;                          // whole waves, where no barrier follows
     const int T = B * k;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x % NT;
     for (int j0 = 0; j0 < k; j0 += J) {
         int r[J];
         float w[J], dot[J];
@@ -513,11 +518,11 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
             w[j] = in && weights ? weights[b * k + j0 + j] : 1.0f;
             dot[j] = 0.0f;
         }
-        for (int c0 = tid; c0 < chunks; c0 += 256 * U) {
+        for (int c0 = tid; c0 < chunks; c0 += NT * U) {
             u32x4 d[U], v[U][J];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * 256;
+                const int c = c0 + u * NT;
                 if (c >= chunks) continue;
                 d[u] = dy[(size_t)b * chunks + c];
                 if (dweights) {
@@ -528,7 +533,7 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * 256;
+                const int c = c0 + u * NT;
                 if (c >= chunks) continue;
                 float g[8];
                 unpack8(d[u], g);
@@ -539,7 +544,7 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
                     if (drows) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) f[i] = w[j] * g[i];
-                        store_row<STREAM>(drows + (size_t)r[j] * chunks + c, pack8(f));
+                        store_row<true>(drows + (size_t)r[j] * chunks + c, pack8(f));
                     }
                     if (dweights) {
                         unpack8(v[u][j], f);
@@ -553,30 +558,34 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 dot[j] = wave_sum(dot[j]);
-                if ((tid & 63) == 0) red[tid >> 6][j] = dot[j];
+                if (NT == 64 && tid == 0 && j0 + j < k) dweights[b * k + j0 + j] = dot[j];
+                if (NT > 64 && (tid & 63) == 0) red[tid >> 6][j] = dot[j];
             }
-            __syncthreads();
-            if (tid < J && j0 + tid < k)
-                dweights[b * k + j0 + tid] = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
-            __syncthreads();
+            if constexpr (NT > 64) {
+                __syncthreads();
+                if (tid < J && j0 + tid < k)
+                    dweights[b * k + j0 + tid] = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
+                __syncthreads();
+            }
         }
     }
 }
 
 void launch_moe_combine_backward(const uint16_t* dy, const uint16_t* rows, const int* row_of_slot, const float* weights,
                                  int B, int k, int K, uint16_t* drows, float* dweights, hipStream_t st) {
-    auto go = [&](auto j, auto stream) {
-        hipLaunchKernelGGL((moe_combine_backward_kernel<decltype(j)::value, decltype(stream)::value>), dim3(B), dim3(256),
+    auto go = [&](auto nt, auto j) {
+        constexpr int NT = decltype(nt)::value;
+        hipLaunchKernelGGL((moe_combine_backward_kernel<NT, decltype(j)::value>), dim3(NT == 64 ? (B + 3) / 4 : B), dim3(256),
                            0, st, reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(rows), row_of_slot,
                            weights, B, k, K / 8, reinterpret_cast<u32x4*>(drows), dweights);
     };
-    auto by_k = [&](auto stream) {
-        if (k <= 2) go(ic<2>{}, stream);
-        else if (k <= 4) go(ic<4>{}, stream);
-        else go(ic<8>{}, stream);
+    auto by_row = [&](auto j) {
+        if (K <= QG_MOE_BWD_WAVE_K) go(ic<64>{}, j);
+        else go(ic<256>{}, j);
     };
-    if ((size_t)B * k * K * 2 >= kStreamBytes) by_k(std::true_type{});
-    else by_k(std::false_type{});
+    if (k <= 2) by_row(ic<2>{});
+    else if (k <= 4) by_row(ic<4>{});
+    else by_row(ic<8>{});
 }
 
 }  // namespace qg

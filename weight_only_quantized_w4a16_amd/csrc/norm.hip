@@ -47,11 +47,26 @@ __device__ __forceinline__ uint32_t encode4(const float* q) {
     }
 }
 
-// Reductions over the NT threads of a row (`red`: one LDS word per wave, used
-// once per launch); every thread gets the result.  The order is fixed.
+// Reductions over the NT threads of a row, in a fixed order; every thread gets
+// the result.  NT < 64: lanes of one wave, by shuffles; 64: a wave; more: one LDS
+// word per wave (`red`, used once per launch) and a barrier.
+template <int NT>
+__device__ __forceinline__ double lanes_sum(double v) {
+    if constexpr (NT >= 64) return wave_sum(v);
+#pragma unroll
+    for (int o = NT / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+template <int NT>
+__device__ __forceinline__ float lanes_max(float v) {
+    if constexpr (NT >= 64) return wave_max_abs(v);
+#pragma unroll
+    for (int o = NT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
 template <int NT>
 __device__ __forceinline__ double row_sum(double v, double* red) {
-    v = wave_sum(v);
+    v = lanes_sum<NT>(v);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
         __syncthreads();
@@ -63,7 +78,7 @@ __device__ __forceinline__ double row_sum(double v, double* red) {
 }
 template <int NT>
 __device__ __forceinline__ float row_max(float v, float* red) {
-    v = wave_max_abs(v);
+    v = lanes_max<NT>(v);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
         __syncthreads();
@@ -76,8 +91,8 @@ __device__ __forceinline__ float row_max(float v, float* red) {
 // both at once: one barrier
 template <int NT>
 __device__ __forceinline__ void row_sum_max(double& sum, float& top, double* red_sum, float* red_max) {
-    sum = wave_sum(sum);
-    top = wave_max_abs(top);
+    sum = lanes_sum<NT>(sum);
+    top = lanes_max<NT>(top);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0) {
             red_sum[threadIdx.x >> 6] = sum;
@@ -92,6 +107,12 @@ __device__ __forceinline__ void row_sum_max(double& sum, float& top, double* red
             top = fmaxf(top, red_max[w]);
         }
     }
+}
+
+// rows of NT < 256 threads share workgroups of 256
+template <int NT>
+__device__ __forceinline__ int row_of_thread() {
+    return NT < 256 ? (int)(blockIdx.x * (256 / NT) + threadIdx.x / NT) : (int)blockIdx.x;
 }
 
 // The scale of a row and its codes: y times the rounded reciprocal of s (within
@@ -124,8 +145,7 @@ struct RowScale {
 };
 
 // ---------------------------------------------------------------------------
-// rms_norm: NT threads per row (64: one wave per row, four rows per workgroup;
-// else one row per workgroup), CPT 16-byte chunks per thread in registers.
+// rms_norm: NT threads per row, CPT 16-byte chunks per thread in registers.
 // x, residual and h may be the same memory: a thread reads its elements before
 // it writes them, and no other thread touches them.
 // ---------------------------------------------------------------------------
@@ -161,8 +181,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
     __shared__ double red_sum[NW];
     __shared__ float red_max[2][NW];
     const int tid = threadIdx.x % NT;
-    const int m = NT == 64 ? blockIdx.x * 4 + (int)(threadIdx.x >> 6) : (int)blockIdx.x;
-    if (m >= p.M) return;                                    // whole waves (NT = 64) or workgroups
+    const int m = row_of_thread<NT>();
+    if (m >= p.M) return;                                    // all threads of a row together
     const int chunks = p.K >> 3;
     const size_t row = (size_t)m * chunks;
     u32x4 xv[CPT], rv[CPT], wv[CPT];
@@ -301,16 +321,20 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs p) {
     }
 }
 
-// Threads per row and chunks per thread of a row of `chunks` pieces: one wave up
-// to 128 pieces, else one workgroup with two to four chunks a thread (measured
-// against one chunk and 1024 threads, and against eight: norm to e4m3 at 8191 x
-// 8192 81 us, 93 and 83; swiglu to e4m3 at 8192 x 4096 30 us with 256 threads, 38
-// with 512).  `many` (coded rows, four a CU or more): one wave up to 256 pieces,
-// which saves the barriers (swiglu at 16384 / 256 x 2048 30 / 3.2 us against 37 /
-// 2.9; the bf16 norm, with one barrier, gains nothing).
+// Threads per row and chunks per thread of a row of `chunks` pieces: part of a
+// wave up to 32 pieces (norm to e4m3 at 16384 x 128 5.7 us, with a whole wave a
+// row 11.6), one wave up to 128, else one workgroup with two to four chunks a
+// thread (measured against one chunk and 1024 threads, and against eight: norm to
+// e4m3 at 8191 x 8192 81 us, 93 and 83; swiglu to e4m3 at 8192 x 4096 30 us with 256
+// threads, 38 with 512).  `many` (coded rows, four a CU or more): one wave up to
+// 256 pieces, which saves the barriers (swiglu at 16384 / 256 x 2048 30 / 3.2 us
+// against 37 / 2.9; the bf16 norm, with one barrier, gains nothing).
 template <class Go>
 static bool with_row_shape(int chunks, bool many, Go&& go) {
-    if (chunks <= 64) go(ic<64>{}, ic<1>{});
+    if (chunks <= 8) go(ic<8>{}, ic<1>{});
+    else if (chunks <= 16) go(ic<16>{}, ic<1>{});
+    else if (chunks <= 32) go(ic<32>{}, ic<1>{});
+    else if (chunks <= 64) go(ic<64>{}, ic<1>{});
     else if (chunks <= 128) go(ic<64>{}, ic<2>{});
     else if (chunks <= 192 && many) go(ic<64>{}, ic<3>{});
     else if (chunks <= 256 && many) go(ic<64>{}, ic<4>{});
@@ -325,9 +349,9 @@ static bool with_row_shape(int chunks, bool many, Go&& go) {
 static bool many_rows(int M) { return M >= 4 * device_cu_count(); }
 // workgroups and threads of M rows at NT threads a row
 template <int NT>
-static dim3 row_grid(int M) { return dim3(NT == 64 ? (M + 3) / 4 : M); }
+static dim3 row_grid(int M) { return dim3(NT < 256 ? (M + 256 / NT - 1) / (256 / NT) : M); }
 template <int NT>
-static dim3 row_block() { return dim3(NT == 64 ? 256 : NT); }
+static dim3 row_block() { return dim3(NT < 256 ? 256 : NT); }
 
 template <class Fmt>
 static void launch_norm(const NormArgs& p, hipStream_t st) {
@@ -396,7 +420,7 @@ template <class Fmt, int NT, int CPT, bool STREAM>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void swiglu_quant_kernel(SwigluArgs p) {
     __shared__ float red[NT < 256 ? 4 : NT / 64];
     const int tid = threadIdx.x % NT;
-    const int m = NT == 64 ? blockIdx.x * 4 + (int)(threadIdx.x >> 6) : (int)blockIdx.x;
+    const int m = row_of_thread<NT>();
     if (m >= p.M) return;
     const int chunks = p.I >> 3;
     const u32x4* gate = p.gu + (size_t)m * 2 * chunks;
