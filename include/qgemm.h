@@ -92,7 +92,9 @@ size_t qg_int4_g128_scale_bytes(int64_t K, int64_t N);
  * shape), e.g. "w4a16_decode_kernel<KW, U, D> S=s", "w4a16_small_m_kernel<MT,
  * CT>", "w4a16_large_m_kernel<NS, NB, BM> S=s", "w8a8_small_m_kernel<MT, CT>",
  * "w8a8_large_m_kernel<NS, NB, BM> S=s" (S: K slices across workgroups).
- * Useful to match profiler records to calls.
+ * Useful to match profiler records to calls (the W4A16 kernels' records have one
+ * more template argument, the epilogue; qgemm_w4a16_epilogue runs the kernel of
+ * the same name).
  */
 const char *qg_w4a16_kernel_for(int64_t M, int64_t N, int64_t K);
 const char *qg_w8a8_kernel_for(int64_t M, int64_t N, int64_t K);
