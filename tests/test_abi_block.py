@@ -151,3 +151,18 @@ def test_activation_names(ops):
     assert codes == ops.ACTIVATIONS
     from oracle import block
     assert set(block.EPILOGUE_ACTIVATIONS) == set(codes)
+
+
+def test_binding_refuses_wrong_arguments(ops):
+    with pytest.raises(TypeError, match="tensor or None"):
+        ops.rms_norm("x", None, None, 1e-5, 2, 64, None, None)
+    with pytest.raises(TypeError):
+        ops.swiglu(None, 2.5, 64, None)
+    with pytest.raises(OverflowError):
+        ops.swiglu(None, 2 ** 40, 64, None)
+    with pytest.raises((OverflowError, ValueError)):
+        ops.moe_dispatch(None, None, None, 1, 1, 1, 0, None, None, None, None, None, -1)
+    with pytest.raises(ValueError, match="no tensor"):
+        ops.swiglu(None, 2, 64, None)
+    with pytest.raises(ValueError, match="activation"):
+        ops.qgemm_w4a16_epilogue(None, None, None, None, "tanh", None, None, 1, 16, 128)

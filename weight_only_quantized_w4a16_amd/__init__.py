@@ -1,4 +1,5 @@
-"""MI355X (gfx950) quantized linear layer for LLM decode: W4A16 INT4-g128 and W8A8-FP8.
+"""MI355X (gfx950) quantized linear layer for LLM decode: W4A16 INT4-g128 and W8A8-FP8,
+with the operators that stand between two such layers of a decoder block.
 
 The compute lives in the HIP library libqgemm.so (C ABI declared in
 include/qgemm.h); `ops` is a thin ctypes binding with the same entry-point

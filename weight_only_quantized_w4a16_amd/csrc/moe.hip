@@ -111,8 +111,8 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
                                                             int* __restrict__ row_of_slot) {
     extern __shared__ int lds[];
     int* all = lds;                              // [E]: slots of the expert
-    int* first = lds + E;                        // [E]: first row of the expert, then of its share in this segment
-    int* next = lds + 2 * E;                     // [SORT_WAVES][E]: counts, then next rows, by wave
+    int* first = lds + E;                        // [E]: its slots in the segments before, then its first row
+    int* next = lds + 2 * E;                     // [SORT_WAVES][E]: counts by wave, then the next row past `first`
     __shared__ int wave_total[SORT_WAVES];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(const int* __restric
         for (int s = s0 + lane; s < s1; s += 64) count(ids[s]);
     }
     __syncthreads();
-    // counts become the first row of each (expert, wave)
+    // counts become the number of the expert's slots before each wave's
     for (int e = tid; e < E; e += SORT_NT) {
         int at = first[e];
         for (int w = 0; w < SORT_WAVES; ++w) {

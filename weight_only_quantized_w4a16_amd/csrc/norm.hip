@@ -406,11 +406,10 @@ static bool stream_gate_up(const SwigluArgs& p) { return (size_t)p.M * p.I * 4 >
 template <bool STREAM>
 __global__ __launch_bounds__(256) void swiglu_kernel(SwigluArgs p) {
     const int chunks = p.I >> 3;
-    const size_t total = (size_t)p.M * chunks;
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
-    const size_t m = i / chunks;
-    const u32x4* gate = p.gu + i + m * chunks;
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x;      // a dispatch holds fewer than 2^32 threads
+    const uint32_t m = i / (uint32_t)chunks;
+    if (m >= (uint32_t)p.M) return;
+    const u32x4* gate = p.gu + i + (size_t)m * chunks;
     float y[8];
     swiglu8(load_row<STREAM>(gate), load_row<STREAM>(gate + chunks), y);
     p.y[i] = pack8(y);
