@@ -14,7 +14,7 @@
 // in slot order, so no atomics and no second order of summation exist.  All of
 // them are bound by memory from about a thousand tokens on, by the launch below.
 // Graph-timed (top-8 of 128, rows of 2048, 8192 / 64 / 1 tokens, us): dispatch of
-// e4m3 rows 27 / 4.9 / 4.2 (5.5 TB/s at 8192), combine of bf16 rows 53 / 3.0 / 2.7 (6.3
+// e4m3 rows 27 / 4.5 / 3.8 (5.5 TB/s at 8192), combine of bf16 rows 53 / 3.0 / 2.7 (6.3
 // TB/s), its gradient 92 / 4.1 / 3.7 (6.2 TB/s).
 #include <algorithm>
 #include <atomic>
@@ -306,7 +306,7 @@ void launch_moe_gather(const void* rows, const float* scale, const int* row_of_s
 // slot) while the token's row is on its way from memory; one more workgroup
 // writes the offsets.  The work grows with the workgroups times T: DIRECT_MAX_WORK
 // bounds it (top-8 of 128, e4m3 rows of 2048, this / the two-launch sort and the
-// copy, us: 128 tokens 5.8 / 8.0, 256 7.4 / 8.6, 512 11.1 / 9.6; top-2 of 8, rows of
+// copy, us: 128 tokens 5.4 / 8.0, 256 7.0 / 8.6, 512 10.7 / 9.6; top-2 of 8, rows of
 // 4096: 512 5.0 / 7.9, 1024 8.5 / 9.4).
 // ---------------------------------------------------------------------------
 #ifndef QG_MOE_DIRECT_MAX_WORK
@@ -353,11 +353,14 @@ __global__ __launch_bounds__(256) void moe_dispatch_direct_kernel(const int* __r
         // (expert, slot) as one number: T <= DIRECT_MAX_WORK and E <= 2^10 fit 32 bits
         unsigned key[SLOTS];
         int n[SLOTS];
+        unsigned kept = 0;                       // bit j: slot j has a row
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
             const int slot = b * k + j0 + j;
             const int e = j0 + j < k ? ids[slot] : -1;
-            key[j] = e >= 0 && e < E ? (unsigned)e * (unsigned)T + (unsigned)slot : 0u;
+            const bool in = e >= 0 && e < E;
+            key[j] = in ? (unsigned)e * (unsigned)T + (unsigned)slot : 0u;
+            kept |= in ? 1u << j : 0u;
             n[j] = 0;
         }
         for (int t0 = wave * 64; t0 < T; t0 += 256) {
@@ -373,17 +376,20 @@ __global__ __launch_bounds__(256) void moe_dispatch_direct_kernel(const int* __r
             for (int j = 0; j < SLOTS; ++j) mine[wave][j] = n[j];
         }
         __syncthreads();                         // the other half of `below` is free again after it
+        int r[SLOTS];
 #pragma unroll
-        for (int j = 0; j < SLOTS; ++j) {
-            if (j0 + j >= k) break;
-            const int slot = b * k + j0 + j;
-            const int e = ids[slot];
-            const bool kept = e >= 0 && e < E;
-            const int r = mine[0][j] + mine[1][j] + mine[2][j] + mine[3][j];
-            if (part == 0 && tid == j) row_of_slot[slot] = kept ? r : -1;
-            if (!kept) continue;
-            if (c < chunks) out[(size_t)r * chunks + c] = v;
-            if (scale && c == 0) scale_out[r] = s;
+        for (int j = 0; j < SLOTS; ++j) r[j] = mine[0][j] + mine[1][j] + mine[2][j] + mine[3][j];
+        if (c < chunks) {
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j)
+                if (kept >> j & 1) out[(size_t)r[j] * chunks + c] = v;
+        }
+        if (c == 0) {
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) {
+                if (j0 + j < k) row_of_slot[b * k + j0 + j] = kept >> j & 1 ? r[j] : -1;
+                if (scale && (kept >> j & 1)) scale_out[r[j]] = s;
+            }
         }
     }
 }
