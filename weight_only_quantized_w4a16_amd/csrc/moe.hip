@@ -306,11 +306,11 @@ void launch_moe_gather(const void* rows, const float* scale, const int* row_of_s
 // slot) while the token's row is on its way from memory; one more workgroup
 // writes the offsets.  The work grows with the workgroups times T: DIRECT_MAX_WORK
 // bounds it (top-8 of 128, e4m3 rows of 2048, this / the two-launch sort and the
-// copy, us: 128 tokens 5.4 / 8.0, 256 7.0 / 8.6, 512 10.7 / 9.6; top-2 of 8, rows of
-// 4096: 512 5.0 / 7.9, 1024 8.5 / 9.4).
+// copy, us: 192 tokens 6.2 / 8.4, 256 7.0 / 8.6, 512 10.6 / 9.7; top-2 of 8, rows of
+// 4096: 512 5.0 / 7.9, 1024 8.5 / 9.5).
 // ---------------------------------------------------------------------------
 #ifndef QG_MOE_DIRECT_MAX_WORK
-#define QG_MOE_DIRECT_MAX_WORK (1 << 20)
+#define QG_MOE_DIRECT_MAX_WORK (5 << 18)
 #endif
 
 // work of `parts` workgroups per token
