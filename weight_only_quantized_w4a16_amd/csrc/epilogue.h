@@ -4,8 +4,14 @@
 // together (an In) while other work is under way, and applies them before the
 // first store: y may be the residual's memory, so the compiler may not move a
 // load over such a store.  Loaded bits stay as they are until then: a conversion
-// next to the load would wait for it (1 x 4096 x 28672 with a bias 14.4 us so, 13.9
-// otherwise, 13.0 for the plain product).
+// next to the load would wait for it.  Whether there is a residual and an
+// activation is part of the type: fetched residuals cost the products of few rows
+// up to 19 registers, and the branch over the activations' code some time per
+// tile, which the wide layers that have neither do not pay.  A bias alone, 1 / 8 /
+// 16 x 4096 x 28672 (plain product 13.0 / 13.8 / 14.5 us), costs 0.2 / 0.1 / 0.1 us
+// so, 0.8 / 0.6 / 0.6 with the activation decided at run time and 1.2 / 0.7 / 0.9
+// with the residual too.  Beside a residual the activation stays a branch: left out,
+// 16 x 14336 x 4096 took 14.3 us instead of 14.1.
 #pragma once
 
 #include "device_common.h"
@@ -86,12 +92,13 @@ __device__ __forceinline__ void activate(V& v, int act) {
     }
 }
 
+template <bool RES, bool ACT>
 struct Epilogue {
     using out_ptr = uint16_t*;
     static constexpr bool kActive = true;
     const uint16_t* bias;                        // [N] or null
-    const uint16_t* residual;                    // [M, N] or null
-    int act;
+    const uint16_t* residual;                    // [M, N], read if RES
+    int act;                                     // qg_activation, looked at if ACT
 
     template <int C>
     struct In {
@@ -110,7 +117,7 @@ struct Epilogue {
     }
     template <bool BIAS, int C, class Row, class Col>
     __device__ __forceinline__ void fetch(In<C>& in, int M, int N, Row row, Col col) const {
-        if (residual) {
+        if (RES) {
 #pragma unroll
             for (int i = 0; i < C; ++i) in.r[i] = residual[(size_t)min(row(i), M - 1) * N + min(col(i), N - 1)];
         }
@@ -139,8 +146,8 @@ struct Epilogue {
 private:
     template <int C, class V>
     __device__ __forceinline__ void finish(V& v, const In<C>& in) const {
-        activate<C>(v, act);
-        if (residual) {
+        if (ACT) activate<C>(v, act);
+        if (RES) {
 #pragma unroll
             for (int i = 0; i < C; ++i) v[i] += bf16_to_f32(in.r[i]);
         }

@@ -1961,7 +1961,9 @@ void launch_qgemm_w4a16_epilogue(const uint16_t* a, const uint32_t* packed, cons
                                  int activation, const uint16_t* residual, uint16_t* y, int M, int N, int K, void* ws,
                                  hipStream_t s) {
     if (!bias && !residual && activation == 0) launch_qgemm_w4a16(a, packed, scales, y, M, N, K, ws, s);
-    else launch_w4a16(a, packed, scales, y, M, N, K, ws, Epilogue{bias, residual, activation}, s);
+    else if (residual) launch_w4a16(a, packed, scales, y, M, N, K, ws, Epilogue<true, true>{bias, residual, activation}, s);
+    else if (activation) launch_w4a16(a, packed, scales, y, M, N, K, ws, Epilogue<false, true>{bias, nullptr, activation}, s);
+    else launch_w4a16(a, packed, scales, y, M, N, K, ws, Epilogue<false, false>{bias, nullptr, 0}, s);
 }
 
 }  // namespace qg
