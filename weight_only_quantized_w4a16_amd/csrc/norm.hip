@@ -31,8 +31,8 @@ struct FmtNone {                               // bf16 output only
 template <class Fmt>
 constexpr bool kCodes = !std::is_same<Fmt, FmtNone>::value;
 
-// Four quotients -> four codes.  |q| exceeds q_max by roundings only (the scale
-// is the row's own maximum), so it rounds to the largest code without a clamp.
+// Four quotients -> four codes.  |q| <= q_max up to roundings, which still round
+// to the largest code: no clamp here.
 template <class Fmt>
 __device__ __forceinline__ uint32_t encode4(const float* q) {
     if constexpr (std::is_same<Fmt, FmtE4M3>::value) {
@@ -117,7 +117,10 @@ __device__ __forceinline__ int row_of_thread() {
 
 // The scale of a row and its codes: y times the rounded reciprocal of s (within
 // one unit in the last place of the IEEE quotient y / s); a scale too small for
-// a finite reciprocal divides.
+// a finite reciprocal divides.  The scale is the row's own maximum over q_max, so
+// |y / s| exceeds q_max by roundings only -- except where s is subnormal, a whole
+// number of steps of 2^-149 that max|y| / q_max may be far from (max|y| = 178
+// steps: an int8 scale of one).  There the quotient is clamped.
 struct RowScale {
     float s, r;
     bool fast;
@@ -138,7 +141,10 @@ struct RowScale {
             for (int j = 0; j < 8; ++j) q[j] = y[j] * r;
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = y[j] / s;
+            for (int j = 0; j < 8; ++j) {
+                q[j] = y[j] / s;
+                if (fabsf(q[j]) > Fmt::qmax) q[j] = copysignf(Fmt::qmax, q[j]);
+            }
         }
         return make_uint2(encode4<Fmt>(q), encode4<Fmt>(q + 4));
     }
