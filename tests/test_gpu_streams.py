@@ -1,0 +1,91 @@
+"""Work on a stream that the caller gives: what it reads, clears and keeps is ordered
+on that stream, whatever the current stream is busy with.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import announce, dev_bf16
+from weight_only_quantized_w4a16_amd import synth
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    from weight_only_quantized_w4a16_amd import ops as _ops
+    return _ops
+
+
+class Busy:
+    """A few milliseconds of work on the current stream."""
+
+    def __init__(self):
+        self.a = torch.randn((4096, 4096), device="cuda:0")
+        self.a @ self.a                                       # the library's own preparations
+
+    def __call__(self):
+        for _ in range(8):
+            self.a = torch.sin(self.a @ self.a)
+
+
+# dense products whose plans split K (workspaces with counters), with M rows that grow
+SPLIT = [(16, 1024, 14336), (100, 4096, 4096)]
+
+
+def products(ops, N, K):
+    """name -> a function that makes a new helper and returns its call."""
+    w = dev_bf16(synth.weights(K, N, seed=3))
+    w4, w8, wi = ops.Int4G128Weight.from_bf16(w), ops.Fp8Weight.from_bf16(w), ops.Int8Weight.from_bf16(w)
+    bias = dev_bf16(synth.normal_bf16((N,), 2))
+    return {
+        "w4a16": lambda: ops.W4A16Linear(w4),
+        "w4a16 epilogue": lambda: ops.W4A16Linear(w4, bias, "gelu"),
+        "w8a8 fp8": lambda: ops.W8A8Fp8Linear(w8),
+        "w8a8 int8": lambda: ops.W8A8Int8Linear(wi),
+        "w4a8": lambda: ops.W4A8Linear(w4),
+    }
+
+
+@pytest.mark.parametrize("M,N,K", SPLIT)
+def test_first_call_on_another_stream(ops, M, N, K):
+    """The first call brings its workspace: its clearing must not wait behind the current stream's work."""
+    announce(f"first call on another stream M={M} N={N} K={K}")
+    assert not ops.w4a16_kernel_for(M, N, K).endswith("S=1")
+    a = dev_bf16(synth.activations(M, K, seed=1))
+    makers = products(ops, N, K)
+    want = {name: make()(a) for name, make in makers.items()}
+    busy, st = Busy(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for name, make in makers.items():
+        lin = make()
+        busy()
+        got = lin(a, stream=st)
+        again = lin(a, stream=st)
+        st.synchronize()
+        assert torch.equal(got, want[name]) and torch.equal(again, want[name]), name
+        torch.cuda.synchronize()
+
+
+def test_growing_on_another_stream(ops):
+    """A workspace that a call outgrows is not handed out while the given stream still uses it."""
+    announce("workspace outgrown on another stream")
+    N, K = 4096, 4096
+    small, large = (dev_bf16(synth.activations(M, K, seed=M)) for M in (70, 100))
+    need = ops.w4a16_workspace_bytes(70, N, K)
+    assert 0 < need < ops.w4a16_workspace_bytes(100, N, K)
+    make = products(ops, N, K)["w4a16 epilogue"]
+    want = make()(small), make()(large)
+    busy, st = Busy(), torch.cuda.Stream()
+    for _ in range(3):
+        lin = make()
+        first = lin(small)                                    # the workspace belongs to the current stream
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            busy()
+        got = lin(small, stream=st), lin(large, stream=st)
+        spoil = [torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda:0") for _ in range(16)]
+        torch.cuda.synchronize()
+        assert torch.equal(first, want[0]) and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        del spoil

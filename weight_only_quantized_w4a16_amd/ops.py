@@ -9,6 +9,7 @@ the block operators' calls) is missing, importing this module raises.
 bf16 data travels as torch.bfloat16 (or int16 / uint16 bit patterns) tensors;
 e4m3 codes as torch.uint8 (or torch.float8_e4m3fn) tensors.
 """
+import contextlib
 import ctypes
 import os
 
@@ -345,6 +346,38 @@ def moe_combine_backward(dy_bf16, rows_bf16, row_of_slot, weights, B, k, K, drow
 
 # ---- tensor-level helpers (allocate outputs with torch, then call the above) --
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream, t):
+    """Context in which `stream` is the current stream (None: no change): what a helper
+    allocates, clears or copies then belongs to the stream that launches the work on it,
+    and may be freed while that runs."""
+    if stream is None:
+        return _HERE
+    if stream.device_index != t.get_device():
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
+class _Scratch:
+    """A workspace kept from call to call, for calls that do not overlap in time."""
+
+    _ws = None
+
+    def _scratch(self, need, device, alloc=torch.zeros):
+        """(buffer, need), or (None, 0) if nothing is needed.  A new buffer comes from the
+        current stream; a call on another stream follows the one that brought it."""
+        if not need:
+            return None, 0
+        if self._ws is None or self._ws.numel() * self._ws.element_size() < need:
+            if self._ws is not None:
+                # the last calls may have used it on another stream than its own; this call follows them
+                self._ws.record_stream(torch.cuda.current_stream(device))
+            self._ws = alloc(need, dtype=torch.uint8, device=device)
+        return self._ws, need
+
+
 def _bf16(t):
     if t.dtype in (torch.int16, torch.uint16):
         return t
@@ -364,23 +397,25 @@ class Int4G128Weight:
         """Abs-max scales, or with mse_grid > 0 the MSE-optimal clipping
         threshold searched over alpha = i / mse_grid, i = 1 .. mse_grid."""
         K, N = w.shape
-        packed = torch.empty(max(packed_bytes(K, N) // 4, 1), dtype=torch.int32, device=w.device)
-        scales = torch.empty(max(scale_bytes(K, N) // 2, 1), dtype=torch.int16, device=w.device)
-        if mse_grid:
-            pack_int4_g128_mse(_bf16(w.contiguous()), K, N, mse_grid, packed, scales, stream)
-        else:
-            pack_int4_g128(_bf16(w.contiguous()), K, N, packed, scales, stream)
+        with _on(stream, w):
+            packed = torch.empty(max(packed_bytes(K, N) // 4, 1), dtype=torch.int32, device=w.device)
+            scales = torch.empty(max(scale_bytes(K, N) // 2, 1), dtype=torch.int16, device=w.device)
+            if mse_grid:
+                pack_int4_g128_mse(_bf16(w.contiguous()), K, N, mse_grid, packed, scales)
+            else:
+                pack_int4_g128(_bf16(w.contiguous()), K, N, packed, scales)
         return cls(packed, scales, K, N)
 
     def dequant(self, with_codes=False, stream=None):
-        w = torch.empty((self.K, self.N), dtype=torch.bfloat16, device=self.packed.device)
-        codes = torch.empty((self.K, self.N), dtype=torch.uint8, device=self.packed.device) \
-            if with_codes else None
-        dequant_int4_g128(self.packed, self.scales, self.K, self.N, w, codes, stream)
+        with _on(stream, self.packed):
+            w = torch.empty((self.K, self.N), dtype=torch.bfloat16, device=self.packed.device)
+            codes = torch.empty((self.K, self.N), dtype=torch.uint8, device=self.packed.device) \
+                if with_codes else None
+            dequant_int4_g128(self.packed, self.scales, self.K, self.N, w, codes)
         return (w, codes) if with_codes else w
 
 
-class W4A16Linear:
+class W4A16Linear(_Scratch):
     """y = act(a @ w_hat + bias) + residual for a packed INT4 g128 weight; owns a
     reusable workspace.  bias: bf16 [N] or None; activation: a name of ACTIVATIONS."""
 
@@ -390,30 +425,27 @@ class W4A16Linear:
         self.w = weight
         self.bias = None if bias is None else _is(bias, _BF16, (weight.N,), "bias")
         self.activation = activation
-        self._ws = None
 
     def workspace(self, M):
-        need = w4a16_workspace_bytes(M, self.w.N, self.w.K)
-        if need and (self._ws is None or self._ws.numel() < need):
-            # zero-filled once; every call resets the counters it uses
-            self._ws = torch.zeros(need, dtype=torch.uint8, device=self.w.packed.device)
-        return (self._ws, need) if need else (None, 0)
+        # zero-filled once; every call resets the counters it uses
+        return self._scratch(w4a16_workspace_bytes(M, self.w.N, self.w.K), self.w.packed.device)
 
     def __call__(self, a, out=None, stream=None, residual=None):
         """residual: bf16 [M, N] added after the activation; it may be `out` itself."""
         M, K = a.shape
         if K != self.w.K:
             raise ValueError(f"activation K={K} != weight K={self.w.K}")
-        y = out if out is not None else torch.empty((M, self.w.N), dtype=torch.bfloat16,
-                                                    device=a.device)
-        ws, nbytes = self.workspace(M)
-        if residual is not None or self.bias is not None or self.activation != "none":
-            if residual is not None:
-                _is(residual, _BF16, (M, self.w.N), "residual")
-            qgemm_w4a16_epilogue(_bf16(a), self.w.packed, self.w.scales, self.bias, self.activation, residual,
-                                 _is(y, _BF16, (M, self.w.N), "out"), M, self.w.N, K, ws, nbytes, stream)
-            return y
-        qgemm_w4a16(_bf16(a), self.w.packed, self.w.scales, y, M, self.w.N, K, ws, nbytes, stream)
+        with _on(stream, a):
+            y = out if out is not None else torch.empty((M, self.w.N), dtype=torch.bfloat16,
+                                                        device=a.device)
+            ws, nbytes = self.workspace(M)
+            if residual is not None or self.bias is not None or self.activation != "none":
+                if residual is not None:
+                    _is(residual, _BF16, (M, self.w.N), "residual")
+                qgemm_w4a16_epilogue(_bf16(a), self.w.packed, self.w.scales, self.bias, self.activation, residual,
+                                     _is(y, _BF16, (M, self.w.N), "out"), M, self.w.N, K, ws, nbytes)
+            else:
+                qgemm_w4a16(_bf16(a), self.w.packed, self.w.scales, y, M, self.w.N, K, ws, nbytes)
         return y
 
 
@@ -426,9 +458,10 @@ class Fp8Weight:
     @classmethod
     def from_bf16(cls, w, stream=None):
         K, N = w.shape
-        codes = torch.empty(K * N, dtype=torch.uint8, device=w.device)
-        scales = torch.empty(N, dtype=torch.float32, device=w.device)
-        quant_weight_fp8_per_channel(_bf16(w.contiguous()), K, N, codes, scales, stream)
+        with _on(stream, w):
+            codes = torch.empty(K * N, dtype=torch.uint8, device=w.device)
+            scales = torch.empty(N, dtype=torch.float32, device=w.device)
+            quant_weight_fp8_per_channel(_bf16(w.contiguous()), K, N, codes, scales)
         return cls(codes, scales, K, N)
 
 
@@ -444,23 +477,23 @@ def qgemm_w4a16_grouped(a_bf16, offsets_i32, packed, scales, y_bf16, E, T, N, K,
                                     _stream(stream)))
 
 
-class GroupedInt4Weight:
+class GroupedInt4Weight(_Scratch):
     """E experts' [K, N] weights packed back to back (device buffers owned by torch)."""
 
     def __init__(self, packed, scales, E, K, N):
         self.packed, self.scales, self.E, self.K, self.N = packed, scales, E, K, N
-        self._ws = None
 
     @classmethod
     def from_bf16(cls, w, stream=None):
         """w: [E, K, N] bf16 on the device."""
         E, K, N = w.shape
         words, nsc = packed_bytes(K, N) // 4, scale_bytes(K, N) // 2
-        packed = torch.empty(E * words, dtype=torch.int32, device=w.device)
-        scales = torch.empty(E * nsc, dtype=torch.int16, device=w.device)
-        for e in range(E):
-            pack_int4_g128(_bf16(w[e].contiguous()), K, N, packed[e * words:(e + 1) * words],
-                           scales[e * nsc:(e + 1) * nsc], stream)
+        with _on(stream, w):
+            packed = torch.empty(E * words, dtype=torch.int32, device=w.device)
+            scales = torch.empty(E * nsc, dtype=torch.int16, device=w.device)
+            for e in range(E):
+                pack_int4_g128(_bf16(w[e].contiguous()), K, N, packed[e * words:(e + 1) * words],
+                               scales[e * nsc:(e + 1) * nsc])
         return cls(packed, scales, E, K, N)
 
     def __call__(self, a, offsets, out=None, stream=None):
@@ -468,12 +501,10 @@ class GroupedInt4Weight:
         T, K = a.shape
         if K != self.K or offsets.numel() != self.E + 1 or offsets.dtype != torch.int32:
             raise ValueError("grouped GEMM: activation K or offsets do not match the weights")
-        y = out if out is not None else torch.empty((T, self.N), dtype=torch.bfloat16, device=a.device)
-        need = w4a16_grouped_workspace_bytes(self.E, T, self.N, K)
-        if need and (self._ws is None or self._ws.numel() * 4 < need):
-            self._ws = torch.empty((need + 3) // 4, dtype=torch.int32, device=a.device)
-        qgemm_w4a16_grouped(_bf16(a), offsets, self.packed, self.scales, y, self.E, T, self.N, K,
-                            self._ws if need else None, need, stream)
+        with _on(stream, a):
+            y = out if out is not None else torch.empty((T, self.N), dtype=torch.bfloat16, device=a.device)
+            ws, need = self._scratch(w4a16_grouped_workspace_bytes(self.E, T, self.N, K), a.device, torch.empty)
+            qgemm_w4a16_grouped(_bf16(a), offsets, self.packed, self.scales, y, self.E, T, self.N, K, ws, need)
         return y
 
     def w4a8(self, qa, sa, offsets, out=None, stream=None):
@@ -481,12 +512,10 @@ class GroupedInt4Weight:
         T, K = qa.shape
         if K != self.K or offsets.numel() != self.E + 1 or offsets.dtype != torch.int32:
             raise ValueError("grouped GEMM: activation K or offsets do not match the weights")
-        y = out if out is not None else torch.empty((T, self.N), dtype=torch.bfloat16, device=qa.device)
-        need = w4a16_grouped_workspace_bytes(self.E, T, self.N, K)
-        if need and (self._ws is None or self._ws.numel() * 4 < need):
-            self._ws = torch.empty((need + 3) // 4, dtype=torch.int32, device=qa.device)
-        qgemm_w4a8_fp8_grouped(qa, sa, offsets, self.packed, self.scales, y, self.E, T, self.N, K,
-                               self._ws if need else None, need, stream)
+        with _on(stream, qa):
+            y = out if out is not None else torch.empty((T, self.N), dtype=torch.bfloat16, device=qa.device)
+            ws, need = self._scratch(w4a16_grouped_workspace_bytes(self.E, T, self.N, K), qa.device, torch.empty)
+            qgemm_w4a8_fp8_grouped(qa, sa, offsets, self.packed, self.scales, y, self.E, T, self.N, K, ws, need)
         return y
 
     def w4a8_dynamic(self, a, offsets, out=None, stream=None):
@@ -494,36 +523,32 @@ class GroupedInt4Weight:
         T, K = a.shape
         if K != self.K or offsets.numel() != self.E + 1 or offsets.dtype != torch.int32:
             raise ValueError("grouped GEMM: activation K or offsets do not match the weights")
-        y = out if out is not None else torch.empty((T, self.N), dtype=torch.bfloat16, device=a.device)
-        need = w4a8_grouped_dynamic_workspace_bytes(self.E, T, self.N, K)
-        if need and (self._ws is None or self._ws.numel() * 4 < need):
-            self._ws = torch.empty((need + 3) // 4, dtype=torch.int32, device=a.device)
-        qgemm_w4a8_fp8_grouped_dynamic(_bf16(a), offsets, self.packed, self.scales, y, self.E, T, self.N, K,
-                                       self._ws if need else None, need, stream)
+        with _on(stream, a):
+            y = out if out is not None else torch.empty((T, self.N), dtype=torch.bfloat16, device=a.device)
+            ws, need = self._scratch(w4a8_grouped_dynamic_workspace_bytes(self.E, T, self.N, K), a.device, torch.empty)
+            qgemm_w4a8_fp8_grouped_dynamic(_bf16(a), offsets, self.packed, self.scales, y, self.E, T, self.N, K, ws, need)
         return y
 
 
 def quantize_activations(a, stream=None):
     M, K = a.shape
-    q = torch.empty((M, K), dtype=torch.uint8, device=a.device)
-    s = torch.empty(M, dtype=torch.float32, device=a.device)
-    quant_act_per_token(_bf16(a), M, K, q, s, stream)
+    with _on(stream, a):
+        q = torch.empty((M, K), dtype=torch.uint8, device=a.device)
+        s = torch.empty(M, dtype=torch.float32, device=a.device)
+        quant_act_per_token(_bf16(a), M, K, q, s)
     return q, s
 
 
-class W8A8Fp8Linear:
+class W8A8Fp8Linear(_Scratch):
     """y = bf16(s_a s_w (qa @ qw)) with per-token quantization of a on every call."""
 
     def __init__(self, weight: Fp8Weight):
         self.w = weight
-        self._ws = None
 
     def workspace(self, M, dynamic=False):
         need = (w8a8_dynamic_workspace_bytes if dynamic else w8a8_workspace_bytes)(M, self.w.N, self.w.K)
-        if need and (self._ws is None or self._ws.numel() < need):
-            # zero-filled once; every call resets the counters it uses
-            self._ws = torch.zeros(need, dtype=torch.uint8, device=self.w.codes.device)
-        return (self._ws, need) if need else (None, 0)
+        # zero-filled once; every call resets the counters it uses
+        return self._scratch(need, self.w.codes.device)
 
     def __call__(self, a, out=None, stream=None, qa=None, sa=None):
         """Without qa / sa the activations are quantized inside the call
@@ -531,14 +556,14 @@ class W8A8Fp8Linear:
         M, K = a.shape
         if K != self.w.K:
             raise ValueError(f"activation K={K} != weight K={self.w.K}")
-        y = out if out is not None else torch.empty((M, self.w.N), dtype=torch.bfloat16,
-                                                    device=a.device)
-        ws, need = self.workspace(M, dynamic=qa is None)
-        if qa is None:
-            qgemm_w8a8_fp8_dynamic(_bf16(a), self.w.codes, self.w.scales, y, M, self.w.N, K, ws, need,
-                                   stream)
-        else:
-            qgemm_w8a8_fp8(qa, sa, self.w.codes, self.w.scales, y, M, self.w.N, K, ws, need, stream)
+        with _on(stream, a):
+            y = out if out is not None else torch.empty((M, self.w.N), dtype=torch.bfloat16,
+                                                        device=a.device)
+            ws, need = self.workspace(M, dynamic=qa is None)
+            if qa is None:
+                qgemm_w8a8_fp8_dynamic(_bf16(a), self.w.codes, self.w.scales, y, M, self.w.N, K, ws, need)
+            else:
+                qgemm_w8a8_fp8(qa, sa, self.w.codes, self.w.scales, y, M, self.w.N, K, ws, need)
         return y
 
 
@@ -552,10 +577,11 @@ class W4A8Linear:
         M, K = a.shape
         if K != self.w.K:
             raise ValueError(f"activation K={K} != weight K={self.w.K}")
-        if qa is None:
-            qa, sa = quantize_activations(a, stream)
-        y = out if out is not None else torch.empty((M, self.w.N), dtype=torch.bfloat16, device=a.device)
-        qgemm_w4a8_fp8(qa, sa, self.w.packed, self.w.scales, y, M, self.w.N, K, stream)
+        with _on(stream, a):
+            if qa is None:
+                qa, sa = quantize_activations(a)
+            y = out if out is not None else torch.empty((M, self.w.N), dtype=torch.bfloat16, device=a.device)
+            qgemm_w4a8_fp8(qa, sa, self.w.packed, self.w.scales, y, M, self.w.N, K)
         return y
 
 
@@ -568,33 +594,32 @@ class Int8Weight:
     @classmethod
     def from_bf16(cls, w, stream=None):
         K, N = w.shape
-        codes = torch.empty(K * N, dtype=torch.int8, device=w.device)
-        scales = torch.empty(N, dtype=torch.float32, device=w.device)
-        quant_weight_int8_per_channel(_bf16(w.contiguous()), K, N, codes, scales, stream)
+        with _on(stream, w):
+            codes = torch.empty(K * N, dtype=torch.int8, device=w.device)
+            scales = torch.empty(N, dtype=torch.float32, device=w.device)
+            quant_weight_int8_per_channel(_bf16(w.contiguous()), K, N, codes, scales)
         return cls(codes, scales, K, N)
 
 
 def quantize_activations_int8(a, stream=None):
     M, K = a.shape
-    q = torch.empty((M, K), dtype=torch.int8, device=a.device)
-    s = torch.empty(M, dtype=torch.float32, device=a.device)
-    quant_act_per_token_int8(_bf16(a), M, K, q, s, stream)
+    with _on(stream, a):
+        q = torch.empty((M, K), dtype=torch.int8, device=a.device)
+        s = torch.empty(M, dtype=torch.float32, device=a.device)
+        quant_act_per_token_int8(_bf16(a), M, K, q, s)
     return q, s
 
 
-class W8A8Int8Linear:
+class W8A8Int8Linear(_Scratch):
     """y = bf16(s_a s_w (qa @ qw)) with int8 codes, per-token quantization of a on every call."""
 
     def __init__(self, weight: Int8Weight):
         self.w = weight
-        self._ws = None
 
     def workspace(self, M, dynamic=False):
         need = (w8a8_dynamic_workspace_bytes if dynamic else w8a8_int8_workspace_bytes)(
             M, self.w.N, self.w.K)
-        if need and (self._ws is None or self._ws.numel() < need):
-            self._ws = torch.zeros(need, dtype=torch.uint8, device=self.w.codes.device)
-        return (self._ws, need) if need else (None, 0)
+        return self._scratch(need, self.w.codes.device)
 
     def __call__(self, a, out=None, stream=None, qa=None, sa=None):
         """Without qa / sa the activations are quantized inside the call
@@ -602,14 +627,14 @@ class W8A8Int8Linear:
         M, K = a.shape
         if K != self.w.K:
             raise ValueError(f"activation K={K} != weight K={self.w.K}")
-        y = out if out is not None else torch.empty((M, self.w.N), dtype=torch.bfloat16,
-                                                    device=a.device)
-        ws, need = self.workspace(M, dynamic=qa is None)
-        if qa is None:
-            qgemm_w8a8_int8_dynamic(_bf16(a), self.w.codes, self.w.scales, y, M, self.w.N, K, ws, need,
-                                    stream)
-        else:
-            qgemm_w8a8_int8(qa, sa, self.w.codes, self.w.scales, y, M, self.w.N, K, ws, need, stream)
+        with _on(stream, a):
+            y = out if out is not None else torch.empty((M, self.w.N), dtype=torch.bfloat16,
+                                                        device=a.device)
+            ws, need = self.workspace(M, dynamic=qa is None)
+            if qa is None:
+                qgemm_w8a8_int8_dynamic(_bf16(a), self.w.codes, self.w.scales, y, M, self.w.N, K, ws, need)
+            else:
+                qgemm_w8a8_int8(qa, sa, self.w.codes, self.w.scales, y, M, self.w.N, K, ws, need)
         return y
 
 
@@ -626,13 +651,6 @@ def _is(t, dtypes, shape, what):
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 
-
-def _on(stream, t):
-    """Context in which `stream` is the current stream (None: no change): what a helper
-    allocates then belongs to the stream that writes it, and may be freed while it runs."""
-    if stream is not None and stream.device_index != t.get_device():
-        raise ValueError("the stream belongs to another device than the tensors")
-    return torch.cuda.stream(stream)
 _CODES = {"e4m3": torch.uint8, "int8": torch.int8}
 
 
