@@ -89,3 +89,48 @@ def test_growing_on_another_stream(ops):
         torch.cuda.synchronize()
         assert torch.equal(first, want[0]) and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         del spoil
+
+
+def test_work_follows_the_given_stream(ops):
+    """Inputs that an earlier piece of work on the given stream writes are the ones that a call there reads."""
+    announce("order on the given stream")
+    Mx, Kx = 64, 4096
+    old, new = dev_bf16(synth.activations(Mx, Kx, 1)), dev_bf16(synth.activations(Mx, Kx, 2))
+    w = dev_bf16(synth.normal_bf16((Kx,), 9))
+    ids_old = torch.zeros((Mx, 4), dtype=torch.int32, device="cuda:0")
+    ids_new = torch.from_numpy(np.random.default_rng(0).integers(0, 8, (Mx, 4)).astype(np.int32)).cuda()
+    norm = ops.RMSNorm(w)
+    y = torch.empty((Mx, Kx), dtype=torch.bfloat16, device="cuda:0")
+    q, s = torch.empty((Mx, Kx), dtype=torch.uint8, device="cuda:0"), torch.empty(Mx, device="cuda:0")
+    half = torch.empty((Mx, Kx // 2), dtype=torch.bfloat16, device="cuda:0")
+
+    def raw(call, out):
+        def f(x, ids, stream):
+            out.zero_() if stream is None else None
+            call(x, stream)
+            return out
+        return f
+    calls = {
+        "norm": lambda x, ids, st: norm(x, stream=st)[0],
+        "norm quantized": lambda x, ids, st: norm.quantized(x, stream=st)[0],
+        "gated_silu": lambda x, ids, st: ops.gated_silu(x, stream=st),
+        "gated_silu_quantized": lambda x, ids, st: ops.gated_silu_quantized(x, "int8", stream=st)[0],
+        "dispatch": lambda x, ids, st: ops.MoeRouting.dispatch(ids, 8, x, stream=st)[1],
+        "rms_norm": raw(lambda x, st: ops.rms_norm(x, None, w, 1e-5, Mx, Kx, None, y, stream=st), y),
+        "rms_norm_quant": raw(lambda x, st: ops.rms_norm_quant(x, None, w, 1e-5, Mx, Kx, None, None, q, s, stream=st), q),
+        "swiglu": raw(lambda x, st: ops.swiglu(x, Mx, Kx // 2, half, stream=st), half),
+    }
+    busy, st = Busy(), torch.cuda.Stream()
+    for name, f in calls.items():
+        want = f(new, ids_new, None).clone()
+        x, ids = old.clone(), ids_old.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            busy()
+            x.copy_(new)
+            ids.copy_(ids_new)
+        got = f(x, ids, st)
+        assert not st.query(), "the work ahead was over too soon to show an order"
+        st.synchronize()
+        assert torch.equal(got, want), name
+        torch.cuda.synchronize()
