@@ -134,3 +134,32 @@ def test_work_follows_the_given_stream(ops):
         st.synchronize()
         assert torch.equal(got, want), name
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M,N,K", SPLIT)
+def test_workspace_of_a_captured_first_call(ops, M, N, K):
+    """Captured before any eager call, then used eagerly, replayed, outgrown and replayed again."""
+    announce(f"captured first call M={M} N={N} K={K}")
+    a, b = (dev_bf16(synth.activations(M, K, seed=s)) for s in (1, 2))
+    more = dev_bf16(synth.activations(128, K, seed=3))
+    for name, make in products(ops, N, K).items():
+        want_a, want_b, want_more = make()(a), make()(b), make()(more)
+        torch.cuda.synchronize()
+        lin, held = make(), a.clone()
+        graphs, outs = [], []
+        for _ in range(2):                                    # the second with the eager calls' workspace
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                outs.append(lin(held))
+            graphs.append(graph)
+            assert torch.equal(lin(b), want_b), name
+        assert torch.equal(lin(more), want_more), name        # may outgrow it
+        spoil = [torch.full((1 << 20,), 0xFF, dtype=torch.uint8, device="cuda:0") for _ in range(32)]
+        for turn in range(4):
+            held.copy_((a, b)[turn % 2])
+            for graph, out in zip(graphs, outs):
+                graph.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(out, (want_a, want_b)[turn % 2]), f"{name} replay {turn}"
+                assert torch.equal(lin(b), want_b), name
+        del spoil

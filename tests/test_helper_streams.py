@@ -6,6 +6,7 @@ recorders of the stream that is current when they are called.
 import contextlib
 import os
 import types
+import weakref
 
 import pytest
 import torch
@@ -104,3 +105,25 @@ def test_outgrown_workspace_waits_for_the_calls_before(recorded, monkeypatch):
     monkeypatch.setattr(ops, "w4a16_workspace_bytes", lambda *a: 4096)
     lin(bf(M, K), stream=GIVEN)
     assert told == [(1024, "given")]
+
+
+def test_workspace_of_a_capture(recorded, monkeypatch):
+    """A capture's clearing runs in its replays only: a buffer that the capture brought is not kept for other calls.
+    One that it found stays alive when later calls outgrow it."""
+    ops, events = recorded
+    capturing, need = [True], [1024]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(ops, "w4a16_workspace_bytes", lambda *a: need[0])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    lin = ops.W4A16Linear(ops.Int4G128Weight(bf(1), bf(1), K, N))
+    first, _ = lin.workspace(M)
+    capturing[0] = False
+    del events[:]
+    held, _ = lin.workspace(M)
+    assert held is not first and events == [("zeros", "current")]
+    capturing[0] = True
+    assert lin.workspace(M)[0] is held
+    capturing[0], need[0] = False, 4096
+    alive = weakref.ref(held)
+    del held
+    assert lin.workspace(M)[0].numel() == 4096 and alive() is not None

@@ -364,17 +364,27 @@ class _Scratch:
     """A workspace kept from call to call, for calls that do not overlap in time."""
 
     _ws = None
+    _captured = False            # a captured graph uses _ws
+    _outgrown = ()               # buffers that captured graphs go on using
 
-    def _scratch(self, need, device, alloc=torch.zeros):
+    def _scratch(self, need, device, cleared=True):
         """(buffer, need), or (None, 0) if nothing is needed.  A new buffer comes from the
         current stream; a call on another stream follows the one that brought it."""
         if not need:
             return None, 0
+        alloc = torch.zeros if cleared else torch.empty
+        capturing = torch.cuda.is_current_stream_capturing()
         if self._ws is None or self._ws.numel() * self._ws.element_size() < need:
-            if self._ws is not None:
+            if capturing:
+                # the graph's own, cleared in every replay: kept, it would not be cleared until the first one
+                return alloc(need, dtype=torch.uint8, device=device), need
+            if self._captured:
+                self._outgrown += (self._ws,)
+            elif self._ws is not None:
                 # the last calls may have used it on another stream than its own; this call follows them
                 self._ws.record_stream(torch.cuda.current_stream(device))
-            self._ws = alloc(need, dtype=torch.uint8, device=device)
+            self._ws, self._captured = alloc(need, dtype=torch.uint8, device=device), False
+        self._captured |= capturing
         return self._ws, need
 
 
@@ -503,7 +513,7 @@ class GroupedInt4Weight(_Scratch):
             raise ValueError("grouped GEMM: activation K or offsets do not match the weights")
         with _on(stream, a):
             y = out if out is not None else torch.empty((T, self.N), dtype=torch.bfloat16, device=a.device)
-            ws, need = self._scratch(w4a16_grouped_workspace_bytes(self.E, T, self.N, K), a.device, torch.empty)
+            ws, need = self._scratch(w4a16_grouped_workspace_bytes(self.E, T, self.N, K), a.device, cleared=False)
             qgemm_w4a16_grouped(_bf16(a), offsets, self.packed, self.scales, y, self.E, T, self.N, K, ws, need)
         return y
 
@@ -514,7 +524,7 @@ class GroupedInt4Weight(_Scratch):
             raise ValueError("grouped GEMM: activation K or offsets do not match the weights")
         with _on(stream, qa):
             y = out if out is not None else torch.empty((T, self.N), dtype=torch.bfloat16, device=qa.device)
-            ws, need = self._scratch(w4a16_grouped_workspace_bytes(self.E, T, self.N, K), qa.device, torch.empty)
+            ws, need = self._scratch(w4a16_grouped_workspace_bytes(self.E, T, self.N, K), qa.device, cleared=False)
             qgemm_w4a8_fp8_grouped(qa, sa, offsets, self.packed, self.scales, y, self.E, T, self.N, K, ws, need)
         return y
 
@@ -525,7 +535,7 @@ class GroupedInt4Weight(_Scratch):
             raise ValueError("grouped GEMM: activation K or offsets do not match the weights")
         with _on(stream, a):
             y = out if out is not None else torch.empty((T, self.N), dtype=torch.bfloat16, device=a.device)
-            ws, need = self._scratch(w4a8_grouped_dynamic_workspace_bytes(self.E, T, self.N, K), a.device, torch.empty)
+            ws, need = self._scratch(w4a8_grouped_dynamic_workspace_bytes(self.E, T, self.N, K), a.device, cleared=False)
             qgemm_w4a8_fp8_grouped_dynamic(_bf16(a), offsets, self.packed, self.scales, y, self.E, T, self.N, K, ws, need)
         return y
 
