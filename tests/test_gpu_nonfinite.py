@@ -1,0 +1,56 @@
+"""Values that overflowed or went wrong further up stay visible: an activation or
+a coded output never turns them into ordinary numbers.
+
+Finite inputs reach all of these: a product's fp32 accumulators overflow, and so
+do x + residual and silu(gate) * up.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import announce, dev_bf16, host_bits16
+from oracle import int4_g128 as q4
+from oracle.bf16 import bf16_bits_to_f32, f32_to_bf16_bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    from weight_only_quantized_w4a16_amd import ops as _ops
+    return _ops
+
+
+# a decode kernel of one and of several waves a tile, its K split, the small-M
+# kernel of one, two and four row tiles, the large one with and without a K split
+PRODUCTS = [(3, 8256, 1024), (1, 256, 4096), (16, 1024, 14336), (9, 528, 1280), (17, 512, 512), (40, 1040, 1024),
+            (100, 4096, 4096), (130, 14336, 256), (520, 14336, 256)]
+
+
+def overflowing(ops, M, N, K, act):
+    """(y, kind): rows of kind 0 add 1.4e37 to a bias of +-3.38e38, rows of kind 1 subtract it; even columns have the
+    positive bias.  In rows of kind 2 two groups' fp32 sums overflow with opposite signs."""
+    codes = np.full((K, N), 8, np.uint8)                             # zero weights but in the first two groups
+    codes[:128], codes[128:256] = 15, 1                              # 7 and -7 times the scale
+    scales = np.full((K // 128, N), f32_to_bf16_bits(np.float32(2e36)), np.uint16)
+    packed, scales = q4.pack_native(codes, scales)
+    w = ops.Int4G128Weight(torch.from_numpy(packed.view(np.int32)).cuda(), torch.from_numpy(scales.view(np.int16)).cuda(), K, N)
+    kind = np.arange(M) % 3 if M > 2 else np.full(M, 2)
+    a = np.zeros((M, K), np.float32)
+    a[kind == 0, 5] = 1.0
+    a[kind == 1, 200] = 1.0
+    a[kind == 2, 5] = a[kind == 2, 200] = 3e38
+    bias = np.where(np.arange(N) % 2 == 0, 3.38e38, -3.38e38).astype(np.float32)
+    y = ops.W4A16Linear(w, dev_bf16(f32_to_bf16_bits(bias)), act)(dev_bf16(f32_to_bf16_bits(a)))
+    torch.cuda.synchronize()
+    return bf16_bits_to_f32(host_bits16(y)), kind
+
+
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+def test_relu_keeps_nan(ops, M, N, K):
+    announce(f"relu of nan M={M} N={N} K={K} {ops.w4a16_kernel_for(M, N, K)}")
+    y, kind = overflowing(ops, M, N, K, "relu")
+    assert np.isnan(y[kind == 2]).all()
+    assert np.isposinf(y[kind == 0][:, ::2]).all() and not y[kind == 0][:, 1::2].any()
+    assert not y[kind == 1][:, 1::2].any() and np.isfinite(y[kind == 1][:, ::2]).all()

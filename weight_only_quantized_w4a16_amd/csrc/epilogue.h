@@ -72,8 +72,9 @@ template <int C, class V>
 __device__ __forceinline__ void activate(V& v, int act) {
     switch (act) {                               // uniform: one branch for all C values
         case ACT_RELU:
+            // the maximum that keeps NaN: sums that overflowed with both signs stay visible
 #pragma unroll
-            for (int i = 0; i < C; ++i) v[i] = fmaxf(v[i], 0.0f);
+            for (int i = 0; i < C; ++i) v[i] = __builtin_elementwise_maximum(v[i], 0.0f);
             break;
         case ACT_GELU:
 #pragma unroll
