@@ -54,3 +54,14 @@ def test_relu_keeps_nan(ops, M, N, K):
     assert np.isnan(y[kind == 2]).all()
     assert np.isposinf(y[kind == 0][:, ::2]).all() and not y[kind == 0][:, 1::2].any()
     assert not y[kind == 1][:, 1::2].any() and np.isfinite(y[kind == 1][:, ::2]).all()
+
+
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_activations_of_infinity(ops, M, N, K, act):
+    """act(+inf) = +inf, act(nan) = nan; far below zero the result is a zero (at -inf: nan, infinity times zero)."""
+    announce(f"{act} of infinity M={M} N={N} K={K}")
+    y, kind = overflowing(ops, M, N, K, act)
+    assert np.isnan(y[kind == 2]).all()
+    assert np.isposinf(y[kind == 0][:, ::2]).all() and not y[kind == 0][:, 1::2].any()
+    assert np.isfinite(y[kind == 1][:, ::2]).all() and not np.nan_to_num(y[kind == 1][:, 1::2]).any()

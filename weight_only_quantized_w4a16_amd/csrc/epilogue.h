@@ -62,10 +62,11 @@ __device__ __forceinline__ float x_phi(float x) {
     p = fmaf(p, t, 0.103921967f);
     p = fmaf(p, t, 0.11283476f);
     p = fmaf(p, t, 0.112837932f);
-    // past |x| = 2^63 the square would overflow: the tail is zero long before
+    // past |x| = 2^63 the square would overflow: the tail is zero from 20 on, where
+    // b also keeps +inf from meeting it (-inf times zero stays NaN)
     const float b = fminf(a, 20.0f);
     const float tail = p * t * __builtin_amdgcn_exp2f(-0.721347520f * b * b);
-    return x < 0.0f ? x * tail : fmaf(-x, tail, x);
+    return x < 0.0f ? x * tail : fmaf(-b, tail, x);
 }
 
 template <int C, class V>
