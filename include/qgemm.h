@@ -465,7 +465,9 @@ qg_status qgemm_w8a8_int8_dynamic(const uint16_t *a_bf16, const int8_t *w_i8,
  *   y_e4m3 / y_i8  out  [M, K] codes of y, y_scale out [M]: s = max|y| / 448
  *                  (/ 127) in IEEE fp32, codes rnd(y / s) of the fp32 quotient
  *                  (to one unit in its last place), saturated at the largest
- *                  code; a zero row gives s = 0 and codes 0.
+ *                  code; a zero row gives s = 0 and codes 0.  A row of y that
+ *                  overflowed or holds a NaN has an infinite or NaN scale, so
+ *                  the products that read it are infinite or NaN as well.
  *   y_bf16         out  [M, K] y as bf16 too (a router reads it), or NULL.
  */
 qg_status rms_norm(const uint16_t *x_bf16, const uint16_t *residual_bf16,

@@ -65,3 +65,62 @@ def test_activations_of_infinity(ops, M, N, K, act):
     assert np.isnan(y[kind == 2]).all()
     assert np.isposinf(y[kind == 0][:, ::2]).all() and not y[kind == 0][:, 1::2].any()
     assert np.isfinite(y[kind == 1][:, ::2]).all() and not np.nan_to_num(y[kind == 1][:, 1::2]).any()
+
+
+FORMATS = {"e4m3": ("_quant", torch.uint8), "int8": ("_quant_int8", torch.int8)}
+# parts of a wave, a wave, workgroups, the long kernel; more rows: one wave a row up to 2048 columns
+ROWS = [(6, 8), (6, 72), (6, 256), (6, 512), (6, 1024), (6, 2056), (6, 14336), (6, 32776), (1100, 1536)]
+
+
+def coded(ops, op, fmt, *args):
+    M, K = args[-2:]
+    q, s = torch.empty((M, K), dtype=FORMATS[fmt][1], device="cuda:0"), torch.empty(M, device="cuda:0")
+    extra = (None, None) if op == "rms_norm" else ()
+    getattr(ops, op + FORMATS[fmt][0])(*args, *extra, q, s)
+    torch.cuda.synchronize()
+    return q.cpu().numpy(), s.cpu().numpy()
+
+
+def check_coded(got, clean, bad):
+    """The scales of the rows in `bad` are no numbers or infinite; the other rows are as without them."""
+    (q, s), (q0, s0) = got, clean
+    good = np.setdiff1d(np.arange(s.size), bad)
+    assert not np.isfinite(s[bad]).any(), s[bad]
+    assert np.array_equal(q[good], q0[good]) and np.array_equal(s[good], s0[good]) and np.isfinite(s[good]).all()
+
+
+@pytest.mark.parametrize("M,I", ROWS)
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_swiglu_codes(ops, M, I, fmt):
+    announce(f"swiglu codes of non-finite rows M={M} I={I} {fmt}")
+    rng = np.random.default_rng(I)
+    gu = rng.standard_normal((M, 2 * I)).astype(np.float32)
+    clean = coded(ops, "swiglu", fmt, dev_bf16(f32_to_bf16_bits(gu)), M, I)
+    c = rng.integers(0, I, 4)
+    gu[0, I + c[0]] = np.nan
+    gu[1, c[1]] = np.nan
+    gu[3, :] = np.nan
+    gu[4, c[2]] = gu[4, I + c[2]] = 3e38                             # their product overflows
+    gu[5, c[3]], gu[5, I + c[3]] = np.inf, 0.0
+    got = coded(ops, "swiglu", fmt, dev_bf16(f32_to_bf16_bits(gu)), M, I)
+    check_coded(got, clean, np.array([0, 1, 3, 4, 5]))
+
+
+@pytest.mark.parametrize("M,K", ROWS)
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_rms_norm_codes(ops, M, K, fmt):
+    announce(f"norm codes of non-finite rows M={M} K={K} {fmt}")
+    rng = np.random.default_rng(K)
+    x, r = (rng.standard_normal((M, K)).astype(np.float32) for _ in range(2))
+    w = dev_bf16(f32_to_bf16_bits(rng.standard_normal(K).astype(np.float32)))
+    run = lambda w: coded(ops, "rms_norm", fmt, *(dev_bf16(f32_to_bf16_bits(v)) for v in (x, r)), w, 1e-5, M, K)
+    clean = run(w)
+    c = rng.integers(0, K, 3)
+    x[0, c[0]] = np.nan
+    x[2, :] = np.nan
+    x[3, c[1]] = r[3, c[1]] = 3e38                                   # their sum overflows
+    r[5, c[2]] = -np.inf
+    check_coded(run(w), clean, np.array([0, 2, 3, 5]))
+    w[K // 2] = float("nan")                                         # a weight that is no number: in every row
+    q, s = run(w)
+    assert not np.isfinite(s).any()

@@ -5,7 +5,8 @@
 //
 //   rms_norm   h = x + residual, y = (h * rsqrt(mean(h^2) + eps)) * weight
 //   swiglu     y = gate / (1 + exp(-gate)) * up
-//   codes      s = max|y| / q_max (IEEE), q = rnd(y / s); a zero row: s = 0, q = 0
+//   codes      s = max|y| / q_max (IEEE), q = rnd(y / s); a zero row: s = 0, q = 0;
+//              a row with a NaN: s is NaN; with an infinity: infinite or NaN
 //
 // Everything between the bf16 inputs and the output is fp32 (the sum of squares
 // fp64): y is rounded once, to bf16 or to its code, and h (stored as bf16)
@@ -61,7 +62,7 @@ template <int NT>
 __device__ __forceinline__ float lanes_max(float v) {
     if constexpr (NT >= 64) return wave_max_abs(v);
 #pragma unroll
-    for (int o = NT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    for (int o = NT / 2; o > 0; o >>= 1) v = max_abs(v, __shfl_xor(v, o, 64));
     return v;
 }
 template <int NT>
@@ -84,7 +85,7 @@ __device__ __forceinline__ float row_max(float v, float* red) {
         __syncthreads();
         v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < NT / 64; ++w) v = fmaxf(v, red[w]);
+        for (int w = 0; w < NT / 64; ++w) v = max_abs(v, red[w]);
     }
     return v;
 }
@@ -104,7 +105,7 @@ __device__ __forceinline__ void row_sum_max(double& sum, float& top, double* red
 #pragma unroll
         for (int w = 0; w < NT / 64; ++w) {
             sum += red_sum[w];
-            top = fmaxf(top, red_max[w]);
+            top = max_abs(top, red_max[w]);
         }
     }
 }
@@ -180,7 +181,7 @@ __device__ __forceinline__ float rstd_of(double sum, double inv_K, float eps) {
 
 // The scale needs max |h rstd w|.  max |h w| is known before rstd, so both
 // reductions share one barrier, and the maximum is that times rstd; a row whose
-// |h w| leaves the middle of fp32's range reduces once more.
+// |h w| leaves the middle of fp32's range, or holds a NaN, reduces once more.
 template <class Fmt, int NT, int CPT>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs p) {
     constexpr int NW = NT < 256 ? 4 : NT / 64;
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
             float f[8];
             unpack8(wv[i], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j] * f[j]));
+            for (int j = 0; j < 8; ++j) top = max_abs(top, v[i][j] * f[j]);
         }
     }
     if constexpr (kCodes<Fmt>) row_sum_max<NT>(sum, top, red_sum, red_max[0]);
@@ -257,7 +258,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
 #pragma unroll
             for (int i = 0; i < CPT; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j]));
+                for (int j = 0; j < 8; ++j) top = max_abs(top, v[i][j]);
             top = row_max<NT>(top, red_max[1]);
         }
         const RowScale sc = RowScale::of<Fmt>(top);
@@ -312,7 +313,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs p) {
             load(c, v);
             norm(c, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+            for (int j = 0; j < 8; ++j) amax = max_abs(amax, v[j]);
         }
         sc = RowScale::of<Fmt>(row_max<NT>(amax, red_max));
         if (tid == 0) p.s[m] = sc.s;
@@ -445,7 +446,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void swiglu_quant_kernel(Swigl
     for (int i = 0; i < CPT; ++i) {
         swiglu8(g[i], u[i], y[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[i][j]));
+        for (int j = 0; j < 8; ++j) amax = max_abs(amax, y[i][j]);
     }
     const RowScale sc = RowScale::of<Fmt>(row_max<NT>(amax, red));
     if (tid == 0) p.s[m] = sc.s;
@@ -468,7 +469,7 @@ __global__ __launch_bounds__(1024) void swiglu_quant_long_kernel(SwigluArgs p) {
         float y[8];
         swiglu8(gate[c], gate[chunks + c], y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
+        for (int j = 0; j < 8; ++j) amax = max_abs(amax, y[j]);
     }
     const RowScale sc = RowScale::of<Fmt>(row_max<NT>(amax, red));
     if (threadIdx.x == 0) p.s[m] = sc.s;

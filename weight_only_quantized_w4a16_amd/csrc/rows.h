@@ -84,15 +84,18 @@ __device__ __forceinline__ T wave_sum(T v) {
     v += dpp<0x143, 0xc>(v);
     return lane63(v);
 }
-// The largest of non-negative values.
-__device__ __forceinline__ float wave_max_abs(float v) {
-    v = fmaxf(v, dpp<0x111>(v));
-    v = fmaxf(v, dpp<0x112>(v));
-    v = fmaxf(v, dpp<0x114>(v));
-    v = fmaxf(v, dpp<0x118>(v));
-    v = fmaxf(v, dpp<0x142, 0xa>(v));
-    v = fmaxf(v, dpp<0x143, 0xc>(v));
-    return lane63(v);
+// The largest magnitude; a NaN counts as larger than any number and stays one.
+__device__ __forceinline__ float max_abs(float a, float b) { return __builtin_elementwise_maximum(a, fabsf(b)); }
+// Over the wave's lanes, for a >= 0 or NaN: their bits order as the values do.
+__device__ __forceinline__ float wave_max_abs(float a) {
+    uint32_t u = __float_as_uint(a) & 0x7fffffffu;
+    u = max(u, dpp_u32<0x111>(0u, u));
+    u = max(u, dpp_u32<0x112>(0u, u));
+    u = max(u, dpp_u32<0x114>(0u, u));
+    u = max(u, dpp_u32<0x118>(0u, u));
+    u = max(u, dpp_u32<0x142, 0xa>(0u, u));
+    u = max(u, dpp_u32<0x143, 0xc>(0u, u));
+    return lane63(__uint_as_float(u));
 }
 
 }  // namespace qg
