@@ -2,7 +2,8 @@
 with the operators that stand between two such layers of a decoder block.
 
 The compute lives in the HIP library libqgemm.so (C ABI declared in
-include/qgemm.h); `ops` is a thin ctypes binding with the same entry-point
-names.  Import `weight_only_quantized_w4a16_amd.ops` to load the library.
+include/qgemm.h); `ops` is a thin binding with the same entry-point names, by
+ctypes for the products and by the compiled extension _calls for the operators
+between them.  Import `weight_only_quantized_w4a16_amd.ops` to load the library.
 """
 __all__ = ["ops", "synth"]

@@ -1,5 +1,8 @@
-"""Build libqgemm.so in-tree with hipcc for gfx950, and _calls.so, the binding's
-call marshalling (host code against the installed torch's headers).
+"""Build libqgemm.so in-tree with hipcc for gfx950, and the _calls extension, the
+binding's call marshalling (host code against the installed torch's headers; its
+file name carries the interpreter's ABI, the module the torch it was built with).
+The library is there also when the extension cannot be built; the reason is raised
+after it.
 
     python -m weight_only_quantized_w4a16_amd.build
 
@@ -9,6 +12,7 @@ csrc/_build/, the libraries to the package directory.
 import concurrent.futures
 import importlib.util
 import os
+import runpy
 import subprocess
 import sys
 import sysconfig
@@ -18,7 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(CSRC, "_build")
 LIB = os.path.join(PKG, "libqgemm.so")
-CALLS = os.path.join(PKG, "_calls.so")
+CALLS = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["abi.cpp", "abi_block.cpp", "w4a16.hip", "fp8.hip", "w4a8.hip", "norm.hip", "moe.hip"]
 ARCH = "gfx950"
 
@@ -50,8 +54,10 @@ def _compile(src):
 def _build_calls():
     torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     lib = os.path.join(torch, "lib")
+    version = runpy.run_path(os.path.join(torch, "version.py"))["__version__"]
     tmp = CALLS + ".tmp"
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f'-DQG_TORCH_VERSION="{version}"',
            "-I", os.path.join(torch, "include"), "-I", os.path.join(ROCM, "include"),
            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "calls.cpp"),
            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
@@ -67,7 +73,6 @@ def build(verbose=True):
     with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
         calls = ex.submit(_build_calls)
         results = list(ex.map(_compile, SOURCES))
-        calls.result()
     objs = [o for o, _ in results]
     if verbose:
         for (_, w), src in zip(results, SOURCES):
@@ -81,6 +86,8 @@ def build(verbose=True):
     os.replace(tmp, LIB)
     if verbose:
         print(f"built {LIB}")
+    calls.result()
+    if verbose:
         print(f"built {CALLS}")
     return LIB
 

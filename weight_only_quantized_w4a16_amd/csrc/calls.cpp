@@ -273,4 +273,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "Call marshalling of ops.
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&module); }
+// torch_version: the torch whose headers this was built with
+PyMODINIT_FUNC PyInit__calls(void) {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", QG_TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

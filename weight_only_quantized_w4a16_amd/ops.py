@@ -3,8 +3,9 @@
 Argument marshalling only: every step of the computation runs in the HIP
 library.  Functions take torch tensors on the GPU, pass their device pointers
 and torch's current HIP stream, and raise QGemmError on a non-zero status.
-There is no fallback: if libqgemm.so or _calls.so (the compiled marshalling of
-the block operators' calls) is missing, importing this module raises.
+There is no fallback: if libqgemm.so is missing, importing this module raises; if
+the _calls extension (the compiled marshalling of the calls that stand between two
+products) is missing or belongs to another torch, those calls raise.
 
 bf16 data travels as torch.bfloat16 (or int16 / uint16 bit patterns) tensors;
 e4m3 codes as torch.uint8 (or torch.float8_e4m3fn) tensors.
@@ -18,15 +19,34 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqgemm.so")
 
-for _path in (LIB_PATH, os.path.join(_PKG, "_calls.so")):
-    if not os.path.exists(_path):
-        raise ImportError(
-            f"{_path} is not built; run `python -m weight_only_quantized_w4a16_amd.build` "
-            "(hipcc, gfx950)")
+_BUILD = "run `python -m weight_only_quantized_w4a16_amd.build`"
+
+if not os.path.exists(LIB_PATH):
+    raise ImportError(f"{LIB_PATH} is not built; {_BUILD} (hipcc, gfx950)")
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _calls  # noqa: E402  (call marshalling of the block operators; built beside the library)
+
+class _NoCalls:
+    """In the place of _calls where that cannot be used: every call through it raises."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name}: the compiled call marshalling cannot be used ({self._why}); {_BUILD}")
+
+    def __dir__(self):
+        return []
+
+
+try:
+    from . import _calls                     # built beside the library
+    _built_with = getattr(_calls, "torch_version", "unknown")
+    if _built_with != torch.__version__:
+        _calls = _NoCalls(f"built with torch {_built_with}, this is {torch.__version__}")
+except ImportError as _e:
+    _calls = _NoCalls(str(_e))
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
