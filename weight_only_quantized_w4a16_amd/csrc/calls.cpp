@@ -88,6 +88,17 @@ private:
     int dev_ = -1;
 };
 
+// Lets other Python threads run: a launch may wait for room in the device's queue.
+class WithoutLock {
+public:
+    WithoutLock() : state_(PyEval_SaveThread()) {}
+    ~WithoutLock() { PyEval_RestoreThread(state_); }
+    WithoutLock(const WithoutLock&) = delete;
+
+private:
+    PyThreadState* state_;
+};
+
 // Makes the tensors' device current for one call.
 class OnDevice {
 public:
@@ -101,6 +112,13 @@ public:
 private:
     int before_ = 0;
     bool moved_ = false;
+};
+
+// Everything around the library's call once its arguments are known.
+struct Launch {
+    explicit Launch(int dev) : on(dev) {}
+    WithoutLock lock;
+    OnDevice on;
 };
 
 #define QG_CALLS(X)                                                                                              \
@@ -160,7 +178,7 @@ PyObject* norm(PyObject* const* a, Py_ssize_t n, F f) {
         const int M = g.integer(), K = g.integer();
         const Address h{g.tensor()}, y{g.tensor()}, q{g.tensor()}, s{g.tensor()};
         const qg_stream st = g.stream();
-        const OnDevice on(g.device());
+        const Launch launch(g.device());
         return f(x, r, w, eps, M, K, h, y, q, s, st);
     });
 }
@@ -171,7 +189,7 @@ PyObject* py_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int M = g.integer(), K = g.integer();
         const Address h{g.tensor()}, y{g.tensor()};
         const qg_stream st = g.stream();
-        const OnDevice on(g.device());
+        const Launch launch(g.device());
         return lib.rms_norm(x, r, w, eps, M, K, h, y, st);
     });
 }
@@ -187,7 +205,7 @@ PyObject* gated(PyObject* const* a, Py_ssize_t n, F f) {
         const int M = g.integer(), I = g.integer();
         const Address q{g.tensor()}, s{g.tensor()};
         const qg_stream st = g.stream();
-        const OnDevice on(g.device());
+        const Launch launch(g.device());
         return f(gu, M, I, q, s, st);
     });
 }
@@ -197,7 +215,7 @@ PyObject* py_swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int M = g.integer(), I = g.integer();
         const Address y{g.tensor()};
         const qg_stream st = g.stream();
-        const OnDevice on(g.device());
+        const Launch launch(g.device());
         return lib.swiglu(gu, M, I, y, st);
     });
 }
@@ -213,7 +231,7 @@ PyObject* py_qgemm_w4a16_epilogue(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Address ws{g.tensor()};
         const size_t bytes = g.size();
         const qg_stream st = g.stream();
-        const OnDevice on(g.device());
+        const Launch launch(g.device());
         return lib.qgemm_w4a16_epilogue(x, w, sc, b, act, r, y, M, N, K, ws, bytes, st);
     });
 }
@@ -225,7 +243,7 @@ PyObject* py_moe_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Address offsets{g.tensor()}, row{g.tensor()}, out{g.tensor()}, scale_out{g.tensor()}, ws{g.tensor()};
         const size_t bytes = g.size();
         const qg_stream st = g.stream();
-        const OnDevice on(g.device());
+        const Launch launch(g.device());
         return lib.moe_dispatch(ids, rows, scale, B, k, E, width, offsets, row, out, scale_out, ws, bytes, st);
     });
 }
@@ -235,7 +253,7 @@ PyObject* py_moe_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int B = g.integer(), k = g.integer(), width = g.integer();
         const Address out{g.tensor()}, scale_out{g.tensor()};
         const qg_stream st = g.stream();
-        const OnDevice on(g.device());
+        const Launch launch(g.device());
         return lib.moe_gather(rows, scale, row, B, k, width, out, scale_out, st);
     });
 }
@@ -245,7 +263,7 @@ PyObject* py_moe_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int B = g.integer(), k = g.integer(), K = g.integer();
         const Address y{g.tensor()};
         const qg_stream st = g.stream();
-        const OnDevice on(g.device());
+        const Launch launch(g.device());
         return lib.moe_combine(rows, row, w, res, B, k, K, y, st);
     });
 }
@@ -255,7 +273,7 @@ PyObject* py_moe_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int B = g.integer(), k = g.integer(), K = g.integer();
         const Address drows{g.tensor()}, dw{g.tensor()};
         const qg_stream st = g.stream();
-        const OnDevice on(g.device());
+        const Launch launch(g.device());
         return lib.moe_combine_backward(dy, rows, row, w, B, k, K, drows, dw, st);
     });
 }
