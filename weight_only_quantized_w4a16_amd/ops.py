@@ -15,6 +15,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqgemm.so")
@@ -750,9 +751,54 @@ def gated_silu_quantized(gate_up, fmt="e4m3", stream=None):
     return q, s
 
 
+def _differentiable(*tensors):
+    """Whether torch records a gradient for one of the tensors (None: no tensor)."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+class _Combine(torch.autograd.Function):
+    """MoeRouting.combine with the gradients of rows, weights and residual."""
+
+    @staticmethod
+    def forward(ctx, rows, weights, residual, routing):
+        ctx.routing = routing
+        ctx.save_for_backward(rows if ctx.needs_input_grad[1] else None, weights)
+        return routing._combine(rows, weights, residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        rows, weights = ctx.saved_tensors
+        r, dy = ctx.routing, dy.contiguous()
+        of_rows, of_weights, of_residual, _ = ctx.needs_input_grad
+        # rows of no slot take part in nothing: their gradient is zero
+        drows = torch.zeros((r.B * r.k, dy.shape[1]), dtype=dy.dtype, device=dy.device) if of_rows else None
+        dw = torch.empty_like(weights) if of_weights else None
+        if of_rows or of_weights:
+            moe_combine_backward(dy, rows, r.row_of_slot, weights, r.B, r.k, dy.shape[1], drows, dw)
+        return drows, dw, dy if of_residual else None, None
+
+
+class _Gather(torch.autograd.Function):
+    """The rows of MoeRouting.gather; their gradient is combine without weights."""
+
+    @staticmethod
+    def forward(ctx, rows, routing):
+        ctx.routing = routing
+        return routing._gather(rows, None)[0]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, drows):
+        return ctx.routing._combine(drows.contiguous(), None, None), None
+
+
 class MoeRouting:
     """The slots of B tokens with k experts each, sorted by expert: `offsets` int32
-    [E + 1] for the grouped products and `row_of_slot` int32 [B, k] (-1: no row)."""
+    [E + 1] for the grouped products and `row_of_slot` int32 [B, k] (-1: no row).
+
+    dispatch and gather carry gradients of bf16 rows, combine those of rows, weights and
+    residual, where torch records them (a router trains over frozen experts)."""
 
     def __init__(self, offsets, row_of_slot):
         self.offsets, self.row_of_slot = offsets, row_of_slot
@@ -767,6 +813,10 @@ class MoeRouting:
         _is(expert_ids, (torch.int32,), (B, k), "expert_ids")
         if E < 1:
             raise ValueError(f"E must be positive, got {E}")
+        if _differentiable(rows):
+            with _on(stream, expert_ids):
+                routing = cls.dispatch(expert_ids, E)[0]
+                return (routing, *routing.gather(rows, row_scale))
         dev = expert_ids.device
         with _on(stream, expert_ids):
             offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
@@ -792,12 +842,19 @@ class MoeRouting:
             scale_out = torch.empty(B * k, dtype=torch.float32, device=rows.device)
         return out, scale_out, rows.shape[1] * rows.element_size()
 
+    def _gather(self, rows, row_scale):
+        out, scale_out, width = self._rows_out(rows, row_scale, self.B, self.k)
+        moe_gather(rows, row_scale, self.row_of_slot, self.B, self.k, width, out, scale_out)
+        return out, scale_out
+
     def gather(self, rows, row_scale=None, stream=None):
         """(rows [B k, K], scales or None): another tensor's rows in the routed order."""
         with _on(stream, rows):
-            out, scale_out, width = self._rows_out(rows, row_scale, self.B, self.k)
-            moe_gather(rows, row_scale, self.row_of_slot, self.B, self.k, width, out, scale_out)
-        return out, scale_out
+            if not _differentiable(rows):
+                return self._gather(rows, row_scale)
+            if rows.dtype != torch.bfloat16 or row_scale is not None:
+                raise TypeError("gradients of routed rows are those of bf16 rows without scales; detach others")
+            return _Gather.apply(rows, self), None
 
     def _weights(self, weights):
         return None if weights is None else _is(weights, (torch.float32,), (self.B, self.k), "weights")
@@ -810,9 +867,17 @@ class MoeRouting:
         if residual is not None:
             _is(residual, _BF16, (self.B, K), "residual")
         with _on(stream, rows):
-            y = _is(out, _BF16, (self.B, K), "out") if out is not None else \
-                torch.empty((self.B, K), dtype=torch.bfloat16, device=rows.device)
-            moe_combine(rows, self.row_of_slot, self._weights(weights), residual, self.B, self.k, K, y)
+            if not _differentiable(rows, weights, residual):
+                return self._combine(rows, weights, residual, out)
+            if out is not None:
+                raise RuntimeError("combine(out=...) carries no gradient; leave out= or detach its inputs")
+            return _Combine.apply(rows, weights, residual, self)
+
+    def _combine(self, rows, weights, residual, out=None):
+        K = rows.shape[1]
+        y = _is(out, _BF16, (self.B, K), "out") if out is not None else \
+            torch.empty((self.B, K), dtype=torch.bfloat16, device=rows.device)
+        moe_combine(rows, self.row_of_slot, self._weights(weights), residual, self.B, self.k, K, y)
         return y
 
     def combine_backward(self, dy, rows, weights=None, stream=None):
