@@ -485,7 +485,8 @@ qg_status rms_norm_quant_int8(const uint16_t *x_bf16, const uint16_t *residual_b
 /*
  * swiglu -- y[m, i] = silu(gate_up[m, i]) * gate_up[m, I + i], silu(g) =
  * g / (1 + exp(-g)): the gated unit on the output of a fused gate_up product.
- *   gate_up_bf16  in   [M, 2 I], the gate in the first I columns (I % 8 == 0).
+ *   gate_up_bf16  in   [M, 2 I], the gate in the first I columns (I % 8 == 0);
+ *                 swiglu: M I <= 2^35 - 2048.
  *   y_bf16        out  [M, I]; or, for swiglu_quant and swiglu_quant_int8, codes
  *                 and y_scale as those of rms_norm_quant.
  */

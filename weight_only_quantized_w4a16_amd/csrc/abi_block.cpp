@@ -14,6 +14,7 @@ namespace {
 // Row operators launch up to 1024 threads a row and expert ones 256 a 256-piece
 // part of a token's row; a dispatch holds fewer than 2^32 threads.
 constexpr int64_t kMaxRows = (int64_t(1) << 22) - 1;
+constexpr int64_t kMaxGatedElems = (int64_t(1) << 35) - 2048;
 constexpr int64_t kMaxSlots = int64_t(1) << 24;          // routed rows
 constexpr int kMaxChoices = 1024;                        // experts of one token
 
@@ -45,6 +46,8 @@ qg_status norm(const uint16_t* x, const uint16_t* r, const uint16_t* w, float ep
 
 qg_status gated(const uint16_t* gu, int M, int I, uint16_t* y, void* q, float* s, ActFormat fmt, qg_stream stream) {
     if (!rows_ok(M, I)) return QG_ERR_SHAPE;
+    // the bf16 output's launch: a thread per eight elements, 256 a workgroup
+    if (fmt == ActFormat::bf16 && int64_t(M) * I > kMaxGatedElems) return QG_ERR_SHAPE;
     if (M == 0) return QG_OK;
     if (!gu || (fmt == ActFormat::bf16 ? !y : !q || !s)) return QG_ERR_NULL;
     if (!aligned(gu, 16) || !aligned(y, 16) || !aligned(q, 16) || !aligned(s, 4)) return QG_ERR_ALIGN;
