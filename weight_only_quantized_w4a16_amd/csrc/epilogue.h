@@ -98,6 +98,7 @@ template <bool RES, bool ACT>
 struct Epilogue {
     using out_ptr = uint16_t*;
     static constexpr bool kActive = true;
+    static constexpr bool kResidual = RES, kActivation = ACT;
     const uint16_t* bias;                        // [N] or null
     const uint16_t* residual;                    // [M, N], read if RES
     int act;                                     // qg_activation, looked at if ACT

@@ -769,9 +769,9 @@ constexpr int LM_BM = 128;
 // eight consecutive columns of a row instead, so bias, residual and output move
 // 16 bytes at a time and a result costs about five instructions beside its
 // activation.  No other work covers a tile's end (LDS holds one workgroup per
-// CU), so its instructions count: 1000 x 4096 x 14336 with a bias takes 120 us, with
-// gelu 125, and took 126 and 134 with stores by column; the plain product, which
-// stores by column, 119.
+// CU), so its instructions count: 1000 x 4096 x 14336 with a bias takes 115 us, with
+// gelu 123, with a residual 119, with both and the bias 127; stores by column took
+// 126 with a bias and 134 with gelu; the plain product, which stores by column, 118.
 // region(w): wave w's WROWS x (32 NBW) floats.
 template <int WROWS, int NBW, class EP, class Region>
 __device__ __forceinline__ void large_m_finish(const f32x16 (&total)[WROWS / 32][NBW], Region region, int m_first,
@@ -787,7 +787,7 @@ __device__ __forceinline__ void large_m_finish(const f32x16 (&total)[WROWS / 32]
     float bias[8];
     ep.bias8(bias, in_n ? n : 0);
     u32x4 res[P];
-    if (ep.residual) {
+    if constexpr (EP::kResidual) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int m = min(m_first + r0 + p * (64 / PPR), M - 1);
@@ -821,8 +821,8 @@ __device__ __forceinline__ void large_m_finish(const f32x16 (&total)[WROWS / 32]
             v[j] = lo[j] + bias[j];
             v[4 + j] = hi[j] + bias[4 + j];
         }
-        activate<8>(v, ep.act);
-        if (ep.residual) {
+        if constexpr (EP::kActivation) activate<8>(v, ep.act);
+        if constexpr (EP::kResidual) {
             float f[8];
             unpack8(res[p], f);
 #pragma unroll
