@@ -10,8 +10,10 @@
 // tile, which the wide layers that have neither do not pay.  A bias alone, 1 / 8 /
 // 16 x 4096 x 28672 (plain product 13.0 / 13.8 / 14.5 us), costs 0.2 / 0.1 / 0.1 us
 // so, 0.8 / 0.6 / 0.6 with the activation decided at run time and 1.2 / 0.7 / 0.9
-// with the residual too.  Beside a residual the activation stays a branch: left out,
-// 16 x 14336 x 4096 took 14.3 us instead of 14.1.
+// with the residual too.  Beside a residual the activation stays a branch: a form
+// without it would be one more copy of every kernel for 1 to 2 % either way (us with
+// the branch and without: 16 x 14336 x 4096 13.7 and 13.8, 8 x 14336 x 4096 11.8 and 11.7,
+// 16 x 28672 x 8192 36.6 and 37.0, 16 x 4096 x 28672 15.7 and 15.6).
 #pragma once
 
 #include "device_common.h"

@@ -13,9 +13,9 @@
 // once however many experts chose it, and its k routed rows meet in registers
 // in slot order, so no atomics and no second order of summation exist.  All of
 // them are bound by memory from about a thousand tokens on, by the launch below.
-// Graph-timed (top-8 of 128, rows of 2048, 8192 / 64 / 1 tokens, us): dispatch of
-// e4m3 rows 27 / 4.5 / 3.8 (5.5 TB/s at 8192), combine of bf16 rows 53 / 3.0 / 2.7 (6.3
-// TB/s), its gradient 92 / 4.1 / 3.7 (6.2 TB/s).
+// Graph-timed, on buffers in turn that no cache holds (top-8 of 128, rows of 2048,
+// 8192 / 64 / 1 tokens, us): dispatch of e4m3 rows 38 / 4.5 / 3.8 (4.0 TB/s at 8192),
+// combine of bf16 rows 60 / 3.3 / 2.7 (5.6 TB/s), its gradient 108 / 4.4 / 3.8 (5.3 TB/s).
 #include <algorithm>
 #include <atomic>
 
@@ -433,7 +433,7 @@ void launch_moe_dispatch(const int* ids, const void* rows, const float* scale, i
 }
 
 // STREAM: the experts' rows, dead after this, pass the caches by (8192 tokens of
-// top-8, 2048 bf16, 57 us without, 52 with; 4096 of top-2, 4096 bf16, 26.5 and 22).
+// top-8, 2048 bf16, 65 us without, 60 with; 4096 of top-2, 4096 bf16, 26.7 and 24.8).
 template <bool STREAM>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const u32x4* __restrict__ rows,
                                                           const int* __restrict__ row_of_slot,
@@ -494,12 +494,12 @@ void launch_moe_combine(const uint16_t* rows, const int* row_of_slot, const floa
 }
 
 // NT threads per token, a workgroup or (rows of up to 64 pieces) a wave: 16384 tokens
-// of top-4, 128 / 512 bf16, 12.3 / 29.1 us with a wave, 21.7 / 30.2 with a workgroup; 1000
-// of top-8, 1024, 8.9 and 8.6.  They hold the pieces of dy, and the slots' products
-// <dy, row> are reduced over them, J slots and SLOTS / J pieces a thread at a time (J = 2, 4 or 8, the least that covers k: with 8 alone, 4096
-// tokens of top-2, 4096 bf16, took 37 us).
+// of top-4, 128 / 512 bf16, 12.0 / 30.5 us with a wave, 21.6 / 33.4 with a workgroup.
+// They hold the pieces of dy, and the slots' products <dy, row> are reduced over
+// them, J slots and SLOTS / J pieces a thread at a time (J = 2, 4 or 8, the least
+// that covers k: with 8 alone, 4096 tokens of top-2, 4096 bf16, took 37 us, so 34).
 // drows passes the caches by, which then keep the rows (4099 / 1000 / 256 tokens of
-// top-8, 2048 bf16, 59 / 17.0 / 6.3 us without, 49 / 12.7 / 5.6 with).
+// top-8, 2048 bf16, 59 / 18.1 / 6.3 us without, 57 / 15.8 / 5.7 with).
 #ifndef QG_MOE_BWD_WAVE_K          // longest row of one wave per token
 #define QG_MOE_BWD_WAVE_K 512
 #endif

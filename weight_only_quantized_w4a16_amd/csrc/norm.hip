@@ -12,9 +12,10 @@
 // fp64): y is rounded once, to bf16 or to its code, and h (stored as bf16)
 // enters the norm unrounded.
 // Both are bound by memory: a row is read once and stays in registers between
-// the reductions and the encoding.  Graph-timed: norm with residual at 8191 x 8192
-// to bf16 / e4m3 79 / 73 us (6.8 / 6.4 TB/s), at 1 x 4096 2.6 / 2.9 us; swiglu at 8192
-// x 14336 103 / 94 us (6.9 / 6.3 TB/s), at 16 x 14336 2.3 / 3.9 us (an empty launch
+// the reductions and the encoding.  Graph-timed, on buffers in turn that no cache
+// holds (as every figure of this file): norm with residual at 8191 x 8192 to bf16 /
+// e4m3 90 / 79 us (5.9 TB/s; a copy 5.3), at 1 x 4096 2.6 / 2.9 us; swiglu at 8192 x
+// 14336 116 / 103 us (6.1 / 5.7 TB/s), at 16 x 14336 2.3 / 3.9 us (an empty launch
 // takes about 2).
 
 #include <algorithm>
@@ -194,8 +195,10 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
     const size_t row = (size_t)m * chunks;
     u32x4 xv[CPT], rv[CPT], wv[CPT];
     // with a residual this is the last use of x and of the old stream, and the new
-    // one is read only after two products: both pass the caches by (8191 x 8192 to
-    // bf16 / e4m3 91 / 80 us without, 79 / 72 with)
+    // one is read only after two products: all pass the caches by, at every size
+    // (to bf16 / e4m3 without and with: 8191 x 8192 92.6 / 81.8 and 90.3 / 79.0 us, 1024 x
+    // 8192 15.3 / 14.6 and 13.6 / 12.7, 512 x 8192 8.3 / 8.5 and 8.3 / 8.2, 256 x 4096 4.1 /
+    // 4.3 and 3.9 / 4.0; 128 x 8192 4.2 / 4.6 and 4.5 / 4.4, below no difference)
     if (p.r) {
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
@@ -329,13 +332,14 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(NormArgs p) {
 }
 
 // Threads per row and chunks per thread of a row of `chunks` pieces: part of a
-// wave up to 32 pieces (norm to e4m3 at 16384 x 128 5.7 us, with a whole wave a
-// row 11.6), one wave up to 128, else one workgroup with two to four chunks a
+// wave up to 32 pieces (norm to e4m3 at 16384 x 128 6.0 us, with a whole wave a
+// row 11.7), one wave up to 128, else one workgroup with two to four chunks a
 // thread (measured against one chunk and 1024 threads, and against eight: norm to
-// e4m3 at 8191 x 8192 81 us, 93 and 83; swiglu to e4m3 at 8192 x 4096 30 us with 256
-// threads, 38 with 512).  `many` (coded rows, four a CU or more): one wave up to
-// 256 pieces, which saves the barriers (swiglu at 16384 / 256 x 2048 30 / 3.2 us
-// against 37 / 2.9; the bf16 norm, with one barrier, gains nothing).
+// e4m3 at 8191 x 8192 79 us, 91 and 80, at 1024 x 8192 12.7, 15.0 and 14.2; swiglu to
+// e4m3 at 8192 x 4096 28 us with 256 threads, 37 with 512).  `many` (coded rows, four
+// a CU or more): one wave up to 256 pieces, which saves the barriers (swiglu at
+// 16384 x 2048 29 us against 34; with few rows a CU holds too few waves; the bf16
+// norm, with one barrier, gains nothing).
 template <class Go>
 static bool with_row_shape(int chunks, bool many, Go&& go) {
     if (chunks <= 8) go(ic<8>{}, ic<1>{});
@@ -405,8 +409,8 @@ __device__ __forceinline__ void swiglu8(u32x4 gate, u32x4 up, float* y) {
 }
 
 // STREAM: the gate_up output, dead after this, passes the caches by (8192 x 14336
-// to bf16 / e4m3 121 / 107 us without, 103 / 91 with; 256 x 14336, which the L2s
-// hold, 5.2 / 6.1 without, 5.5 / 6.3 with).
+// to bf16 / e4m3 121 / 109 us without, 116 / 103 with, 16384 x 2048 36 / 33 and 34 / 29;
+// 256 x 14336, which the L2s hold, 5.2 / 6.1 without, 5.5 / 6.3 with).
 static bool stream_gate_up(const SwigluArgs& p) { return (size_t)p.M * p.I * 4 > kStreamBytes; }
 
 // no row reduction: the grid covers the chunks of all rows
