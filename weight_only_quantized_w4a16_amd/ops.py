@@ -9,6 +9,9 @@ products) is missing or belongs to another torch, those calls raise.
 
 bf16 data travels as torch.bfloat16 (or int16 / uint16 bit patterns) tensors;
 e4m3 codes as torch.uint8 (or torch.float8_e4m3fn) tensors.
+
+Only MoeRouting carries gradients; outputs of everything else are cut off from the
+autograd graph of their inputs.
 """
 import contextlib
 import ctypes
