@@ -385,7 +385,8 @@ def _on(stream, t):
 
 
 class _Scratch:
-    """A workspace kept from call to call, for calls that do not overlap in time."""
+    """A workspace kept from call to call, for calls that do not overlap in time.  A
+    call of the largest size before a capture spares the graph one of its own."""
 
     _ws = None
     _captured = False            # a captured graph uses _ws
@@ -801,7 +802,9 @@ class MoeRouting:
     [E + 1] for the grouped products and `row_of_slot` int32 [B, k] (-1: no row).
 
     dispatch and gather carry gradients of bf16 rows, combine those of rows, weights and
-    residual, where torch records them (a router trains over frozen experts)."""
+    residual, where torch records them (a router trains over frozen experts).  As with
+    torch's own operators, capture a backward pass into a graph only while no eager
+    autograd graph of the same leaves is alive."""
 
     def __init__(self, offsets, row_of_slot):
         self.offsets, self.row_of_slot = offsets, row_of_slot
