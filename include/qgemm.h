@@ -590,6 +590,92 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
                                int B, int k, int K, uint16_t *drows_bf16,
                                float *dweights, qg_stream stream);
 
+/*
+ * ---- from the qkv product to the o product ------------------------------------
+ * A batch of B sequences brings T new tokens side by side: sequence b owns tokens
+ * q_offsets[b] .. q_offsets[b + 1] - 1 (ascending; none is fine) and has kv_len[b]
+ * positions, those of its new tokens the last of them.  Its position j is row
+ * j % page_size of page block_table[b][j / page_size] of a paged cache: keys and
+ * values [pages, Hkv, page_size, D], bf16, or e4m3 codes with one fp32 scale for each
+ * position and head, [pages, Hkv, page_size] (k_scale and v_scale, NULL for a bf16
+ * cache; the scale and codes of quant_act_per_token over a head's D elements).
+ *
+ *   qkv_bf16     in  [T, (Hq + 2 Hkv) D] rows of the fused product: query heads, key
+ *                heads, value heads.
+ *   q_offsets    in  int32 [B + 1], on the device, as the next two.
+ *   kv_len       in  int32 [B].
+ *   block_table  in  int32 [B, max_pages]; only entries of positions below kv_len are
+ *                read.
+ * Hq is a multiple of Hkv (query head h reads key head h / (Hq / Hkv)), Hq <= 1024,
+ * D is 64 or 128, page_size 16, 32, 64, 128 or 256, T < 2^22, T Hq <= 2^27, B <= 2^14,
+ * max_pages page_size <= 2^30 (QG_ERR_SHAPE otherwise).
+ * The lists are trusted for no address: an entry of the table outside 0 .. pages - 1,
+ * or a position past the table, holds no key (nothing is stored there and nothing is
+ * seen there); tokens of no sequence are left as they were in every output; offsets
+ * that do not ascend leave the tokens they confuse unspecified.
+ *
+ * qk_norm_rope -- the queries and keys of fused rows: per head the RMS norm with a
+ * weight, then the rotation by position, rounded once.
+ *   q_weight_bf16, k_weight_bf16   in  [D], or NULL: no norm (eps is then not read).
+ *   positions    in  int32 [T], any values.
+ *   inv_freq     in  fp64 [rotary_dim / 2] radians a position; NULL for rotary_dim 0.
+ *   rotary_dim   elements of a head that are rotated, the first ones: 0 .. D, a
+ *                multiple of 16.
+ *   interleaved  0: pairs (i, i + rotary_dim / 2); else neighbours (2 i, 2 i + 1).
+ *   q_bf16, k_bf16   out [T, Hq, D] and [T, Hkv, D].
+ *
+ * kv_append -- the same by the batch's own positions, the keys and the values (as
+ * they are) into the cache, the queries into q_bf16 [T, Hq, D].  Two tokens that name
+ * the same row of the cache leave unspecified contents there.
+ *
+ * paged_attention -- out[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j over the
+ * positions j of the token's sequence up to its own; with window > 0 only those less
+ * than `window` before it and the first `sinks` positions of the sequence.  Scores,
+ * softmax and sums fp32, out rounded once; above 16 rows (token, head of the key
+ * head's group) a sequence the probabilities are rounded to bf16 before their product.
+ *   q_bf16       in  [T, Hq, D].  It must not overlap out_bf16.
+ *   window       0: none; up to 2^30.  sinks >= 0: not read without a window.
+ *   shared_prefix   the first positions of every sequence are the same pages: a
+ *                multiple of page_size (0: none).  They are read by row 0 of the
+ *                table, once for all; the entries of the other rows are not read there.
+ *                The results are those of the same call without it.
+ *   max_q        the largest number of new tokens of a sequence, or 0: not known.  It
+ *                chooses kernels and changes no result beyond their rounding.
+ *   out_bf16     out [T, Hq, D].  A row that sees no key is zero.
+ *   lse          out fp32 [T, Hq] log of the sum of exponentials (-inf for a row that
+ *                sees no key), or NULL.
+ *   workspace    qg_paged_attention_workspace_bytes(...) bytes (NULL when that is 0),
+ *                16-byte aligned, zero-filled before its first use; one sized for the
+ *                largest call serves calls of any shape in any order that do not
+ *                overlap in time.
+ * Masked positions never matter, whatever they hold.  A row whose scores are all -inf
+ * counts as one that sees no key.  The same call gives the same bits on every run.
+ */
+qg_status qk_norm_rope(const uint16_t *qkv_bf16, const uint16_t *q_weight_bf16,
+                       const uint16_t *k_weight_bf16, float eps,
+                       const int32_t *positions, const double *inv_freq,
+                       int rotary_dim, int interleaved, int T, int Hq, int Hkv, int D,
+                       uint16_t *q_bf16, uint16_t *k_bf16, qg_stream stream);
+qg_status kv_append(const uint16_t *qkv_bf16, const uint16_t *q_weight_bf16,
+                    const uint16_t *k_weight_bf16, float eps, const double *inv_freq,
+                    int rotary_dim, int interleaved, const int32_t *q_offsets,
+                    const int32_t *kv_len, const int32_t *block_table, int T, int B,
+                    int max_pages, int Hq, int Hkv, int D, void *k_cache,
+                    void *v_cache, float *k_scale, float *v_scale, int pages,
+                    int page_size, uint16_t *q_bf16, qg_stream stream);
+size_t qg_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_pages,
+                                          int64_t Hq, int64_t Hkv, int64_t D,
+                                          int64_t page_size, int64_t shared_prefix,
+                                          int64_t max_q);
+qg_status paged_attention(const uint16_t *q_bf16, const void *k_cache,
+                          const void *v_cache, const float *k_scale,
+                          const float *v_scale, int pages, int page_size,
+                          const int32_t *q_offsets, const int32_t *kv_len,
+                          const int32_t *block_table, int T, int B, int max_pages,
+                          int Hq, int Hkv, int D, float scale, int window, int sinks,
+                          int shared_prefix, int max_q, uint16_t *out_bf16, float *lse,
+                          void *workspace, size_t workspace_bytes, qg_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

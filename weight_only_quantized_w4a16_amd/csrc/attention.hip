@@ -1,0 +1,654 @@
+// Causal attention of a batch's new tokens over their paged cache.
+//
+//   out[t, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q . k_j - max_j)
+//   j over the positions up to the token's own; with a window W those less than W before
+//   it and the first `sinks` positions of the sequence
+//
+// One pass over the keys with a running maximum m and sum l in fp32 (base-2
+// exponentials).  Scores are formed transposed, S^T = K Q^T, so that a lane of the
+// matrix instruction's result holds one query's scores: the row statistics of the
+// softmax need no LDS, the factors that rescale the running result are the lane's own,
+// and the probabilities are, without a move, the second operand of O^T = V^T P^T (the
+// order of the keys inside a step is free as long as both operands share it).  Its
+// first operand is read transposed from LDS (ds_read_b64_tr).  The rows of a matrix tile are
+// (token, query head of the group) pairs of one key head: a key is read once for its
+// whole group.
+//
+// What a masked key holds never matters: its probability is an exact zero, values that
+// no row sees are replaced by zeros before the product (uninitialised memory may hold
+// NaN), and where a value that only some rows see is infinite or NaN those rows are
+// multiplied one by one.  A row that sees no key is zero, its lse minus infinity.
+
+#include <algorithm>
+
+#include "device_common.h"
+#include "launch.h"
+#include "rows.h"
+#include "sequences.h"
+
+namespace qg {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// What both kernels share: the call, its keys, its work items.
+// ---------------------------------------------------------------------------
+struct Call : AttentionArgs {
+    int G;                       // query heads of a key head
+    float scale2;                // scale log2(e)
+    // the plan
+    int items;                   // work items for each key head at most, below 2^24
+    int target;                  // chunks wanted for each key head over the whole batch; 0: keys are not split
+    int least;                   // tiles of a chunk at least
+    unsigned* counters;          // one a split row tile, zero between calls
+    float* slots;                // partial results of chunks
+};
+
+// Key tiles that some token of a sequence sees: [begin0, end0) around the first
+// positions and [begin1, end1), in tiles of TK positions.
+struct Span {
+    int begin0, begin1, n0, n;
+    __device__ __forceinline__ int tile(int i) const { return i < n0 ? begin0 + i : begin1 + i - n0; }
+};
+template <int TK>
+__device__ __forceinline__ Span span_of(const Call& a, const Sequence& s) {
+    const int limit = (int)min((int64_t)s.len, (int64_t)a.max_pages << a.page_shift);
+    int lo = a.prefix, seen_first = 0;
+    if (a.window > 0) {
+        lo = max(lo, s.len - s.tokens - a.window + 1);
+        seen_first = min(min(a.sinks, lo), limit);
+    }
+    Span r;
+    r.begin1 = lo / TK;
+    const int end1 = max((limit + TK - 1) / TK, r.begin1);
+    r.begin0 = a.prefix / TK;
+    r.n0 = seen_first > a.prefix ? min((seen_first + TK - 1) / TK, r.begin1) - r.begin0 : 0;
+    r.n = r.n0 + end1 - r.begin1;
+    return r;
+}
+
+// A work item: a tile of at most BM rows of a sequence and a chunk of the key tiles.
+struct Item {
+    int b, row0, chunk, chunks, chunk_tiles, first;      // first: the item of the row tile's first chunk
+    Sequence s;
+    Span span;
+};
+
+// The items are numbered sequence by sequence, row tile by row tile, chunk by chunk.  A
+// chunk's length follows from the whole batch: total / target tiles, so that chunks are alike
+// whatever the lengths, and there are at most target + (row tiles) of them.  Every wave
+// finds the item `it` for itself, 64 sequences a step, on scans of DPP moves (false: there
+// is none).
+template <int BM, int TK>
+__device__ __forceinline__ bool find_item(const Call& a, int it, Item& item) {
+    const int lane = threadIdx.x & 63;
+    const int blocks = (a.B + 63) >> 6;
+    auto load = [&](int j, int& lo, int& hi, int& len) {
+        const int b = 64 * j + lane;
+        lo = a.q_offsets[min(b, a.B)];
+        hi = a.q_offsets[min(b + 1, a.B)];
+        len = a.kv_len[min(b, a.B - 1)];
+    };
+    auto rows_of = [&](const Sequence& s) { return (s.tokens * a.G + BM - 1) / BM; };
+    int chunk_tiles = 0x7fffffff;
+    int lo, hi, len;
+    load(0, lo, hi, len);
+    if (a.target > 0) {
+        double total = 0.0;                              // exact: below 2^53
+        int l = lo, h = hi, k = len;
+        for (int j = 0; j < blocks; ++j) {
+            const Sequence s = sequence_of(l, h, k, a.T);
+            if (j + 1 < blocks) load(j + 1, l, h, k);
+            if (64 * j + lane < a.B) total += (double)rows_of(s) * (double)span_of<TK>(a, s).n;
+        }
+        total = wave_sum(total);
+        chunk_tiles = max(a.least, (int)fmin(ceil(total / a.target), 2147483647.0));
+    }
+    int carry = 0;
+    for (int j = 0; j < blocks; ++j) {
+        const int b = 64 * j + lane;
+        const Sequence s = sequence_of(lo, hi, len, a.T);
+        if (j + 1 < blocks) load(j + 1, lo, hi, len);
+        const int rows = b < a.B ? rows_of(s) : 0;
+        const int n = span_of<TK>(a, s).n;
+        const int chunks = a.target > 0 ? max(1, (n - 1) / chunk_tiles + 1) : 1;
+        // (a count past the grid is as good as any other: sums stay inside an int)
+        const int count = (int)min((int64_t)rows * chunks, (int64_t)1 << 24);
+        const int incl = wave_scan(count) + carry;
+        const int total = __builtin_amdgcn_readlane(incl, 63);
+        if (it < total) {
+            const int before = incl - count;
+            const int src = __builtin_ctzll(__ballot(it >= before && it < incl));
+            item.b = __builtin_amdgcn_readfirstlane(64 * j + src);
+            item.s.first_token = __builtin_amdgcn_readlane(s.first_token, src);
+            item.s.tokens = __builtin_amdgcn_readlane(s.tokens, src);
+            item.s.len = __builtin_amdgcn_readlane(s.len, src);
+            item.chunks = __builtin_amdgcn_readlane(chunks, src);
+            item.chunk_tiles = __builtin_amdgcn_readfirstlane(chunk_tiles);
+            const int at = it - __builtin_amdgcn_readlane(before, src);
+            item.row0 = at / item.chunks * BM;
+            item.chunk = at % item.chunks;
+            item.first = it - item.chunk;
+            item.span = span_of<TK>(a, item.s);
+            // offsets that do not ascend may ask for more than the grid holds: such a tile is left out whole
+            return item.first + item.chunks <= a.items;
+        }
+        carry = total;
+    }
+    return false;
+}
+
+// The larger of the two lanes' values at distance 16 / 32, and their sum, in both.
+__device__ __forceinline__ float both16(float v, float& other) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    other = __uint_as_float(r[1]);
+    return __uint_as_float(r[0]);
+}
+__device__ __forceinline__ float both32(float v, float& other) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    other = __uint_as_float(r[1]);
+    return __uint_as_float(r[0]);
+}
+
+// 16 bytes a lane from base + off to lds + 16 lane, as lds_copy_b128 of device_common.h.
+__device__ __forceinline__ void lds_copy_b128(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+// 4 bytes a lane from src to lds + 4 lane
+__device__ __forceinline__ void lds_copy_b32(const void* src, uint32_t lds) {
+    asm volatile("global_load_lds_dword %0, off" : : "v"(src), "{m0}"(lds) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_vmem() {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Transposed LDS reads: the 16 lanes of a group name 8-byte pieces that make the rows
+// of a matrix 16 columns wide (bf16: 4 lanes a row, e4m3: 2), and lane i receives column i.
+__device__ __forceinline__ u32x2 lds_columns_b16(uint32_t at) {
+    const auto p = (__attribute__((address_space(3))) i16x4*)(uintptr_t)at;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+}
+__device__ __forceinline__ u32x2 lds_columns_b8(uint32_t at) {
+    const auto p = (__attribute__((address_space(3))) i32x2*)(uintptr_t)at;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(p));
+}
+template <class T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+    return *(const __attribute__((address_space(3))) T*)(uintptr_t)at;
+}
+
+// Eight e4m3 codes as bf16: exact.
+__device__ __forceinline__ u32x4 e4m3_to_bf16(u32x2 c) {
+    u32x4 r;
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, 1.0f, false));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, 1.0f, true));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, false));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, true));
+    return r;
+}
+
+// An infinity or NaN among eight bf16 values.
+__device__ __forceinline__ bool nonfinite8(u32x4 v) {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = v[i];
+        bad |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    }
+    return bad;
+}
+
+// ---- the running softmax of one query column -------------------------------------
+// m: the largest score so far (base 2), in all lanes of the column; l: this lane's share
+// of the sum.
+struct Running {
+    float m = -__builtin_inff(), l = 0.0f;
+    // The reference to subtract: a column that has seen nothing keeps its exponentials at zero.
+    __device__ __forceinline__ float reference() const { return m == -__builtin_inff() ? 0.0f : m; }
+};
+
+// Joins the partial results of a row's chunks, in order: `o` of N elements with (m, l).
+template <int N>
+struct Joined {
+    float m = -__builtin_inff(), l = 0.0f, o[N];
+    __device__ __forceinline__ Joined() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = 0.0f;
+    }
+    __device__ __forceinline__ void add(float m2, float l2, const float* o2) {
+        const float top = fmaxf(m, m2);
+        const float ref = top == -__builtin_inff() ? 0.0f : top;
+        const float w1 = __builtin_amdgcn_exp2f(m - ref), w2 = __builtin_amdgcn_exp2f(m2 - ref);
+        m = top;
+        l = l * w1 + l2 * w2;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = o[i] * w1 + o2[i] * w2;
+    }
+};
+
+// Agent-scope accesses of N floats, two at a time: other XCDs read what this one wrote.
+template <int N>
+__device__ __forceinline__ void store_agent(float* p, const float* v) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const uint64_t u = (uint64_t)__float_as_uint(v[i]) | ((uint64_t)__float_as_uint(v[i + 1]) << 32);
+        __hip_atomic_store(reinterpret_cast<uint64_t*>(p + i), u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_agent(const float* p, float* v) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const uint64_t u = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p + i), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        v[i] = __uint_as_float((uint32_t)u);
+        v[i + 1] = __uint_as_float((uint32_t)(u >> 32));
+    }
+}
+
+// A row's result: N neighbouring elements from element d0, and once a row the lse.
+template <int N>
+__device__ __forceinline__ void store_row(const Call& a, int D, int64_t row, int d0, const Joined<N>& j) {
+    const float inv = 1.0f / j.l;
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const f32x2 v = j.l == 0.0f ? f32x2{0.0f, 0.0f} : f32x2{j.o[2 * i] * inv, j.o[2 * i + 1] * inv};
+        w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    }
+    uint16_t* p = a.out + row * D + d0;
+    if constexpr (N == 8) *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    if (a.lse && d0 == 0) a.lse[row] = j.l == 0.0f ? -__builtin_inff() : (j.m + log2f(j.l)) * 0.69314718055994530942f;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows a sequence (decoding): a workgroup takes one row tile of 16 and a chunk of
+// keys, its four waves 32 keys each of every 128.  Every wave streams its keys and
+// values into a ring of its own in LDS, with no barrier until its end; the waves' results are
+// joined there, and those of chunks by the last workgroup to arrive, in chunk order.
+//
+// Bound by memory.  The probabilities enter the second product as a sum of two bf16
+// numbers, so it loses nothing to their rounding (matrix instructions are idle here).
+// ---------------------------------------------------------------------------
+template <int D, bool E4M3>
+struct Rows {
+    static constexpr int BM = 16, TK = 32, WAVES = 4, TILE = TK * WAVES;
+    static constexpr int RB = E4M3 ? D : 2 * D;          // bytes of a cached row
+    static constexpr int PIECES = RB / 16;
+    static constexpr int KEYS = 64 / PIECES;             // keys of one copy
+    static constexpr int LOADS = TK / KEYS;
+    static constexpr int SCALES = E4M3 ? 256 : 0;
+    static constexpr int STAGE = 2 * TK * RB + SCALES;
+    static constexpr int NS = RB == 256 ? 2 : 4;         // stages
+    static constexpr int COPIES = 2 * LOADS + (E4M3 ? 1 : 0);
+    static constexpr int OROW = D + 4;                   // floats of a row handed over in LDS
+    static constexpr int WAVE_BYTES = NS * STAGE;
+    static constexpr int SLOT = BM * (D + 2);            // floats
+    static_assert(BM * (OROW + 2) * 4 <= WAVE_BYTES, "the hand-over fits a wave's ring");
+    // Where a row's 16-byte piece lies: pieces change places by the key so that the lanes
+    // of a read meet different banks (16 pieces span all of them).
+    __device__ static __forceinline__ int swap_k(int key) {
+        return PIECES == 16 ? key & 15 : PIECES == 8 ? (key >> 1) & 7 : (key >> 2) & 3;
+    }
+    __device__ static __forceinline__ int swap_v(int key) {
+        if (!E4M3) return PIECES == 16 ? (key & 3) * 4 + (key >> 2 & 1) * 2 : (key >> 1 & 1) * 2 + (key >> 2 & 1) * 4;
+        return PIECES == 8 ? (key >> 1 & 1) + (key >> 4 & 1) * 2 + (key >> 2 & 1) * 4 : (key >> 4 & 1) + (key >> 2 & 1) * 2;
+    }
+};
+
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
+    using R = Rows<D, E4M3>;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    __shared__ int flag;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;              // column (row of the tile), lane group
+    const int h = blockIdx.x % a.Hkv;
+    Item item;
+    if (!find_item<R::BM, R::TILE>(a, (int)(blockIdx.x / a.Hkv), item)) return;
+    const int first_pos = item.s.len - item.s.tokens;
+    const int rows = min(R::BM, item.s.tokens * a.G - item.row0);
+    const int my_row = item.row0 + c;
+    const bool mine = c < rows;
+    const int pos = mine ? first_pos + my_row / a.G : -1;
+    const int pos_min = first_pos + item.row0 / a.G, pos_max = first_pos + (item.row0 + rows - 1) / a.G;
+    const int limit = (int)min((int64_t)item.s.len, (int64_t)a.max_pages << a.page_shift);
+
+    const int i0 = item.chunks > 1 ? item.chunk * item.chunk_tiles : 0;
+    const int tiles = item.chunks > 1 ? min(item.chunk_tiles, item.span.n - i0) : item.span.n;
+    const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem + wave * R::WAVE_BYTES;
+    const int* table = a.table + (int64_t)item.b * a.max_pages;
+
+    // the copies' offsets from a 16-key half's first row
+    uint32_t koff[R::LOADS], voff[R::LOADS];
+#pragma unroll
+    for (int j = 0; j < R::LOADS; ++j) {
+        const int key = j * R::KEYS + lane / R::PIECES;
+        const int at = (key & 15) * R::RB;
+        koff[j] = at + ((lane % R::PIECES) ^ R::swap_k(key)) * 16;
+        voff[j] = at + ((lane % R::PIECES) ^ R::swap_v(key)) * 16;
+    }
+    // the two pages of a wave's 32 keys: their rows in the cache, -1 where there is no page
+    struct Pages { int64_t row[2]; };
+    auto pages_of = [&](int key0) {
+        Pages p;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int key = key0 + 16 * x;
+            const int id = key < limit ? table[key >> a.page_shift] : -1;
+            p.row[x] = id >= 0 && id < a.pages
+                ? ((((int64_t)id * a.Hkv + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) : -1;
+        }
+        return p;
+    };
+    auto key_of = [&](int i) { return item.span.tile(i0 + i) * R::TILE + wave * R::TK; };
+    auto copy = [&](int stage, const Pages& p) {
+        const uint32_t to = ring + stage * R::STAGE;
+#pragma unroll
+        for (int j = 0; j < R::LOADS; ++j) {
+            const int64_t row = max(p.row[j * R::KEYS / 16], (int64_t)0);
+            lds_copy_b128(static_cast<const unsigned char*>(a.k) + row * R::RB, koff[j], to + j * 1024);
+            lds_copy_b128(static_cast<const unsigned char*>(a.v) + row * R::RB, voff[j], to + R::TK * R::RB + j * 1024);
+        }
+        if constexpr (E4M3) {
+            const int64_t row0 = max(p.row[0], (int64_t)0), row1 = max(p.row[1], (int64_t)0);
+            const int64_t row = (lane & 16 ? row1 : row0) + (lane & 15);
+            lds_copy_b32((lane < 32 ? a.k_scale : a.v_scale) + row, to + 2 * R::TK * R::RB);
+        }
+    };
+
+    // this lane's query: 8 elements of every 32
+    bf16x8 q[D / 32];
+    {
+        const int r = min(my_row, item.s.tokens * a.G - 1);
+        const int64_t at = ((int64_t)(item.s.first_token + r / a.G) * a.Hq + h * a.G + r % a.G) * D + 8 * g;
+#pragma unroll
+        for (int ks = 0; ks < D / 32; ++ks) q[ks] = as_bf16x8(*reinterpret_cast<const u32x4*>(a.q + at + 32 * ks));
+    }
+
+    Pages held[R::NS];                                   // of the tiles in the ring
+#pragma unroll
+    for (int s = 0; s < R::NS; ++s)
+        if (s < tiles) {
+            held[s] = pages_of(key_of(s));
+            copy(s, held[s]);
+        }
+
+    Running run;
+    f32x4 o[D / 16];
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    auto step = [&](auto stage, int i) {
+        constexpr int S = decltype(stage)::value;
+        const Pages here = held[S];
+        const bool more = i + R::NS < tiles;
+        if (more) held[S] = pages_of(key_of(i + R::NS));
+        const int ahead = min(tiles - 1 - i, R::NS - 1); // tiles still on their way behind this one
+        if (ahead == R::NS - 1) wait_vmem<(R::NS - 1) * R::COPIES>();
+        else if (R::NS > 2 && ahead == R::NS - 2) wait_vmem<(R::NS > 2 ? R::NS - 2 : 0) * R::COPIES>();
+        else wait_vmem<0>();
+        const int key0 = key_of(i);
+        const uint32_t kb0 = ring + S * R::STAGE, vb0 = kb0 + R::TK * R::RB, sb0 = vb0 + R::TK * R::RB;
+
+        // S^T: lane (c, g) receives keys 16 x + 4 g + r of column c
+        float s[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+            const int key = 16 * x + c;
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks) {
+                u32x4 k;
+                if constexpr (E4M3)
+                    k = e4m3_to_bf16(lds_read<u32x2>(kb0 + key * R::RB + ((2 * ks + (g >> 1)) ^ R::swap_k(key)) * 16 + (g & 1) * 8));
+                else
+                    k = lds_read<u32x4>(kb0 + key * R::RB + ((4 * ks + g) ^ R::swap_k(key)) * 16);
+                acc = mfma_bf16_16x16x32(as_bf16x8(k), q[ks], acc);
+            }
+            f32x4 factor = f32x4{a.scale2, a.scale2, a.scale2, a.scale2};
+            if constexpr (E4M3) factor *= lds_read<f32x4>(sb0 + (16 * x + 4 * g) * 4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[4 * x + r] = acc[r] * factor[r];
+        }
+
+        // which of this lane's keys its row sees
+        const bool whole = here.row[0] >= 0 && here.row[1] >= 0 && key0 >= a.prefix && key0 + 31 <= pos_min &&
+                           (a.window <= 0 || key0 > pos_max - a.window || key0 + 31 < a.sinks);
+        uint32_t seen = 0xff;
+        if (!whole) {
+            seen = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int key = key0 + 16 * (e >> 2) + 4 * g + (e & 3);
+                const bool sees = here.row[e >> 2] >= 0 && key >= a.prefix && key <= pos && key < limit &&
+                                  (a.window <= 0 || key > pos - a.window || key < a.sinks);
+                seen |= sees ? 1u << e : 0u;
+                if (!sees) s[e] = -__builtin_inff();
+            }
+        }
+
+        // the running maximum; its lanes are c, c + 16, c + 32, c + 48
+        float top = s[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
+        float t2;
+        top = both16(top, t2);
+        top = fmaxf(top, t2);
+        top = both32(top, t2);
+        top = fmaxf(top, t2);
+        if (__ballot(top > run.m)) {
+            const float before = run.m;
+            run.m = fmaxf(run.m, top);
+            const float w = __builtin_amdgcn_exp2f(before - run.reference());
+            run.l *= w;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) o[d] *= w;
+        }
+        const float ref = run.reference();
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(s[e] - ref);
+            run.l += p[e];
+        }
+        if constexpr (E4M3) {
+            const f32x4 v0 = lds_read<f32x4>(sb0 + 128 + 16 * g), v1 = lds_read<f32x4>(sb0 + 128 + 64 + 16 * g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = p[e] * (e < 4 ? v0[e & 3] : v1[e & 3]);
+                p[e] = whole || (seen >> e & 1) ? v : 0.0f;
+            }
+        }
+        const u32x4 hi = pack8(p);
+        float rest[8];
+        unpack8(hi, rest);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rest[e] = p[e] - rest[e];
+        // an infinite probability (a scale that overflowed) has no rest
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rest[e] = __builtin_isfinite(rest[e]) ? rest[e] : 0.0f;
+        const u32x4 lo = pack8(rest);
+
+        // V^T: lane (c, g) takes element 16 d + c of keys 4 g .. and 16 + 4 g ..
+        auto values = [&](int d) {
+            if constexpr (E4M3) {
+                const int key = (c >> 3 << 4) + 4 * g + (c >> 1 & 3);
+                return e4m3_to_bf16(lds_columns_b8(vb0 + key * R::RB + (d ^ R::swap_v(key)) * 16 + (c & 1) * 8));
+            } else {
+                const int key = 4 * g + (c >> 2);
+                const uint32_t at = vb0 + key * R::RB + ((2 * d + (c >> 1 & 1)) ^ R::swap_v(key)) * 16 + (c & 1) * 8;
+                const u32x2 v0 = lds_columns_b16(at), v1 = lds_columns_b16(at + 16 * R::RB);
+                return u32x4{v0.x, v0.y, v1.x, v1.y};
+            }
+        };
+        if (whole) {
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                const bf16x8 v = as_bf16x8(values(d));
+                o[d] = mfma_bf16_16x16x32(v, as_bf16x8(lo), o[d]);
+                o[d] = mfma_bf16_16x16x32(v, as_bf16x8(hi), o[d]);
+            }
+        } else {
+            // by slot: the columns that see it, 16 bits of this lane's group
+            uint32_t by[8];
+            u32x4 any = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                by[e] = (uint32_t)(__ballot(seen >> e & 1) >> (16 * g)) & 0xffffu;
+                any[e >> 1] |= by[e] ? 0xffffu << (16 * (e & 1)) : 0u;
+            }
+            bool bad = false;
+            u32x4 v[D / 16];
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                v[d] = values(d) & any;
+                bad |= nonfinite8(v[d]);
+            }
+            if (!__ballot(bad)) {
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    o[d] = mfma_bf16_16x16x32(as_bf16x8(v[d]), as_bf16x8(lo), o[d]);
+                    o[d] = mfma_bf16_16x16x32(as_bf16x8(v[d]), as_bf16x8(hi), o[d]);
+                }
+            } else {
+                // column by column, with zeros for what that column does not see
+                for (int col = 0; col < 16; ++col) {
+                    u32x4 sees = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sees[e >> 1] |= by[e] >> col & 1 ? 0xffffu << (16 * (e & 1)) : 0u;
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        f32x4 r = mfma_bf16_16x16x32(as_bf16x8(v[d] & sees), as_bf16x8(lo), o[d]);
+                        r = mfma_bf16_16x16x32(as_bf16x8(v[d] & sees), as_bf16x8(hi), r);
+                        if (c == col) o[d] = r;
+                    }
+                }
+            }
+        }
+        if (more) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read
+            copy(S, held[S]);
+        }
+    };
+    for (int i = 0; i < tiles; i += R::NS)
+        static_for<R::NS>([&](auto s) {
+            if (i + decltype(s)::value < tiles) step(s, i + decltype(s)::value);
+        });
+
+    // the waves' results meet in LDS, each in its own ring
+    {
+        float t2;
+        float l = both16(run.l, t2);
+        l += t2;
+        l = both32(l, t2);
+        l += t2;
+        float* mine_o = reinterpret_cast<float*>(smem + wave * R::WAVE_BYTES);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) *reinterpret_cast<f32x4*>(mine_o + c * R::OROW + 16 * d + 4 * g) = o[d];
+        if (g == 0) {
+            mine_o[R::BM * R::OROW + 2 * c] = run.m;
+            mine_o[R::BM * R::OROW + 2 * c + 1] = l;
+        }
+    }
+    __syncthreads();
+    constexpr int N = D / 16;                            // elements of a thread
+    const int r = tid >> 4, d0 = (tid & 15) * N;
+    const bool live = r < rows;
+    Joined<N> j;
+    if (live)
+        for (int w = 0; w < R::WAVES; ++w) {
+            const float* from = reinterpret_cast<const float*>(smem + w * R::WAVE_BYTES);
+            j.add(from[R::BM * R::OROW + 2 * r], from[R::BM * R::OROW + 2 * r + 1], from + r * R::OROW + d0);
+        }
+    if (item.chunks > 1) {
+        float* slot = a.slots + ((int64_t)item.first * a.Hkv + (int64_t)h * item.chunks) * R::SLOT;
+        if (live) {
+            float* to = slot + (int64_t)item.chunk * R::SLOT;
+            store_agent<N>(to + r * D + d0, j.o);
+            if (d0 == 0) {
+                const float ml[2] = {j.m, j.l};
+                store_agent<2>(to + R::BM * D + 2 * r, ml);
+            }
+        }
+        unsigned* counter = a.counters + (int64_t)item.first * a.Hkv + h;
+        if (!arrive_and_check_last(counter, item.chunks, &flag)) return;
+        if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (!live) return;
+        j = Joined<N>();
+#pragma unroll 4
+        for (int x = 0; x < item.chunks; ++x) {
+            const float* from = slot + (int64_t)x * R::SLOT;
+            float ml[2], part[N];
+            load_agent<2>(from + R::BM * D + 2 * r, ml);
+            load_agent<N>(from + r * D + d0, part);
+            j.add(ml[0], ml[1], part);
+        }
+    }
+    if (!live) return;
+    const int at = item.row0 + r;
+    store_row<N>(a, D, (int64_t)(item.s.first_token + at / a.G) * a.Hq + h * a.G + at % a.G, d0, j);
+}
+
+// ---------------------------------------------------------------------------
+// The plan of a call, from its sizes alone.
+// ---------------------------------------------------------------------------
+struct Plan {
+    int items;                   // work items for each key head at most
+    int target, least;
+    size_t slots;                // floats
+};
+
+// Chunks are worth their hand-over from 256 keys on, and only while the row tiles leave
+// workgroup slots free.
+Plan plan_rows(int T, int B, int Hq, int Hkv, int D, int64_t max_kv) {
+    const int G = Hq / Hkv;
+    const int64_t tiles = std::min<int64_t>((int64_t)T * G, (int64_t)T * G / 16 + B);      // row tiles at most
+    Plan p{(int)tiles, 0, 2, 0};
+    const int64_t want = 4 * (int64_t)device_cu_count() / Hkv;
+    if (tiles < want && max_kv > 256 && (tiles + want) * Hkv <= kMaxCounters) {
+        p.target = (int)want;
+        p.items = (int)(tiles + want);
+        p.slots = (size_t)p.items * Hkv * 16 * (D + 2);
+    }
+    return p;
+}
+
+template <int D, bool E4M3>
+void launch_rows(Call a, const Plan& p, void* ws, hipStream_t st) {
+    using R = Rows<D, E4M3>;
+    a.items = p.items;
+    a.target = p.target;
+    a.least = p.least;
+    a.counters = static_cast<unsigned*>(ws);
+    a.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kCounterBytes);
+    static std::atomic<uint64_t> done{0};
+    allow_dynamic_lds(reinterpret_cast<const void*>(&attention_rows_kernel<D, E4M3>), R::WAVES * R::WAVE_BYTES, done);
+    attention_rows_kernel<D, E4M3><<<dim3((unsigned)(p.items * a.Hkv)), 256, R::WAVES * R::WAVE_BYTES, st>>>(a);
+}
+
+}  // namespace
+
+size_t paged_attention_workspace_bytes(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, int, int) {
+    if (T == 0 || B == 0) return 0;
+    const size_t floats = plan_rows(T, B, Hq, Hkv, D, max_kv).slots;
+    return floats ? kCounterBytes + floats * 4 : 0;
+}
+
+void launch_paged_attention(const AttentionArgs& args, int D, void* ws, hipStream_t st) {
+    Call a{args};
+    a.G = a.Hq / a.Hkv;
+    a.scale2 = a.scale * 1.44269504088896340736f;
+    a.prefix = 0;                // the shared pages are read by every sequence for itself
+    const Plan p = plan_rows(a.T, a.B, a.Hq, a.Hkv, D, (int64_t)a.max_pages << a.page_shift);
+    if (D == 64) a.k_scale ? launch_rows<64, true>(a, p, ws, st) : launch_rows<64, false>(a, p, ws, st);
+    else a.k_scale ? launch_rows<128, true>(a, p, ws, st) : launch_rows<128, false>(a, p, ws, st);
+}
+
+}  // namespace qg

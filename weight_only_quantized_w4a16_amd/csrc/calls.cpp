@@ -123,7 +123,8 @@ struct Launch {
 
 #define QG_CALLS(X)                                                                                              \
     X(rms_norm) X(rms_norm_quant) X(rms_norm_quant_int8) X(swiglu) X(swiglu_quant) X(swiglu_quant_int8)          \
-    X(qgemm_w4a16_epilogue) X(moe_dispatch) X(moe_gather) X(moe_combine) X(moe_combine_backward)
+    X(qgemm_w4a16_epilogue) X(moe_dispatch) X(moe_gather) X(moe_combine) X(moe_combine_backward)       \
+    X(qk_norm_rope) X(kv_append) X(paged_attention)
 
 struct {
 #define X(f) decltype(&::f) f = nullptr;
@@ -275,6 +276,55 @@ PyObject* py_moe_combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const qg_stream st = g.stream();
         const Launch launch(g.device());
         return lib.moe_combine_backward(dy, rows, row, w, B, k, K, drows, dw, st);
+    });
+}
+
+PyObject* py_qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(a, n, 15, [](Arguments& g) {
+        const Address qkv{g.tensor()}, wq{g.tensor()}, wk{g.tensor()};
+        const float eps = g.real();
+        const Address pos{g.tensor()}, freq{g.tensor()};
+        const int rot = g.integer(), inter = g.integer(), T = g.integer(), Hq = g.integer(), Hkv = g.integer(),
+                  D = g.integer();
+        const Address q{g.tensor()}, k{g.tensor()};
+        const qg_stream st = g.stream();
+        const Launch launch(g.device());
+        return lib.qk_norm_rope(qkv, wq, wk, eps, pos, freq, rot, inter, T, Hq, Hkv, D, q, k, st);
+    });
+}
+PyObject* py_kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(a, n, 24, [](Arguments& g) {
+        const Address qkv{g.tensor()}, wq{g.tensor()}, wk{g.tensor()};
+        const float eps = g.real();
+        const Address freq{g.tensor()};
+        const int rot = g.integer(), inter = g.integer();
+        const Address offsets{g.tensor()}, len{g.tensor()}, table{g.tensor()};
+        const int T = g.integer(), B = g.integer(), max_pages = g.integer(), Hq = g.integer(), Hkv = g.integer(),
+                  D = g.integer();
+        const Address k{g.tensor()}, v{g.tensor()}, ks{g.tensor()}, vs{g.tensor()};
+        const int pages = g.integer(), page = g.integer();
+        const Address q{g.tensor()};
+        const qg_stream st = g.stream();
+        const Launch launch(g.device());
+        return lib.kv_append(qkv, wq, wk, eps, freq, rot, inter, offsets, len, table, T, B, max_pages, Hq, Hkv, D, k, v, ks,
+                             vs, pages, page, q, st);
+    });
+}
+PyObject* py_paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return call(a, n, 26, [](Arguments& g) {
+        const Address q{g.tensor()}, k{g.tensor()}, v{g.tensor()}, ks{g.tensor()}, vs{g.tensor()};
+        const int pages = g.integer(), page = g.integer();
+        const Address offsets{g.tensor()}, len{g.tensor()}, table{g.tensor()};
+        const int T = g.integer(), B = g.integer(), max_pages = g.integer(), Hq = g.integer(), Hkv = g.integer(),
+                  D = g.integer();
+        const float scale = g.real();
+        const int window = g.integer(), sinks = g.integer(), shared = g.integer(), max_q = g.integer();
+        const Address out{g.tensor()}, lse{g.tensor()}, ws{g.tensor()};
+        const size_t bytes = g.size();
+        const qg_stream st = g.stream();
+        const Launch launch(g.device());
+        return lib.paged_attention(q, k, v, ks, vs, pages, page, offsets, len, table, T, B, max_pages, Hq, Hkv, D, scale,
+                                   window, sinks, shared, max_q, out, lse, ws, bytes, st);
     });
 }
 

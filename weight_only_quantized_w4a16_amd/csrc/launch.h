@@ -123,4 +123,39 @@ void launch_moe_combine_backward(const uint16_t* dy, const uint16_t* rows, const
                                  const float* weights, int B, int k, int K, uint16_t* drows, float* dweights,
                                  hipStream_t st);
 
+// Between the qkv product and attention (rope.hip)
+struct RopeArgs {
+    const uint16_t* qkv;         // [T, Hq + 2 Hkv, D]
+    const uint16_t *wq, *wk;     // norm weights [D], or null
+    float eps;
+    const double* inv_freq;      // [rot / 2]
+    int rot, interleaved;
+    int T, Hq, Hkv;
+    uint16_t* q;                 // [T, Hq, D]
+    const int* positions;        // qk_norm_rope: [T], and k [T, Hkv, D]
+    uint16_t* k_dense;
+    const int *q_offsets, *kv_len, *table;      // kv_append: the batch and its cache
+    int B, max_pages, pages, page_shift;
+    void *k, *v;                 // [pages, Hkv, page, D]
+    float *k_scale, *v_scale;    // e4m3: [pages, Hkv, page], else null
+    int parts_shift;             // the launcher's
+};
+void launch_qk_norm_rope(const RopeArgs& p, int D, hipStream_t st);
+void launch_kv_append(const RopeArgs& p, int D, hipStream_t st);
+
+// Attention over a paged cache (attention.hip)
+struct AttentionArgs {
+    const uint16_t* q;           // [T, Hq, D]
+    const void *k, *v;           // [pages, Hkv, page, D]
+    const float *k_scale, *v_scale;             // e4m3: [pages, Hkv, page], else null
+    const int *q_offsets, *kv_len, *table;
+    int T, B, max_pages, Hq, Hkv, pages, page_shift;
+    float scale;
+    int window, sinks, prefix, max_q;
+    uint16_t* out;
+    float* lse;                  // or null
+};
+size_t paged_attention_workspace_bytes(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, int prefix, int max_q);
+void launch_paged_attention(const AttentionArgs& a, int D, void* ws, hipStream_t st);
+
 }  // namespace qg

@@ -102,6 +102,10 @@ _SIGS = {
     "moe_gather": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P]),
     "moe_combine": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P]),
     "moe_combine_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "qk_norm_rope": (_I, [_P, _P, _P, _F, _P, _P] + [_I] * 6 + [_P] * 3),
+    "kv_append": (_I, [_P, _P, _P, _F, _P, _I, _I, _P, _P, _P] + [_I] * 6 + [_P] * 4 + [_I, _I, _P, _P]),
+    "qg_paged_attention_workspace_bytes": (_SZ, [_I64] * 9),
+    "paged_attention": (_I, [_P] * 5 + [_I, _I, _P, _P, _P] + [_I] * 6 + [_F] + [_I] * 4 + [_P, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -366,6 +370,31 @@ def moe_combine(rows_bf16, row_of_slot, weights, residual_bf16, B, k, K, y_bf16,
 def moe_combine_backward(dy_bf16, rows_bf16, row_of_slot, weights, B, k, K, drows_bf16, dweights, stream=None):
     _check("moe_combine_backward", _calls.moe_combine_backward(dy_bf16, rows_bf16, row_of_slot, weights, B, k, K, drows_bf16,
                                                                dweights, stream))
+
+
+def qk_norm_rope(qkv_bf16, q_weight_bf16, k_weight_bf16, eps, positions, inv_freq, rotary_dim, interleaved, T, Hq, Hkv, D,
+                 q_bf16, k_bf16, stream=None):
+    _check("qk_norm_rope", _calls.qk_norm_rope(qkv_bf16, q_weight_bf16, k_weight_bf16, eps, positions, inv_freq, rotary_dim,
+                                               interleaved, T, Hq, Hkv, D, q_bf16, k_bf16, stream))
+
+
+def kv_append(qkv_bf16, q_weight_bf16, k_weight_bf16, eps, inv_freq, rotary_dim, interleaved, q_offsets, kv_len, block_table,
+              T, B, max_pages, Hq, Hkv, D, k_cache, v_cache, k_scale, v_scale, pages, page_size, q_bf16, stream=None):
+    _check("kv_append", _calls.kv_append(qkv_bf16, q_weight_bf16, k_weight_bf16, eps, inv_freq, rotary_dim, interleaved,
+                                         q_offsets, kv_len, block_table, T, B, max_pages, Hq, Hkv, D, k_cache, v_cache,
+                                         k_scale, v_scale, pages, page_size, q_bf16, stream))
+
+
+def paged_attention_workspace_bytes(T, B, max_pages, Hq, Hkv, D, page_size, shared_prefix=0, max_q=0):
+    return _lib.qg_paged_attention_workspace_bytes(T, B, max_pages, Hq, Hkv, D, page_size, shared_prefix, max_q)
+
+
+def paged_attention(q_bf16, k_cache, v_cache, k_scale, v_scale, pages, page_size, q_offsets, kv_len, block_table, T, B,
+                    max_pages, Hq, Hkv, D, scale, window, sinks, shared_prefix, max_q, out_bf16, lse=None, workspace=None,
+                    workspace_bytes=0, stream=None):
+    _check("paged_attention", _calls.paged_attention(q_bf16, k_cache, v_cache, k_scale, v_scale, pages, page_size, q_offsets,
+                                                     kv_len, block_table, T, B, max_pages, Hq, Hkv, D, scale, window, sinks,
+                                                     shared_prefix, max_q, out_bf16, lse, workspace, workspace_bytes, stream))
 
 
 # ---- tensor-level helpers (allocate outputs with torch, then call the above) --
