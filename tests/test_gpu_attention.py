@@ -18,11 +18,13 @@ def ops():
     return _ops
 
 
-def verify(ops, b, what, scale=None, window=0, sinks=0, shared=0, max_q=0):
-    announce(what)
-    out, lse = attend(ops, b, scale, window, sinks, shared, max_q)
+def verify(ops, b, what, scale=None, window=0, sinks=0, shared=0):
+    """Every kernel that the call may choose: by an unknown max_q, the real one, and one that is too small."""
     want = oracle.paged_attention(b.q, b.k, b.v, b.table, b.q_offsets, b.kv_len, scale or b.D ** -0.5, window, sinks)
-    return check(b, out, lse, want, what)
+    for m in (0, int(np.diff(b.q_offsets).max()), 1):
+        announce(f"{what} max_q={m}")
+        out, lse = attend(ops, b, scale, window, sinks, shared, m)
+        check(b, out, lse, want, f"{what} max_q={m}")
 
 
 # (new tokens, positions) of each sequence
@@ -66,3 +68,37 @@ def test_many_sequences(ops, fmt):
     new = [int(rng.integers(0, 3)) for _ in kv]
     b = Batch(new, kv.tolist(), 2, 1, 64, 16, fmt, seed=9)
     verify(ops, b, f"150 sequences {fmt}")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,kv", [([130], [130]), ([65, 3, 200], [400, 300, 200]), ([33, 1, 0, 17], [33, 500, 70, 1100])])
+def test_prefill(ops, new, kv, D, fmt):
+    for Hq, Hkv, page in ((6, 2, 16), (8, 1, 64), (2, 2, 128)):
+        b = Batch(new, kv, Hq, Hkv, D, page, fmt, seed=D + Hq, extra_tokens=3)
+        verify(ops, b, f"prefill {new} {kv} {fmt} D={D} Hq={Hq} Hkv={Hkv} page={page}")
+        verify(ops, b, f"prefill {new} {kv} {fmt} D={D} Hq={Hq} Hkv={Hkv} page={page} windowed", window=50, sinks=3)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("prefix,page", [(16, 16), (48, 16), (256, 256), (640, 64)])
+def test_shared_prefix(ops, prefix, page, fmt):
+    """The same as without it, also where a sequence's new tokens lie inside the prefix or where it has none."""
+    for new, more, D in (([1] * 5, [1, 9, 40, 2, 300], 128), ([2, 4, 1], [2, 70, 33], 64), ([40, 1, 0, 5], [50, 1, 0, 5], 64)):
+        kv = [prefix + m for m in more]
+        b = Batch(new, kv, 8, 2, D, page, fmt, seed=prefix + len(new), extra_tokens=1, shared=prefix)
+        want_table = b.table.copy()
+        b.table[1:, :prefix // page] = -1                # not read
+        want = oracle.paged_attention(b.q, b.k, b.v, want_table, b.q_offsets, b.kv_len, D ** -0.5)
+        for m in (0, max(new)):
+            what = f"shared {prefix} page {page} {fmt} new={new} max_q={m}"
+            announce(what)
+            out, lse = attend(ops, b, shared=prefix, max_q=m)
+            check(b, out, lse, want, what)
+        windowed = oracle.paged_attention(b.q, b.k, b.v, want_table, b.q_offsets, b.kv_len, D ** -0.5, 60, 5)
+        out, lse = attend(ops, b, shared=prefix, window=60, sinks=5)
+        check(b, out, lse, windowed, "windowed")
+    short = Batch([3, 1, 2], [prefix, 0, prefix + 20], 4, 2, 64, page, fmt, seed=1, shared=prefix)
+    want = oracle.paged_attention(short.q, short.k, short.v, short.table, short.q_offsets, short.kv_len, 0.125)
+    out, lse = attend(ops, short, shared=prefix)
+    check(short, out, lse, want, "new tokens inside the prefix")

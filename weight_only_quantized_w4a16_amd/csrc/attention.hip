@@ -20,8 +20,10 @@
 // multiplied one by one.  A row that sees no key is zero, its lse minus infinity.
 
 #include <algorithm>
+#include <atomic>
 
 #include "device_common.h"
+#include "formats.h"
 #include "launch.h"
 #include "rows.h"
 #include "sequences.h"
@@ -38,11 +40,17 @@ struct Call : AttentionArgs {
     float scale2;                // scale log2(e)
     // the plan
     int items;                   // work items for each key head at most, below 2^24
+    int few;                     // 1: sequences of up to kFewRows rows; 0: the others; -1: all
     int target;                  // chunks wanted for each key head over the whole batch; 0: keys are not split
     int least;                   // tiles of a chunk at least
     unsigned* counters;          // one a split row tile, zero between calls
     float* slots;                // partial results of chunks
+    // partial results of the shared prefix: [chunks, Hkv, T G] rows of D elements, (m, l) each
+    int prior_chunks;
+    float *prior, *prior_ml;
 };
+// rows of a sequence that the kernel of one row tile takes at once
+constexpr int kFewRows = 16;
 
 // Key tiles that some token of a sequence sees: [begin0, end0) around the first
 // positions and [begin1, end1), in tiles of TK positions.
@@ -79,7 +87,7 @@ struct Item {
 // whatever the lengths, and there are at most target + (row tiles) of them.  Every wave
 // finds the item `it` for itself, 64 sequences a step, on scans of DPP moves (false: there
 // is none).
-template <int BM, int TK>
+template <int BM, int TK, bool LAST_FIRST>
 __device__ __forceinline__ bool find_item(const Call& a, int it, Item& item) {
     const int lane = threadIdx.x & 63;
     const int blocks = (a.B + 63) >> 6;
@@ -89,7 +97,10 @@ __device__ __forceinline__ bool find_item(const Call& a, int it, Item& item) {
         hi = a.q_offsets[min(b + 1, a.B)];
         len = a.kv_len[min(b, a.B - 1)];
     };
-    auto rows_of = [&](const Sequence& s) { return (s.tokens * a.G + BM - 1) / BM; };
+    auto rows_of = [&](const Sequence& s) {
+        const int rows = s.tokens * a.G;
+        return a.few < 0 || (rows <= kFewRows) == (a.few != 0) ? (rows + BM - 1) / BM : 0;
+    };
     int chunk_tiles = 0x7fffffff;
     int lo, hi, len;
     load(0, lo, hi, len);
@@ -126,7 +137,9 @@ __device__ __forceinline__ bool find_item(const Call& a, int it, Item& item) {
             item.chunks = __builtin_amdgcn_readlane(chunks, src);
             item.chunk_tiles = __builtin_amdgcn_readfirstlane(chunk_tiles);
             const int at = it - __builtin_amdgcn_readlane(before, src);
-            item.row0 = at / item.chunks * BM;
+            const int tile = at / item.chunks;
+            // the last rows of a sequence see the most keys: their tiles begin first
+            item.row0 = (LAST_FIRST ? __builtin_amdgcn_readlane(rows, src) - 1 - tile : tile) * BM;
             item.chunk = at % item.chunks;
             item.first = it - item.chunk;
             item.span = span_of<TK>(a, item.s);
@@ -178,8 +191,25 @@ __device__ __forceinline__ u32x2 lds_columns_b8(uint32_t at) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(p));
 }
 template <class T>
+__device__ __forceinline__ void lds_write(uint32_t at, T v) {
+    *(__attribute__((address_space(3))) T*)(uintptr_t)at = v;
+}
+template <class T>
 __device__ __forceinline__ T lds_read(uint32_t at) {
     return *(const __attribute__((address_space(3))) T*)(uintptr_t)at;
+}
+
+// The order of N products whose operands come from LDS in READS reads each: AHEAD of them are
+// on their way before the first product, then one product's reads behind every product.  (Left
+// alone the compiler requests them all at once, into registers that it does not have.)
+template <int N, int READS, int AHEAD>
+__device__ __forceinline__ void feed_products() {
+    static_for<N>([](auto i) {
+        if constexpr (decltype(i)::value == 0) __builtin_amdgcn_sched_group_barrier(0x100, READS * AHEAD, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if constexpr (decltype(i)::value + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    });
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Eight e4m3 codes as bf16: exact.
@@ -190,6 +220,11 @@ __device__ __forceinline__ u32x4 e4m3_to_bf16(u32x2 c) {
     r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, false));
     r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, true));
     return r;
+}
+
+// Bits 0 .. n: none for a negative n, all from 63 on.
+__device__ __forceinline__ uint64_t bits_to(int n) {
+    return n < 0 ? 0ull : ~0ull >> (63 - min(n, 63));
 }
 
 // An infinity or NaN among eight bf16 values.
@@ -204,12 +239,25 @@ __device__ __forceinline__ bool nonfinite8(u32x4 v) {
 }
 
 // ---- the running softmax of one query column -------------------------------------
-// m: the largest score so far (base 2), in all lanes of the column; l: this lane's share
-// of the sum.
+// m: what is subtracted from the column's scores (base 2), the same in all its lanes; l:
+// this lane's share of the sum.  m follows the largest score only when that has grown by
+// more than kSlack: exponentials up to 2^kSlack cost fp32 sums and bf16 probabilities
+// nothing, and the running result is rarely rescaled after its first tile.
+constexpr float kSlack = 8.0f;
 struct Running {
     float m = -__builtin_inff(), l = 0.0f;
     // The reference to subtract: a column that has seen nothing keeps its exponentials at zero.
     __device__ __forceinline__ float reference() const { return m == -__builtin_inff() ? 0.0f : m; }
+    // whether a tile's largest score moves the reference
+    __device__ __forceinline__ bool outgrown(float top) const { return top > m + kSlack; }
+    // moves it in the lanes that need it; the factor of what was summed before
+    __device__ __forceinline__ float follow(float top) {
+        const float before = m;
+        if (outgrown(top)) m = top;
+        const float w = __builtin_amdgcn_exp2f(before - reference());
+        l *= w;
+        return w;
+    }
 };
 
 // Joins the partial results of a row's chunks, in order: `o` of N elements with (m, l).
@@ -311,7 +359,7 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
     const int c = lane & 15, g = lane >> 4;              // column (row of the tile), lane group
     const int h = blockIdx.x % a.Hkv;
     Item item;
-    if (!find_item<R::BM, R::TILE>(a, (int)(blockIdx.x / a.Hkv), item)) return;
+    if (!find_item<R::BM, R::TILE, false>(a, (int)(blockIdx.x / a.Hkv), item)) return;
     const int first_pos = item.s.len - item.s.tokens;
     const int rows = min(R::BM, item.s.tokens * a.G - item.row0);
     const int my_row = item.row0 + c;
@@ -443,11 +491,8 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
         top = fmaxf(top, t2);
         top = both32(top, t2);
         top = fmaxf(top, t2);
-        if (__ballot(top > run.m)) {
-            const float before = run.m;
-            run.m = fmaxf(run.m, top);
-            const float w = __builtin_amdgcn_exp2f(before - run.reference());
-            run.l *= w;
+        if (__ballot(run.outgrown(top))) {
+            const float w = run.follow(top);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) o[d] *= w;
         }
@@ -593,62 +638,574 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
     }
     if (!live) return;
     const int at = item.row0 + r;
+    for (int x = 0; x < a.prior_chunks; ++x) {
+        const int64_t row = ((int64_t)x * a.Hkv + h) * ((int64_t)a.T * a.G) + (int64_t)item.s.first_token * a.G + at;
+        j.add(a.prior_ml[2 * row], a.prior_ml[2 * row + 1], a.prior + row * D + d0);
+    }
     store_row<N>(a, D, (int64_t)(item.s.first_token + at / a.G) * a.Hq + h * a.G + at % a.G, d0, j);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows (prefill, several tokens a sequence, a prefix shared by a batch): a
+// workgroup takes a row tile of 128, each of its four waves 32 rows, and goes over tiles of 64
+// keys that all waves read from LDS.  bf16 tiles are copied straight into LDS one tile
+// ahead; e4m3 codes go through registers, where they become bf16 (exact, and once for
+// all waves), their scales beside them.
+//
+// Bound by the matrix instructions and, nearly as much, by the exponentials: two
+// workgroups on a CU let one wave's softmax run under another's products.
+// ---------------------------------------------------------------------------
+template <int D>
+struct Tiles {
+    static constexpr int WAVES = 4, BM = 32 * WAVES, TK = 64;
+    static constexpr int RB = 2 * D, PIECES = RB / 16;   // a row of a tile in LDS is bf16
+    static constexpr int KEYS = 64 / PIECES;             // keys of one copy
+    static constexpr int LOADS = 16 / KEYS;              // a wave copies 16 keys and 16 values
+    static constexpr int K0 = 0, V0 = TK * RB, KS = 2 * TK * RB, VS = KS + 4 * TK, LIVE = VS + 4 * TK;
+    static constexpr int BAD = LIVE + 16, STAGE = (BAD + 16 + 255) / 256 * 256;
+    static constexpr int ENDS = 2 * STAGE, FLAG = ENDS + 8 * WAVES;     // the waves' first and last positions; last arriver
+    static constexpr int LDS = FLAG + 16;
+    static constexpr int SLOT = BM * (D + 2);            // floats
+    __device__ static __forceinline__ int swap_k(int key) { return PIECES == 16 ? key & 15 : (key >> 1) & 7; }
+    __device__ static __forceinline__ int swap_v(int key) {
+        return PIECES == 16 ? (key & 3) * 4 + (key >> 2 & 1) * 2 : (key >> 1 & 1) * 4 + (key >> 2 & 1) * 2;
+    }
+};
+
+// PREFIX: the rows are all T tokens' and the keys the shared ones; partial results.
+template <int D, bool E4M3, bool PREFIX>
+__global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
+    using R = Tiles<D>;
+    extern __shared__ __attribute__((aligned(256))) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 31, hf = lane >> 5;             // column (row of the wave), half
+    const int h = blockIdx.x % a.Hkv;
+    Item item;
+    int total_rows;
+    if constexpr (PREFIX) {
+        item.chunks = a.target;
+        item.chunk_tiles = a.least;
+        item.chunk = blockIdx.x / a.Hkv % item.chunks;
+        item.row0 = blockIdx.x / a.Hkv / item.chunks * R::BM;
+        item.b = 0;
+        item.s = Sequence{0, a.T, a.prefix};
+        total_rows = a.T * a.G;
+    } else {
+        if (!find_item<R::BM, R::TK, true>(a, (int)(blockIdx.x / a.Hkv), item)) return;
+        total_rows = item.s.tokens * a.G;
+    }
+    const int my_row = item.row0 + 32 * wave + c;
+    const bool mine = my_row < total_rows;
+    const int token = item.s.first_token + min(my_row, total_rows - 1) / a.G;
+    const int head = h * a.G + min(my_row, total_rows - 1) % a.G;
+    int pos = -1;                                        // sees nothing
+    if constexpr (PREFIX) {
+        // the last offset that is not above the token
+        int lo = 0, hi = a.B;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.q_offsets[mid] <= token) lo = mid;
+            else hi = mid - 1;
+        }
+        if (mine && lo < a.B) {
+            const Sequence s = sequence_of(a.q_offsets[lo], a.q_offsets[lo + 1], a.kv_len[lo], a.T);
+            if (token >= s.first_token && token < s.first_token + s.tokens) pos = s.len - s.tokens + token - s.first_token;
+        }
+    } else if (mine) {
+        pos = item.s.len - item.s.tokens + (token - item.s.first_token);
+    }
+    pos = max(pos, -1);
+    // the wave's rows that exist: their first and last position
+    int pos_min = mine ? pos : 0x7fffffff, pos_max = mine ? pos : -1;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        pos_min = min(pos_min, __shfl_xor(pos_min, o, 64));
+        pos_max = max(pos_max, __shfl_xor(pos_max, o, 64));
+    }
+    pos_min = __builtin_amdgcn_readfirstlane(pos_min);
+    pos_max = __builtin_amdgcn_readfirstlane(pos_max);
+    // and the workgroup's
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
+    int all_min = pos_min, all_max = pos_max;
+    if (lane == 0) lds_write(lds0 + R::ENDS + 8 * wave, i32x2{pos_min, pos_max});
+    __syncthreads();
+    for (int w = 0; w < R::WAVES; ++w) {
+        const i32x2 ends = lds_read<i32x2>(lds0 + R::ENDS + 8 * w);
+        all_min = min(all_min, __builtin_amdgcn_readfirstlane(ends[0]));
+        all_max = max(all_max, __builtin_amdgcn_readfirstlane(ends[1]));
+    }
+    const int key_begin = PREFIX ? 0 : a.prefix;
+    const int limit = PREFIX ? a.prefix : (int)min((int64_t)item.s.len, (int64_t)a.max_pages << a.page_shift);
+
+    // the tiles: a chunk of the sequence's, less those that lie ahead of the whole row tile
+    int i0 = 0, tiles;
+    if constexpr (PREFIX) {
+        item.span = Span{0, 0, 0, (a.prefix + R::TK - 1) / R::TK};
+        i0 = item.chunk * item.chunk_tiles;
+        tiles = min(item.chunk_tiles, item.span.n - i0);
+    } else {
+        if (item.chunks > 1) {
+            i0 = item.chunk * item.chunk_tiles;
+            tiles = min(item.chunk_tiles, item.span.n - i0);
+            while (tiles > 0 && item.span.tile(i0 + tiles - 1) * R::TK > all_max) --tiles;
+        } else {
+            item.span = span_of<R::TK>(a, Sequence{0, all_max - all_min + 1, max(all_max + 1, 0)});
+            tiles = item.span.n;
+        }
+    }
+
+    const int* table = a.table + (int64_t)item.b * a.max_pages;
+    // a wave brings 16 keys of every tile; lane offsets from their first row
+    uint32_t koff[R::LOADS], voff[R::LOADS];
+#pragma unroll
+    for (int j = 0; j < R::LOADS; ++j) {
+        const int key = j * R::KEYS + lane / R::PIECES;
+        koff[j] = key * R::RB + ((lane % R::PIECES) ^ R::swap_k(key)) * 16;
+        voff[j] = key * R::RB + ((lane % R::PIECES) ^ R::swap_v(key)) * 16;
+    }
+    // the cache row of the wave's 16 keys of a tile, -1 where they have no page
+    auto row_of = [&](int i) {
+        const int key = item.span.tile(i0 + i) * R::TK + 16 * wave;
+        const int id = key < limit ? table[key >> a.page_shift] : -1;
+        return id >= 0 && id < a.pages
+            ? ((((int64_t)id * a.Hkv + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) : (int64_t)-1;
+    };
+    auto announce = [&](uint32_t stage, int64_t row) {
+        if (lane == 0) lds_write<int>(stage + R::LIVE + 4 * wave, row >= 0);
+    };
+    auto copy = [&](int i, int64_t row) {                // bf16
+        const uint32_t stage = lds0 + (i & 1) * R::STAGE, to = stage + 16 * wave * R::RB;
+        const int64_t at = max(row, (int64_t)0) * R::RB;
+#pragma unroll
+        for (int j = 0; j < R::LOADS; ++j) {
+            lds_copy_b128(static_cast<const unsigned char*>(a.k) + at, koff[j], to + R::K0 + j * 1024);
+            lds_copy_b128(static_cast<const unsigned char*>(a.v) + at, voff[j], to + R::V0 + j * 1024);
+        }
+        announce(stage, row);
+    };
+    // e4m3: 16 codes a lane and load; the lane's key and piece of the wave's 16 keys
+    constexpr int CLOADS = D / 64;                       // 16 D codes of keys, 16 bytes a lane
+    u32x4 kc[CLOADS], vc[CLOADS];
+    float sc = 0.0f;
+    int64_t held_row = -1;
+    auto fetch = [&](int64_t row) {
+        held_row = row;
+        const int64_t at = max(row, (int64_t)0);
+#pragma unroll
+        for (int j = 0; j < CLOADS; ++j) {
+            kc[j] = *reinterpret_cast<const u32x4*>(static_cast<const unsigned char*>(a.k) + at * D + j * 1024 + lane * 16);
+            vc[j] = *reinterpret_cast<const u32x4*>(static_cast<const unsigned char*>(a.v) + at * D + j * 1024 + lane * 16);
+        }
+        if (lane < 32) sc = (lane < 16 ? a.k_scale : a.v_scale)[at + (lane & 15)];
+    };
+    auto place = [&](int i) {
+        const uint32_t stage = lds0 + (i & 1) * R::STAGE;
+#pragma unroll
+        for (int j = 0; j < CLOADS; ++j) {
+            const int key = (j * 1024 + lane * 16) / D, piece = (j * 1024 + lane * 16) % D / 8;
+            const uint32_t row = stage + (16 * wave + key) * R::RB;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const u32x4 k = e4m3_to_bf16(x ? u32x2{kc[j].z, kc[j].w} : u32x2{kc[j].x, kc[j].y});
+                const u32x4 v = e4m3_to_bf16(x ? u32x2{vc[j].z, vc[j].w} : u32x2{vc[j].x, vc[j].y});
+                lds_write(row + R::K0 + ((piece + x) ^ R::swap_k(key)) * 16, k);
+                lds_write(row + R::V0 + ((piece + x) ^ R::swap_v(key)) * 16, v);
+            }
+        }
+        if (lane < 32) lds_write(stage + (lane < 16 ? R::KS : R::VS) + 4 * (16 * wave + (lane & 15)), sc);
+        announce(stage, held_row);
+    };
+
+    // a lane's place in a tile: its key's row with the first of its pieces, from which piece 2 ks (a
+    // step of keys) and 4 d (a block of values) away is an exclusive or (stages and rows are
+    // multiples of what it changes)
+    const uint32_t kat = R::K0 + c * R::RB + (hf ^ R::swap_k(c)) * 16;
+    const int vkey = 4 * hf + (lane >> 2 & 3);
+    const uint32_t vat = R::V0 + vkey * R::RB + ((2 * (c >> 4) + (lane >> 1 & 1)) ^ R::swap_v(vkey)) * 16 + (lane & 1) * 8;
+
+    // this lane's query: 8 elements of every 16, negated for a negative scale
+    bf16x8 q[D / 16];
+    {
+        const uint16_t* from = a.q + ((int64_t)token * a.Hq + head) * D + 8 * hf;
+        const uint32_t sign = a.scale2 < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+            q[ks] = as_bf16x8(*reinterpret_cast<const u32x4*>(from + 16 * ks) ^ u32x4{sign, sign, sign, sign});
+    }
+    const float scale2 = fabsf(a.scale2);
+
+    if (tiles > 0) {
+        if constexpr (E4M3) {
+            fetch(row_of(0));
+            place(0);
+        } else {
+            copy(0, row_of(0));
+        }
+    }
+
+    Running run;
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
+
+    for (int i = 0; i < tiles; ++i) {
+        // this tile has arrived, and every wave is done with the one before it
+        if constexpr (!E4M3) wait_vmem<0>();
+        __syncthreads();
+        if (i + 1 < tiles) {
+            if constexpr (E4M3) fetch(row_of(i + 1));
+            else copy(i + 1, row_of(i + 1));
+        }
+        const int key0 = item.span.tile(i0 + i) * R::TK;
+        const uint32_t stage = lds0 + (i & 1) * R::STAGE;
+        const auto whole_for = [&](int first, int last) {
+            return key0 >= key_begin && key0 + R::TK <= limit && key0 + R::TK - 1 <= first &&
+                   (a.window <= 0 || key0 > last - a.window || key0 + R::TK - 1 < a.sinks);
+        };
+        const i32x4 live4 = lds_read<i32x4>(stage + R::LIVE);
+        const bool live = __builtin_amdgcn_readfirstlane(live4[0] & live4[1] & live4[2] & live4[3]) != 0;
+        const bool whole = live && whole_for(pos_min, pos_max);
+        // Where a row of the workgroup does not see all keys: values of positions that hold no key
+        // become zeros (a wave its own 16), and an infinity or NaN among the others is found.
+        const bool clean = live && whole_for(all_min, all_max);
+        bool bad = false;
+        if (!clean) {
+            const bool page = live4[wave] != 0;
+            bool odd = false;
+#pragma unroll
+            for (int j = 0; j < R::LOADS; ++j) {
+                const int key = 16 * wave + j * R::KEYS + lane / R::PIECES;
+                const uint32_t at = stage + R::V0 + 16 * wave * R::RB + j * 1024 + 16 * lane;
+                if (page && key0 + key < limit) odd |= nonfinite8(lds_read<u32x4>(at));
+                else lds_write(at, u32x4{0u, 0u, 0u, 0u});
+            }
+            if (E4M3 && lane < 16) {
+                const uint32_t at = stage + R::VS + 4 * (16 * wave + lane);
+                if (page && key0 + 16 * wave + lane < limit) odd |= !__builtin_isfinite(lds_read<float>(at));
+                else lds_write(at, 0.0f);
+            }
+            const uint64_t some = __ballot(odd);
+            if (lane == 0) lds_write<int>(stage + R::BAD + 4 * wave, some != 0);
+            __syncthreads();
+            const i32x4 found = lds_read<i32x4>(stage + R::BAD);
+            bad = __builtin_amdgcn_readfirstlane(found[0] | found[1] | found[2] | found[3]) != 0;
+        }
+        // the keys of the tile that this lane's row sees, its half's first key in bit 0
+        const auto seen_keys = [&] {
+            uint64_t m = ~0ull;
+            if (a.window > 0) m = ~bits_to(pos - a.window - key0) | bits_to(a.sinks - 1 - key0);
+            m &= bits_to(min(pos, limit - 1) - key0) & ~bits_to(key_begin - 1 - key0);
+#pragma unroll
+            for (int w = 0; w < R::WAVES; ++w)
+                if (!__builtin_amdgcn_readfirstlane(live4[w])) m &= ~(0xffffull << (16 * w));
+            return m >> (4 * hf);
+        };
+        const bool useful = key0 <= pos_max && (a.window <= 0 || key0 + R::TK > pos_min - a.window || key0 < a.sinks);
+        if (useful) {
+            // S^T: lane (c, hf) receives keys 32 x + 8 (e / 4) + 4 hf + e % 4 of column c
+            f32x16 s[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[x][e] = 0.0f;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const u32x4 k = lds_read<u32x4>(((stage + kat) ^ (32 * ks)) + 32 * x * R::RB);
+                    s[x] = mfma_bf16_32x32x16(as_bf16x8(k), q[ks], s[x]);
+                }
+            feed_products<D / 8, 1, 4>();
+            if constexpr (E4M3) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const f32x4 k = lds_read<f32x4>(stage + R::KS + (32 * x + 2 * e + 4 * hf) * 4);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) s[x][e + r] *= k[r];
+                    }
+            }
+            if (!whole) {
+                const uint64_t seen = seen_keys();
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t w = (uint32_t)(seen >> (32 * x));
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        s[x][e] = w & (1u << (8 * (e >> 2) + (e & 3))) ? s[x][e] : -__builtin_inff();
+                }
+            }
+            float top = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+            for (int e = 1; e < 16; ++e) top = fmaxf(top, fmaxf(s[0][e], s[1][e]));
+            float t2;
+            top = both32(top, t2);
+            top = fmaxf(top, t2) * scale2;
+            if (__ballot(run.outgrown(top))) {
+                const float w = run.follow(top);
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d) o[d] *= w;
+            }
+            const float ref = run.reference();
+            // P^T: the operand of 16 keys is eight neighbouring results
+            u32x4 p[4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        f[e] = __builtin_amdgcn_exp2f(fmaf(s[x][8 * y + e], scale2, -ref));
+                        run.l += f[e];
+                    }
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int e = 0; e < 8; e += 4) {
+                            const f32x4 v = lds_read<f32x4>(stage + R::VS + (32 * x + 16 * y + 2 * e + 4 * hf) * 4);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                f[e + r] *= v[r];
+                        }
+                    }
+                    p[2 * x + y] = pack8(f);
+                }
+            // V^T: lane (c, hf) takes element 32 d + c of keys 16 y + 4 hf .. and 16 y + 8 + 4 hf ..
+            auto values = [&](int d, int y) {
+                const uint32_t at = ((stage + vat) ^ (64 * d)) + 16 * y * R::RB;
+                const u32x2 v0 = lds_columns_b16(at), v1 = lds_columns_b16(at + 8 * R::RB);
+                return u32x4{v0.x, v0.y, v1.x, v1.y};
+            };
+            if (whole || !bad) {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                    for (int d = 0; d < D / 32; ++d)
+                        o[d] = mfma_bf16_32x32x16(as_bf16x8(values(d, y)), as_bf16x8(p[y]), o[d]);
+                feed_products<D / 8, 2, 4>();
+            } else {
+                // column by column, with zeros for what that column does not see (a probability times a scale
+                // that is not finite is a zero there, too)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const uint32_t w = (uint32_t)(seen_keys() >> (16 * y));
+                    const uint32_t mine8 = (w & 15u) | (w >> 4 & 0xf0u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        p[y][e] &= (mine8 >> (2 * e) & 1 ? 0xffffu : 0u) | (mine8 >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+#pragma unroll 1
+                    for (int col = 0; col < 32; ++col) {
+                        const uint32_t its = __shfl(mine8, col + 32 * hf, 64);
+                        u32x4 keep;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            keep[e] = (its >> (2 * e) & 1 ? 0xffffu : 0u) | (its >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int d = 0; d < D / 32; ++d) {
+                            const f32x16 r = mfma_bf16_32x32x16(as_bf16x8(values(d, y) & keep), as_bf16x8(p[y]), o[d]);
+                            if (c == col) o[d] = r;
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                }
+            }
+        }
+        if constexpr (E4M3)
+            if (i + 1 < tiles) place(i + 1);
+    }
+
+    float t2;
+    float l = both32(run.l, t2);
+    l += t2;
+    float m = run.m;
+    // element 32 d + 8 y + 4 hf + r of the row is o[d][4 y + r]
+    if constexpr (PREFIX) {
+        if (!mine) return;
+        const int64_t row = ((int64_t)item.chunk * a.Hkv + h) * total_rows + my_row;
+        float* to = a.prior + row * D + 4 * hf;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                *reinterpret_cast<f32x4*>(to + 32 * d + 8 * y) = f32x4{o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]};
+        if (hf == 0) *reinterpret_cast<f32x2*>(a.prior_ml + 2 * row) = f32x2{m, l};
+        return;
+    }
+    // joins another part of this row, its elements given four at a time
+    auto join = [&](float m2, float l2, auto&& part) {
+        const float m1 = fmaxf(m, m2);
+        const float ref = m1 == -__builtin_inff() ? 0.0f : m1;
+        const float w1 = __builtin_amdgcn_exp2f(m - ref), w2 = __builtin_amdgcn_exp2f(m2 - ref);
+        m = m1;
+        l = l * w1 + l2 * w2;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const f32x4 v = part(32 * d + 8 * y + 4 * hf);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[d][4 * y + r] = o[d][4 * y + r] * w1 + v[r] * w2;
+            }
+    };
+    if (item.chunks > 1) {
+        float* slot = a.slots + ((int64_t)item.first * a.Hkv + (int64_t)h * item.chunks) * R::SLOT;
+        const int r = 32 * wave + c;
+        if (mine) {
+            float* to = slot + (int64_t)item.chunk * R::SLOT;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float v[4] = {o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]};
+                    store_agent<4>(to + r * D + 32 * d + 8 * y + 4 * hf, v);
+                }
+            const float ml[2] = {m, l};
+            if (hf == 0) store_agent<2>(to + R::BM * D + 2 * r, ml);
+        }
+        unsigned* counter = a.counters + (int64_t)item.first * a.Hkv + h;
+        if (!arrive_and_check_last(counter, item.chunks, reinterpret_cast<int*>(smem + R::FLAG))) return;
+        if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (!mine) return;
+        m = -__builtin_inff();
+        l = 0.0f;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
+        for (int x = 0; x < item.chunks; ++x) {
+            const float* from = slot + (int64_t)x * R::SLOT;
+            float ml[2];
+            load_agent<2>(from + R::BM * D + 2 * r, ml);
+            join(ml[0], ml[1], [&](int at) {
+                float v[4];
+                load_agent<4>(from + r * D + at, v);
+                return f32x4{v[0], v[1], v[2], v[3]};
+            });
+        }
+    }
+    if (!mine) return;
+    for (int x = 0; x < a.prior_chunks; ++x) {
+        const int64_t row = ((int64_t)x * a.Hkv + h) * ((int64_t)a.T * a.G) + (int64_t)token * a.G + my_row % a.G;
+        join(a.prior_ml[2 * row], a.prior_ml[2 * row + 1],
+             [&](int at) { return *reinterpret_cast<const f32x4*>(a.prior + row * D + at); });
+    }
+    const int64_t row = (int64_t)token * a.Hq + head;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            Joined<4> j;
+            j.m = m;
+            j.l = l;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) j.o[r] = o[d][4 * y + r];
+            store_row<4>(a, D, row, 32 * d + 8 * y + 4 * hf, j);
+        }
 }
 
 // ---------------------------------------------------------------------------
 // The plan of a call, from its sizes alone.
 // ---------------------------------------------------------------------------
 struct Plan {
-    int items;                   // work items for each key head at most
-    int target, least;
-    size_t slots;                // floats
+    bool rows, tiles;            // which kernels run
+    int row_items, row_target;   // their work items for each key head at most; chunks wanted (0: keys are not split)
+    int tile_items, tile_target;
+    int prior_chunks, prior_tiles;       // of the shared prefix: chunks, and key tiles of one
+    size_t slots, prior;         // floats
+    size_t bytes() const { return slots + prior ? kCounterBytes + (slots + prior) * 4 : 0; }
 };
 
-// Chunks are worth their hand-over from 256 keys on, and only while the row tiles leave
-// workgroup slots free.
-Plan plan_rows(int T, int B, int Hq, int Hkv, int D, int64_t max_kv) {
-    const int G = Hq / Hkv;
-    const int64_t tiles = std::min<int64_t>((int64_t)T * G, (int64_t)T * G / 16 + B);      // row tiles at most
-    Plan p{(int)tiles, 0, 2, 0};
-    const int64_t want = 4 * (int64_t)device_cu_count() / Hkv;
-    if (tiles < want && max_kv > 256 && (tiles + want) * Hkv <= kMaxCounters) {
-        p.target = (int)want;
-        p.items = (int)(tiles + want);
-        p.slots = (size_t)p.items * Hkv * 16 * (D + 2);
+Plan plan_of(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, int prefix, int max_q) {
+    const int64_t G = Hq / Hkv, all = (int64_t)T * G;
+    const int64_t cus = device_cu_count();
+    Plan p{};
+    // Sequences of up to 16 rows stream their keys; more rows are worth tiles.  A ragged
+    // batch (fewer tokens than B times the largest count) holds both.
+    p.rows = max_q > 0 && max_q * G <= kFewRows;
+    p.tiles = !p.rows;
+    if (p.tiles && B > 1 && !(max_q > 0 && (int64_t)max_q * B == T)) p.rows = true;
+    const int64_t own = max_kv - prefix;
+    // Keys are split while row tiles leave workgroups free: four a CU, each of 256 keys at least
+    // (rows), two a CU of 256 keys at least (tiles).
+    auto split = [&](int64_t tiles, int64_t want, int BM, int& items, int& target) {
+        items = (int)tiles;
+        if (tiles < want && own > 256 && (tiles + want) * Hkv <= kMaxCounters) {
+            target = (int)want;
+            items = (int)(tiles + want);
+            p.slots = std::max(p.slots, (size_t)items * Hkv * BM * (D + 2));
+        }
+    };
+    if (p.rows) split(std::min(all, all / 16 + B), std::max<int64_t>(4 * cus / Hkv, 1), 16, p.row_items, p.row_target);
+    if (p.tiles) split(std::min(all, all / 128 + B), std::max<int64_t>(2 * cus / Hkv, 1), 128, p.tile_items, p.tile_target);
+    if (prefix > 0) {
+        const int64_t tiles = (prefix + 63) / 64, rows = (all + 127) / 128;
+        const int64_t chunks = std::clamp<int64_t>(2 * cus / (rows * Hkv), 1, (tiles + 3) / 4);
+        p.prior_tiles = (int)((tiles + chunks - 1) / chunks);
+        p.prior_chunks = (int)((tiles + p.prior_tiles - 1) / p.prior_tiles);
+        p.prior = (size_t)p.prior_chunks * Hkv * all * (D + 2);
     }
     return p;
 }
 
+template <class Kernel>
+void launch(Kernel* kernel, std::atomic<uint64_t>& done, int64_t workgroups, int lds, const Call& a, hipStream_t st) {
+    allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds, done);
+    kernel<<<dim3((unsigned)workgroups), 256, lds, st>>>(a);
+}
+
 template <int D, bool E4M3>
-void launch_rows(Call a, const Plan& p, void* ws, hipStream_t st) {
+void launch_all(Call a, const Plan& p, void* ws, hipStream_t st) {
     using R = Rows<D, E4M3>;
-    a.items = p.items;
-    a.target = p.target;
-    a.least = p.least;
+    using M = Tiles<D>;
+    static std::atomic<uint64_t> rows_done{0}, tiles_done{0}, prior_done{0};
     a.counters = static_cast<unsigned*>(ws);
     a.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kCounterBytes);
-    static std::atomic<uint64_t> done{0};
-    allow_dynamic_lds(reinterpret_cast<const void*>(&attention_rows_kernel<D, E4M3>), R::WAVES * R::WAVE_BYTES, done);
-    attention_rows_kernel<D, E4M3><<<dim3((unsigned)(p.items * a.Hkv)), 256, R::WAVES * R::WAVE_BYTES, st>>>(a);
+    a.prior = a.slots + p.slots;
+    const int64_t rows = (int64_t)a.T * a.G;
+    a.prior_ml = a.prior + (size_t)p.prior_chunks * a.Hkv * rows * D;
+    if (p.prior_chunks) {
+        Call c = a;
+        c.target = p.prior_chunks;
+        c.least = p.prior_tiles;
+        launch(&attention_tiles_kernel<D, E4M3, true>, prior_done, (rows + M::BM - 1) / M::BM * p.prior_chunks * a.Hkv, M::LDS, c, st);
+    }
+    a.prior_chunks = p.prior_chunks;
+    if (p.tiles) {
+        Call c = a;
+        c.few = p.rows ? 0 : -1;
+        c.items = p.tile_items;
+        c.target = p.tile_target;
+        c.least = 4;
+        launch(&attention_tiles_kernel<D, E4M3, false>, tiles_done, (int64_t)c.items * a.Hkv, M::LDS, c, st);
+    }
+    if (p.rows) {
+        a.few = p.tiles ? 1 : -1;
+        a.items = p.row_items;
+        a.target = p.row_target;
+        a.least = 2;
+        launch(&attention_rows_kernel<D, E4M3>, rows_done, (int64_t)a.items * a.Hkv, R::WAVES * R::WAVE_BYTES, a, st);
+    }
 }
 
 }  // namespace
 
-size_t paged_attention_workspace_bytes(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, int, int) {
-    if (T == 0 || B == 0) return 0;
-    const size_t floats = plan_rows(T, B, Hq, Hkv, D, max_kv).slots;
-    return floats ? kCounterBytes + floats * 4 : 0;
+size_t paged_attention_workspace_bytes(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, int prefix, int max_q) {
+    return T == 0 || B == 0 ? 0 : plan_of(T, B, max_kv, Hq, Hkv, D, prefix, max_q).bytes();
 }
 
 void launch_paged_attention(const AttentionArgs& args, int D, void* ws, hipStream_t st) {
     Call a{args};
     a.G = a.Hq / a.Hkv;
     a.scale2 = a.scale * 1.44269504088896340736f;
-    a.prefix = 0;                // the shared pages are read by every sequence for itself
-    const Plan p = plan_rows(a.T, a.B, a.Hq, a.Hkv, D, (int64_t)a.max_pages << a.page_shift);
-    if (D == 64) a.k_scale ? launch_rows<64, true>(a, p, ws, st) : launch_rows<64, false>(a, p, ws, st);
-    else a.k_scale ? launch_rows<128, true>(a, p, ws, st) : launch_rows<128, false>(a, p, ws, st);
+    const Plan p = plan_of(a.T, a.B, (int64_t)a.max_pages << a.page_shift, a.Hq, a.Hkv, D, a.prefix, a.max_q);
+    if (D == 64) a.k_scale ? launch_all<64, true>(a, p, ws, st) : launch_all<64, false>(a, p, ws, st);
+    else a.k_scale ? launch_all<128, true>(a, p, ws, st) : launch_all<128, false>(a, p, ws, st);
 }
 
 }  // namespace qg
