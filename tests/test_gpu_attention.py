@@ -102,3 +102,61 @@ def test_shared_prefix(ops, prefix, page, fmt):
     want = oracle.paged_attention(short.q, short.k, short.v, short.table, short.q_offsets, short.kv_len, 0.125)
     out, lse = attend(ops, short, shared=prefix)
     check(short, out, lse, want, "new tokens inside the prefix")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,kv,window", [([5], [20], 0), ([90, 3], [150, 130], 0), ([90], [150], 16), ([4, 1], [200, 9], 16)])
+def test_values_that_are_not_finite_reach_only_rows_that_see_them(ops, fmt, new, kv, window):
+    """Infinite and NaN values (and, in 8 bits, a NaN code and an infinite scale) at a few positions: rows that see one are
+    not finite in its elements, all others are as if they were not there."""
+    b = Batch(new, kv, 4, 2, 64, 16, fmt, seed=7)
+    spots = []                                               # (sequence, position, element)
+    for s, n in enumerate(kv):
+        for p in {n - 1, n - 2, max(0, n - new[s] // 2), max(0, n - 40)}:
+            spots.append((s, p, int((7 * p + 3) % 64)))
+    for i, (s, p, e) in enumerate(spots):
+        page, slot = b.table[s, p // 16], p % 16
+        if fmt == "bf16":
+            x = [float("inf"), float("-inf"), float("nan")][i % 3]
+            b.v[page, :, slot, e] = x
+            b.v_t[page, :, slot, e] = x
+        elif p < kv[s] - 1:
+            b.v[page, :, slot, e] = np.nan
+            b.v_t[page, :, slot, e] = 0x7f
+        else:
+            b.v_scale_t[page, :, slot] = float("inf")        # the whole row: infinities, NaN where the code is zero
+            b.v[page, :, slot] = np.inf
+    want, l64, mean, reach = oracle.paged_attention(b.q, b.k, b.v, b.table, b.q_offsets, b.kv_len, 0.125, window, 0)
+    fine = np.isfinite(want)
+    assert fine.any() and not fine.all()
+    for m in (0, max(new)):
+        announce(f"values {fmt} {new} {kv} window {window} max_q={m}")
+        out, lse = attend(ops, b, 0.125, window=window, max_q=m)
+        got = out.double().cpu().numpy()
+        assert np.array_equal(np.isfinite(got), fine), np.argwhere(np.isfinite(got) != fine)[:5]
+        lim = 2.0 ** -7 * np.where(fine, mean, 0) + 2.0 ** -8 * np.abs(np.where(fine, want, 0)) + 1e-6
+        assert (np.abs(np.where(fine, got - want, 0)) <= lim).all()
+
+
+def test_keys_that_are_not_finite(ops):
+    """A NaN key makes the rows that see it NaN, an infinite one those whose scores it leaves infinite; the others stay."""
+    for new, kv in (([3], [40]), ([80], [140])):
+        b = Batch(new, kv, 2, 1, 64, 16, seed=2)
+        p = kv[0] - 2
+        page, slot = b.table[0, p // 16], p % 16
+        b.k[page, :, slot, 5] = np.nan
+        b.k_t[page, :, slot, 5] = float("nan")
+        want = oracle.paged_attention(b.q, b.k, b.v, b.table, b.q_offsets, b.kv_len, 0.125)
+        out, lse = attend(ops, b, 0.125)
+        got = out.double().cpu().numpy()
+        sees = np.arange(kv[0] - new[0], kv[0]) >= p
+        assert np.isnan(got[sees]).all() and np.isnan(lse.cpu().numpy()[sees]).all()
+        assert (np.abs(got - want[0]) <= 2.0 ** -7 * want[2] + 2.0 ** -8 * np.abs(want[0]) + 1e-6)[~sees].all()
+
+
+def test_scores_of_any_size_and_sign(ops):
+    """Large scores (one key takes all), a negative and a zero scale."""
+    for new, kv in (([2], [50]), ([40], [90])):
+        b = Batch(new, kv, 4, 2, 64, 16, seed=4)
+        for scale in (30.0, -0.125, 1e-30):
+            verify(ops, b, f"scale {scale} new={new}", scale=scale)

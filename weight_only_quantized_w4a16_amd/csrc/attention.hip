@@ -45,6 +45,8 @@ struct Call : AttentionArgs {
     int least;                   // tiles of a chunk at least
     unsigned* counters;          // one a split row tile, zero between calls
     float* slots;                // partial results of chunks
+    bool stream;                 // the cache is read once, past the caches
+    int shared;                  // positions below are found by row 0 of the table
     // partial results of the shared prefix: [chunks, Hkv, T G] rows of D elements, (m, l) each
     int prior_chunks;
     float *prior, *prior_ml;
@@ -86,8 +88,8 @@ struct Item {
 // chunk's length follows from the whole batch: total / target tiles, so that chunks are alike
 // whatever the lengths, and there are at most target + (row tiles) of them.  Every wave
 // finds the item `it` for itself, 64 sequences a step, on scans of DPP moves (false: there
-// is none).
-template <int BM, int TK, bool LAST_FIRST>
+// is none).  BY_TILE: `it` numbers the row tiles, the item is the tile's first chunk.
+template <int BM, int TK, bool LAST_FIRST, bool BY_TILE = false>
 __device__ __forceinline__ bool find_item(const Call& a, int it, Item& item) {
     const int lane = threadIdx.x & 63;
     const int blocks = (a.B + 63) >> 6;
@@ -115,7 +117,7 @@ __device__ __forceinline__ bool find_item(const Call& a, int it, Item& item) {
         total = wave_sum(total);
         chunk_tiles = max(a.least, (int)fmin(ceil(total / a.target), 2147483647.0));
     }
-    int carry = 0;
+    int carry = 0, carry_items = 0;
     for (int j = 0; j < blocks; ++j) {
         const int b = 64 * j + lane;
         const Sequence s = sequence_of(lo, hi, len, a.T);
@@ -124,8 +126,10 @@ __device__ __forceinline__ bool find_item(const Call& a, int it, Item& item) {
         const int n = span_of<TK>(a, s).n;
         const int chunks = a.target > 0 ? max(1, (n - 1) / chunk_tiles + 1) : 1;
         // (a count past the grid is as good as any other: sums stay inside an int)
-        const int count = (int)min((int64_t)rows * chunks, (int64_t)1 << 24);
+        const int items = (int)min((int64_t)rows * chunks, (int64_t)1 << 24);
+        const int count = BY_TILE ? rows : items;
         const int incl = wave_scan(count) + carry;
+        const int incl_items = BY_TILE ? wave_scan(items) + carry_items : incl;
         const int total = __builtin_amdgcn_readlane(incl, 63);
         if (it < total) {
             const int before = incl - count;
@@ -135,18 +139,19 @@ __device__ __forceinline__ bool find_item(const Call& a, int it, Item& item) {
             item.s.tokens = __builtin_amdgcn_readlane(s.tokens, src);
             item.s.len = __builtin_amdgcn_readlane(s.len, src);
             item.chunks = __builtin_amdgcn_readlane(chunks, src);
-            item.chunk_tiles = __builtin_amdgcn_readfirstlane(chunk_tiles);
             const int at = it - __builtin_amdgcn_readlane(before, src);
-            const int tile = at / item.chunks;
+            const int tile = BY_TILE ? at : at / item.chunks;
             // the last rows of a sequence see the most keys: their tiles begin first
             item.row0 = (LAST_FIRST ? __builtin_amdgcn_readlane(rows, src) - 1 - tile : tile) * BM;
-            item.chunk = at % item.chunks;
-            item.first = it - item.chunk;
+            item.chunk = BY_TILE ? 0 : at % item.chunks;
+            item.first = BY_TILE ? __builtin_amdgcn_readlane(incl_items - items, src) + tile * item.chunks : it - item.chunk;
             item.span = span_of<TK>(a, item.s);
+            item.chunk_tiles = (item.span.n + item.chunks - 1) / item.chunks;
             // offsets that do not ascend may ask for more than the grid holds: such a tile is left out whole
             return item.first + item.chunks <= a.items;
         }
         carry = total;
+        if (BY_TILE) carry_items = __builtin_amdgcn_readlane(incl_items, 63);
     }
     return false;
 }
@@ -167,6 +172,10 @@ __device__ __forceinline__ float both32(float v, float& other) {
 __device__ __forceinline__ void lds_copy_b128(const void* base, uint32_t off, uint32_t lds) {
     asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
+// The same past the caches (bytes that nothing reads again soon).
+__device__ __forceinline__ void lds_copy_b128_nt(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("global_load_lds_dwordx4 %0, %1 nt" : : "v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
 // 4 bytes a lane from src to lds + 4 lane
 __device__ __forceinline__ void lds_copy_b32(const void* src, uint32_t lds) {
     asm volatile("global_load_lds_dword %0, off" : : "v"(src), "{m0}"(lds) : "memory");
@@ -174,6 +183,32 @@ __device__ __forceinline__ void lds_copy_b32(const void* src, uint32_t lds) {
 template <int N>
 __device__ __forceinline__ void wait_vmem() {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// Waits for all but the copies of the tiles behind this one: `left` remain, at most MOST have
+// been requested.
+template <int COPIES, int MOST>
+__device__ __forceinline__ void wait_tiles(int left) {
+    if (left >= MOST) wait_vmem<MOST * COPIES>();
+    else if (MOST > 1 && left == MOST - 1) wait_vmem<(MOST > 1 ? MOST - 1 : 0) * COPIES>();
+    else if (MOST > 2 && left == MOST - 2) wait_vmem<(MOST > 2 ? MOST - 2 : 0) * COPIES>();
+    else wait_vmem<0>();
+}
+// Waits for all but the copies behind what is needed: `first` of them, and TILE for each of
+// the tiles that follow in LDS (`left` remain, at most NS - 1 are there).
+template <int NS, int TILE, int FIRST>
+__device__ __forceinline__ void wait_behind(int left, bool first = true) {
+    if (first) {
+        if (left >= NS - 1) wait_vmem<(NS - 1) * TILE + FIRST>();
+        else if (NS > 2 && left == NS - 2) wait_vmem<(NS > 2 ? NS - 2 : 0) * TILE + FIRST>();
+        else if (NS > 3 && left == NS - 3) wait_vmem<(NS > 3 ? NS - 3 : 0) * TILE + FIRST>();
+        else wait_vmem<FIRST>();
+    } else {
+        if (NS > 1 && left >= NS - 1) wait_vmem<(NS - 1) * TILE>();
+        else if (NS > 2 && left == NS - 2) wait_vmem<(NS > 2 ? NS - 2 : 0) * TILE>();
+        else if (NS > 3 && left == NS - 3) wait_vmem<(NS > 3 ? NS - 3 : 0) * TILE>();
+        else wait_vmem<0>();
+    }
 }
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
@@ -222,6 +257,27 @@ __device__ __forceinline__ u32x4 e4m3_to_bf16(u32x2 c) {
     return r;
 }
 
+// An entry of a list that is the same for the whole wave and does not change under the
+// launch: a scalar load, which waits for no copy in flight (as a vector load it would
+// share their counter, and wait for all of them).
+__device__ __forceinline__ int load_scalar(const int* p) {
+    return *(const __attribute__((address_space(4))) int*)(uintptr_t)p;
+}
+
+// Ends the compiler's wait for loaded registers here.  It does not know the copies to LDS:
+// a register still awaited in the loop would make every tile wait for the copies behind it.
+template <int N>
+__device__ __forceinline__ void arrived(bf16x8 (&q)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(q[i]));
+}
+
+// Keeps an array in memory, out of the registers.
+template <class T>
+__device__ __forceinline__ void in_memory(T& array) {
+    asm volatile("" : : "v"(&array) : "memory");
+}
+
 // Bits 0 .. n: none for a negative n, all from 63 on.
 __device__ __forceinline__ uint64_t bits_to(int n) {
     return n < 0 ? 0ull : ~0ull >> (63 - min(n, 63));
@@ -244,6 +300,9 @@ __device__ __forceinline__ bool nonfinite8(u32x4 v) {
 // more than kSlack: exponentials up to 2^kSlack cost fp32 sums and bf16 probabilities
 // nothing, and the running result is rarely rescaled after its first tile.
 constexpr float kSlack = 8.0f;
+// The larger score; a NaN stays one (its row is NaN whatever is subtracted), which spares
+// the instructions that would quiet it.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 struct Running {
     float m = -__builtin_inff(), l = 0.0f;
     // The reference to subtract: a column that has seen nothing keeps its exponentials at zero.
@@ -317,11 +376,14 @@ __device__ __forceinline__ void store_row(const Call& a, int D, int64_t row, int
 // ---------------------------------------------------------------------------
 // Few rows a sequence (decoding): a workgroup takes one row tile of 16 and a chunk of
 // keys, its four waves 32 keys each of every 128.  Every wave streams its keys and
-// values into a ring of its own in LDS, with no barrier until its end; the waves' results are
-// joined there, and those of chunks by the last workgroup to arrive, in chunk order.
+// values through buffers of its own in LDS, with no barrier until its end: a buffer is
+// requested again as soon as its product has read it, so keys arrive under a tile's softmax
+// and second product and values under the next one's first.  The waves' results
+// are joined in LDS, those of chunks by the last workgroup to arrive, in chunk order.
 //
-// Bound by memory.  The probabilities enter the second product as a sum of two bf16
-// numbers, so it loses nothing to their rounding (matrix instructions are idle here).
+// Bound by memory: two workgroups a CU keep 100 KB on their way.  The probabilities
+// enter the second product as a sum of two bf16 numbers, so it loses nothing to their
+// rounding (matrix instructions are idle here).
 // ---------------------------------------------------------------------------
 template <int D, bool E4M3>
 struct Rows {
@@ -330,14 +392,14 @@ struct Rows {
     static constexpr int PIECES = RB / 16;
     static constexpr int KEYS = 64 / PIECES;             // keys of one copy
     static constexpr int LOADS = TK / KEYS;
-    static constexpr int SCALES = E4M3 ? 256 : 0;
-    static constexpr int STAGE = 2 * TK * RB + SCALES;
-    static constexpr int NS = RB == 256 ? 2 : 4;         // stages
-    static constexpr int COPIES = 2 * LOADS + (E4M3 ? 1 : 0);
-    static constexpr int OROW = D + 4;                   // floats of a row handed over in LDS
+    static constexpr int NS = 256 / RB;                  // tiles in LDS for each wave
+    static constexpr int KCOPIES = LOADS + (E4M3 ? 1 : 0), VCOPIES = LOADS;      // of a tile; scales come with the keys
+    static constexpr int K0 = 0, V0 = TK * RB, S0 = 2 * TK * RB, STAGE = S0 + (E4M3 ? 256 : 0);
     static constexpr int WAVE_BYTES = NS * STAGE;
+    static constexpr int LDS = WAVES * WAVE_BYTES + 16;
+    static constexpr int OROW = D + 4;                   // floats of a row handed over in LDS
     static constexpr int SLOT = BM * (D + 2);            // floats
-    static_assert(BM * (OROW + 2) * 4 <= WAVE_BYTES, "the hand-over fits a wave's ring");
+    static_assert(BM * (OROW + 2) * 4 <= WAVE_BYTES && 256 * (16 * 8 + D / 16 * 4) <= WAVES * WAVE_BYTES, "LDS");
     // Where a row's 16-byte piece lies: pieces change places by the key so that the lanes
     // of a read meet different banks (16 pieces span all of them).
     __device__ static __forceinline__ int swap_k(int key) {
@@ -349,11 +411,105 @@ struct Rows {
     }
 };
 
+// The larger value, and the sum, of 16 neighbouring lanes, in each of them.
+__device__ __forceinline__ float max_of_16(float v) {
+    v = fmaxf(v, dpp<0xb1>(v));
+    v = fmaxf(v, dpp<0x4e>(v));
+    v = fmaxf(v, dpp<0x141>(v));
+    return fmaxf(v, dpp<0x140>(v));
+}
+__device__ __forceinline__ float sum_of_16(float v) {
+    v += dpp<0xb1>(v);
+    v += dpp<0x4e>(v);
+    v += dpp<0x141>(v);
+    return v + dpp<0x140>(v);
+}
+
+// What the join of parts needs of a workgroup's LDS: the (m, l) of 16 rows of at most 256
+// parts, and a sum from every thread.
+constexpr int kParts = 256, kJoinSums = kParts * 16 * 8;
+template <int D>
+constexpr int kJoinBytes = kJoinSums + 256 * (D / 16) * 4;
+
+// Joins all parts of up to 16 rows at once: `own` chunks in slots (`stride` floats apart, (m, l)
+// of the rows from `ml_at` on), and those of a shared prefix (its rows from `row0` on).  First
+// every part's (m, l), then its weight, then the weighted sums, the parts dealt to as many
+// threads as there are: three trips to memory, whatever their number.  Thread t
+// receives elements t % 16 * D / 16 .. of row t / 16 in j, which with no chunk of its own is
+// one more part.
+template <int D>
+__device__ __forceinline__ void join_parts(const Call& a, unsigned char* smem, int h, int rows, int64_t row0, const float* slot,
+                                           int64_t stride, int ml_at, int own, Joined<D / 16>& j) {
+    constexpr int N = D / 16;
+    const int tid = threadIdx.x, r = tid >> 4, d0 = (tid & 15) * N;
+    const bool live = r < rows;
+    const int parts = own + a.prior_chunks;
+    const int64_t prior_rows = (int64_t)a.T * a.G;
+    float* ml = reinterpret_cast<float*>(smem);
+    __syncthreads();
+    for (int x = tid; x < parts * 16; x += 256) {
+        const int part = x / 16, pr = x % 16;
+        if (pr >= rows) continue;
+        if (part < own) load_agent<2>(slot + part * stride + ml_at + 2 * pr, ml + 2 * x);
+        else
+            *reinterpret_cast<f32x2*>(ml + 2 * x) =
+                *reinterpret_cast<const f32x2*>(a.prior_ml + 2 * (((int64_t)(part - own) * a.Hkv + h) * prior_rows + row0 + pr));
+    }
+    __syncthreads();
+    float m = own ? -__builtin_inff() : j.m, l = 0.0f;
+    if (live) {
+        for (int x = tid & 15; x < parts; x += 16) m = fmaxf(m, ml[2 * (x * 16 + r)]);
+        m = max_of_16(m);
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
+        for (int x = tid & 15; x < parts; x += 16) {
+            float* at = ml + 2 * (x * 16 + r);
+            const float w = __builtin_amdgcn_exp2f(at[0] - ref);
+            l += at[1] * w;
+            at[0] = w;
+        }
+        l = sum_of_16(l);
+    }
+    __syncthreads();
+    const int sets = 16 / rows, set = r / rows, pr = r % rows;
+    float sum[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[e] = 0.0f;
+    if (set < sets) {
+#pragma unroll 4
+        for (int x = set; x < own; x += sets) {
+            float v[N];
+            load_agent<N>(slot + x * stride + pr * D + d0, v);
+            const float w = ml[2 * (x * 16 + pr)];
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum[e] = fmaf(v[e], w, sum[e]);
+        }
+#pragma unroll 4
+        for (int x = set; x < a.prior_chunks; x += sets) {
+            const float* v = a.prior + (((int64_t)x * a.Hkv + h) * prior_rows + row0 + pr) * D + d0;
+            const float w = ml[2 * ((own + x) * 16 + pr)];
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum[e] = fmaf(v[e], w, sum[e]);
+        }
+    }
+    float* sums = reinterpret_cast<float*>(smem + kJoinSums);
+#pragma unroll
+    for (int e = 0; e < N; ++e) sums[tid * N + e] = sum[e];
+    __syncthreads();
+    if (!live) return;
+    for (int x = 1; x < sets; ++x)
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum[e] += sums[(x * rows * 16 + tid) * N + e];
+    const float w = own ? 0.0f : __builtin_amdgcn_exp2f(j.m - (m == -__builtin_inff() ? 0.0f : m));
+#pragma unroll
+    for (int e = 0; e < N; ++e) j.o[e] = own ? sum[e] : fmaf(j.o[e], w, sum[e]);
+    j.l = own ? l : fmaf(j.l, w, l);
+    j.m = m;
+}
+
 template <int D, bool E4M3>
-__global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
+__global__ __launch_bounds__(256, 2) void attention_rows_kernel(Call a) {
     using R = Rows<D, E4M3>;
-    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    __shared__ int flag;
+    extern __shared__ __attribute__((aligned(256))) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;              // column (row of the tile), lane group
@@ -364,14 +520,13 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
     const int rows = min(R::BM, item.s.tokens * a.G - item.row0);
     const int my_row = item.row0 + c;
     const bool mine = c < rows;
-    const int pos = mine ? first_pos + my_row / a.G : -1;
+    const int pos = mine ? max(first_pos + my_row / a.G, -1) : -1;
     const int pos_min = first_pos + item.row0 / a.G, pos_max = first_pos + (item.row0 + rows - 1) / a.G;
     const int limit = (int)min((int64_t)item.s.len, (int64_t)a.max_pages << a.page_shift);
 
-    const int i0 = item.chunks > 1 ? item.chunk * item.chunk_tiles : 0;
-    const int tiles = item.chunks > 1 ? min(item.chunk_tiles, item.span.n - i0) : item.span.n;
+    const int i0 = item.chunk * item.chunk_tiles;        // (a last chunk may be left without tiles)
+    const int tiles = min(item.chunk_tiles, item.span.n - i0);
     const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem + wave * R::WAVE_BYTES;
-    const int* table = a.table + (int64_t)item.b * a.max_pages;
 
     // the copies' offsets from a 16-key half's first row
     uint32_t koff[R::LOADS], voff[R::LOADS];
@@ -389,26 +544,34 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int key = key0 + 16 * x;
-            const int id = key < limit ? table[key >> a.page_shift] : -1;
+            const int64_t b = key < a.shared ? 0 : item.b;
+            const int id = key < limit ? load_scalar(a.table + b * a.max_pages + (key >> a.page_shift)) : -1;
             p.row[x] = id >= 0 && id < a.pages
                 ? ((((int64_t)id * a.Hkv + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) : -1;
         }
         return p;
     };
     auto key_of = [&](int i) { return item.span.tile(i0 + i) * R::TILE + wave * R::TK; };
-    auto copy = [&](int stage, const Pages& p) {
-        const uint32_t to = ring + stage * R::STAGE;
+    auto copy_rows = [&](const void* cache, const uint32_t (&off)[R::LOADS], uint32_t to, int64_t row0, int64_t row1) {
+        const unsigned char* half0 = static_cast<const unsigned char*>(cache) + row0 * R::RB;
+        const unsigned char* half1 = static_cast<const unsigned char*>(cache) + row1 * R::RB;
+        if (a.stream) {
 #pragma unroll
-        for (int j = 0; j < R::LOADS; ++j) {
-            const int64_t row = max(p.row[j * R::KEYS / 16], (int64_t)0);
-            lds_copy_b128(static_cast<const unsigned char*>(a.k) + row * R::RB, koff[j], to + j * 1024);
-            lds_copy_b128(static_cast<const unsigned char*>(a.v) + row * R::RB, voff[j], to + R::TK * R::RB + j * 1024);
+            for (int j = 0; j < R::LOADS; ++j) lds_copy_b128_nt(j * R::KEYS < 16 ? half0 : half1, off[j], to + j * 1024);
+        } else {
+#pragma unroll
+            for (int j = 0; j < R::LOADS; ++j) lds_copy_b128(j * R::KEYS < 16 ? half0 : half1, off[j], to + j * 1024);
         }
-        if constexpr (E4M3) {
-            const int64_t row0 = max(p.row[0], (int64_t)0), row1 = max(p.row[1], (int64_t)0);
-            const int64_t row = (lane & 16 ? row1 : row0) + (lane & 15);
-            lds_copy_b32((lane < 32 ? a.k_scale : a.v_scale) + row, to + 2 * R::TK * R::RB);
-        }
+    };
+    auto copy_keys = [&](int stage, const Pages& p) {
+        const uint32_t to = ring + stage * R::STAGE;
+        const int64_t row0 = max(p.row[0], (int64_t)0), row1 = max(p.row[1], (int64_t)0);
+        copy_rows(a.k, koff, to + R::K0, row0, row1);
+        if constexpr (E4M3)
+            lds_copy_b32((lane < 32 ? a.k_scale : a.v_scale) + (lane & 16 ? row1 : row0) + (lane & 15), to + R::S0);
+    };
+    auto copy_values = [&](int stage, const Pages& p) {
+        copy_rows(a.v, voff, ring + stage * R::STAGE + R::V0, max(p.row[0], (int64_t)0), max(p.row[1], (int64_t)0));
     };
 
     // this lane's query: 8 elements of every 32
@@ -420,12 +583,16 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
         for (int ks = 0; ks < D / 32; ++ks) q[ks] = as_bf16x8(*reinterpret_cast<const u32x4*>(a.q + at + 32 * ks));
     }
 
-    Pages held[R::NS];                                   // of the tiles in the ring
+    Pages held[R::NS];                                   // of the tiles in LDS
+#pragma unroll
+    for (int s = 0; s < R::NS; ++s)
+        if (s < tiles) held[s] = pages_of(key_of(s));
+    arrived(q);
 #pragma unroll
     for (int s = 0; s < R::NS; ++s)
         if (s < tiles) {
-            held[s] = pages_of(key_of(s));
-            copy(s, held[s]);
+            copy_keys(s, held[s]);
+            copy_values(s, held[s]);
         }
 
     Running run;
@@ -438,15 +605,14 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
         const Pages here = held[S];
         const bool more = i + R::NS < tiles;
         if (more) held[S] = pages_of(key_of(i + R::NS));
-        const int ahead = min(tiles - 1 - i, R::NS - 1); // tiles still on their way behind this one
-        if (ahead == R::NS - 1) wait_vmem<(R::NS - 1) * R::COPIES>();
-        else if (R::NS > 2 && ahead == R::NS - 2) wait_vmem<(R::NS > 2 ? R::NS - 2 : 0) * R::COPIES>();
-        else wait_vmem<0>();
+        // behind this tile's keys: its values, and the tiles after it
+        wait_behind<R::NS, R::KCOPIES + R::VCOPIES, R::VCOPIES>(tiles - 1 - i);
         const int key0 = key_of(i);
-        const uint32_t kb0 = ring + S * R::STAGE, vb0 = kb0 + R::TK * R::RB, sb0 = vb0 + R::TK * R::RB;
+        const uint32_t kb0 = ring + S * R::STAGE + R::K0, vb0 = ring + S * R::STAGE + R::V0, sb0 = ring + S * R::STAGE + R::S0;
 
         // S^T: lane (c, g) receives keys 16 x + 4 g + r of column c
         float s[8];
+        f32x4 vs[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -461,9 +627,16 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
                 acc = mfma_bf16_16x16x32(as_bf16x8(k), q[ks], acc);
             }
             f32x4 factor = f32x4{a.scale2, a.scale2, a.scale2, a.scale2};
-            if constexpr (E4M3) factor *= lds_read<f32x4>(sb0 + (16 * x + 4 * g) * 4);
+            if constexpr (E4M3) {
+                factor *= lds_read<f32x4>(sb0 + (16 * x + 4 * g) * 4);
+                vs[x] = lds_read<f32x4>(sb0 + 128 + (16 * x + 4 * g) * 4);
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) s[4 * x + r] = acc[r] * factor[r];
+        }
+        if (more) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the keys have been read
+            copy_keys(S, held[S]);
         }
 
         // which of this lane's keys its row sees
@@ -471,26 +644,26 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
                            (a.window <= 0 || key0 > pos_max - a.window || key0 + 31 < a.sinks);
         uint32_t seen = 0xff;
         if (!whole) {
-            seen = 0;
+            uint64_t m = ~0ull;
+            if (a.window > 0) m = ~bits_to(pos - a.window - key0) | bits_to(a.sinks - 1 - key0);
+            m &= bits_to(min(pos, limit - 1) - key0) & ~bits_to(a.prefix - 1 - key0);
+            if (here.row[0] < 0) m &= ~0xffffull;
+            if (here.row[1] < 0) m &= 0xffffull;
+            const uint32_t w = (uint32_t)m >> (4 * g);
+            seen = (w & 15u) | (w >> 12 & 0xf0u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int key = key0 + 16 * (e >> 2) + 4 * g + (e & 3);
-                const bool sees = here.row[e >> 2] >= 0 && key >= a.prefix && key <= pos && key < limit &&
-                                  (a.window <= 0 || key > pos - a.window || key < a.sinks);
-                seen |= sees ? 1u << e : 0u;
-                if (!sees) s[e] = -__builtin_inff();
-            }
+            for (int e = 0; e < 8; ++e) s[e] = seen >> e & 1 ? s[e] : -__builtin_inff();
         }
 
         // the running maximum; its lanes are c, c + 16, c + 32, c + 48
         float top = s[0];
 #pragma unroll
-        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
+        for (int e = 1; e < 8; ++e) top = larger(top, s[e]);
         float t2;
         top = both16(top, t2);
-        top = fmaxf(top, t2);
+        top = larger(top, t2);
         top = both32(top, t2);
-        top = fmaxf(top, t2);
+        top = larger(top, t2);
         if (__ballot(run.outgrown(top))) {
             const float w = run.follow(top);
 #pragma unroll
@@ -502,24 +675,21 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
         for (int e = 0; e < 8; ++e) {
             p[e] = __builtin_amdgcn_exp2f(s[e] - ref);
             run.l += p[e];
+            if constexpr (E4M3) p[e] *= vs[e >> 2][e & 3];
         }
-        if constexpr (E4M3) {
-            const f32x4 v0 = lds_read<f32x4>(sb0 + 128 + 16 * g), v1 = lds_read<f32x4>(sb0 + 128 + 64 + 16 * g);
+        if constexpr (E4M3)
+            if (!whole) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float v = p[e] * (e < 4 ? v0[e & 3] : v1[e & 3]);
-                p[e] = whole || (seen >> e & 1) ? v : 0.0f;
+                for (int e = 0; e < 8; ++e) p[e] = seen >> e & 1 ? p[e] : 0.0f;   // whatever its scale
             }
-        }
         const u32x4 hi = pack8(p);
         float rest[8];
         unpack8(hi, rest);
+        // an infinite product (its scale overflowed) has no rest: the finite number here adds to the infinity
 #pragma unroll
-        for (int e = 0; e < 8; ++e) rest[e] = p[e] - rest[e];
-        // an infinite probability (a scale that overflowed) has no rest
-#pragma unroll
-        for (int e = 0; e < 8; ++e) rest[e] = __builtin_isfinite(rest[e]) ? rest[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) rest[e] = E4M3 ? fminf(p[e] - rest[e], 0x1p100f) : p[e] - rest[e];
         const u32x4 lo = pack8(rest);
+        wait_behind<R::NS, R::KCOPIES + R::VCOPIES, R::KCOPIES>(tiles - 1 - i, more);
 
         // V^T: lane (c, g) takes element 16 d + c of keys 4 g .. and 16 + 4 g ..
         auto values = [&](int d) {
@@ -578,8 +748,8 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
             }
         }
         if (more) {
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage has been read
-            copy(S, held[S]);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the values have been read
+            copy_values(S, held[S]);
         }
     };
     for (int i = 0; i < tiles; i += R::NS)
@@ -587,7 +757,7 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
             if (i + decltype(s)::value < tiles) step(s, i + decltype(s)::value);
         });
 
-    // the waves' results meet in LDS, each in its own ring
+    // the waves' results meet in LDS, each in its own buffers
     {
         float t2;
         float l = both16(run.l, t2);
@@ -612,10 +782,11 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
             const float* from = reinterpret_cast<const float*>(smem + w * R::WAVE_BYTES);
             j.add(from[R::BM * R::OROW + 2 * r], from[R::BM * R::OROW + 2 * r + 1], from + r * R::OROW + d0);
         }
-    if (item.chunks > 1) {
-        float* slot = a.slots + ((int64_t)item.first * a.Hkv + (int64_t)h * item.chunks) * R::SLOT;
+    const int own = item.chunks > 1 ? item.chunks : 0;
+    const float* slot = a.slots + ((int64_t)item.first * a.Hkv + (int64_t)h * item.chunks) * R::SLOT;
+    if (own) {
         if (live) {
-            float* to = slot + (int64_t)item.chunk * R::SLOT;
+            float* to = const_cast<float*>(slot) + (int64_t)item.chunk * R::SLOT;
             store_agent<N>(to + r * D + d0, j.o);
             if (d0 == 0) {
                 const float ml[2] = {j.m, j.l};
@@ -623,25 +794,13 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
             }
         }
         unsigned* counter = a.counters + (int64_t)item.first * a.Hkv + h;
-        if (!arrive_and_check_last(counter, item.chunks, &flag)) return;
+        if (!arrive_and_check_last(counter, own, reinterpret_cast<int*>(smem + R::WAVES * R::WAVE_BYTES))) return;
         if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (!live) return;
-        j = Joined<N>();
-#pragma unroll 4
-        for (int x = 0; x < item.chunks; ++x) {
-            const float* from = slot + (int64_t)x * R::SLOT;
-            float ml[2], part[N];
-            load_agent<2>(from + R::BM * D + 2 * r, ml);
-            load_agent<N>(from + r * D + d0, part);
-            j.add(ml[0], ml[1], part);
-        }
     }
+    if (own + a.prior_chunks)
+        join_parts<D>(a, smem, h, rows, (int64_t)item.s.first_token * a.G + item.row0, slot, R::SLOT, R::BM * D, own, j);
     if (!live) return;
     const int at = item.row0 + r;
-    for (int x = 0; x < a.prior_chunks; ++x) {
-        const int64_t row = ((int64_t)x * a.Hkv + h) * ((int64_t)a.T * a.G) + (int64_t)item.s.first_token * a.G + at;
-        j.add(a.prior_ml[2 * row], a.prior_ml[2 * row + 1], a.prior + row * D + d0);
-    }
     store_row<N>(a, D, (int64_t)(item.s.first_token + at / a.G) * a.Hq + h * a.G + at % a.G, d0, j);
 }
 
@@ -655,16 +814,22 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(Call a) {
 // Bound by the matrix instructions and, nearly as much, by the exponentials: two
 // workgroups on a CU let one wave's softmax run under another's products.
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, bool E4M3>
 struct Tiles {
     static constexpr int WAVES = 4, BM = 32 * WAVES, TK = 64;
-    static constexpr int RB = 2 * D, PIECES = RB / 16;   // a row of a tile in LDS is bf16
+    static constexpr int RB = 2 * D, PIECES = RB / 16;   // a row of a tile that is multiplied: bf16
     static constexpr int KEYS = 64 / PIECES;             // keys of one copy
     static constexpr int LOADS = 16 / KEYS;              // a wave copies 16 keys and 16 values
-    static constexpr int K0 = 0, V0 = TK * RB, KS = 2 * TK * RB, VS = KS + 4 * TK, LIVE = VS + 4 * TK;
-    static constexpr int BAD = LIVE + 16, STAGE = (BAD + 16 + 255) / 256 * 256;
-    static constexpr int ENDS = 2 * STAGE, FLAG = ENDS + 8 * WAVES;     // the waves' first and last positions; last arriver
-    static constexpr int LDS = FLAG + 16;
+    static constexpr int K0 = 0, V0 = TK * RB, KS = 2 * TK * RB, VS = KS + 4 * TK, LIVE = VS + 4 * TK, BAD = LIVE + 16;
+    static constexpr int STAGE = (BAD + 16 + 255) / 256 * 256;
+    // bf16: NB stages, one multiplied, the others on their way.  e4m3: one, and NR raw tiles of codes.
+    static constexpr int NB = E4M3 ? 1 : D == 64 ? 4 : 2, NR = E4M3 ? (D == 64 ? 4 : 2) : 0;
+    static constexpr int RLOADS = D / 64;                // copies of a wave's 16 raw keys
+    static constexpr int RAWK = 0, RAWV = 16 * D, RAWS = 32 * D, RAW = RAWS + 256;       // of one wave
+    static constexpr int COPIES = E4M3 ? 2 * RLOADS + 1 : 2 * LOADS;
+    static constexpr int RAW0 = NB * STAGE;
+    static constexpr int ENDS = RAW0 + NR * WAVES * RAW;                 // the waves' first and last positions
+    static constexpr int LDS = ENDS + 8 * WAVES;
     static constexpr int SLOT = BM * (D + 2);            // floats
     __device__ static __forceinline__ int swap_k(int key) { return PIECES == 16 ? key & 15 : (key >> 1) & 7; }
     __device__ static __forceinline__ int swap_v(int key) {
@@ -675,7 +840,7 @@ struct Tiles {
 // PREFIX: the rows are all T tokens' and the keys the shared ones; partial results.
 template <int D, bool E4M3, bool PREFIX>
 __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
-    using R = Tiles<D>;
+    using R = Tiles<D, E4M3>;
     extern __shared__ __attribute__((aligned(256))) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -755,74 +920,58 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
         }
     }
 
-    const int* table = a.table + (int64_t)item.b * a.max_pages;
-    // a wave brings 16 keys of every tile; lane offsets from their first row
-    uint32_t koff[R::LOADS], voff[R::LOADS];
-#pragma unroll
-    for (int j = 0; j < R::LOADS; ++j) {
-        const int key = j * R::KEYS + lane / R::PIECES;
-        koff[j] = key * R::RB + ((lane % R::PIECES) ^ R::swap_k(key)) * 16;
-        voff[j] = key * R::RB + ((lane % R::PIECES) ^ R::swap_v(key)) * 16;
-    }
-    // the cache row of the wave's 16 keys of a tile, -1 where they have no page
-    auto row_of = [&](int i) {
+    // bf16: a wave brings 16 keys of every tile; the first copy's offset from their first row, from
+    // which copy j lies 64 j (keys; values of 128 elements: 32 (j % 2)) away by exclusive or
+    uint32_t koff = lane / R::PIECES * R::RB + ((lane % R::PIECES) ^ R::swap_k(lane / R::PIECES)) * 16;
+    uint32_t voff = lane / R::PIECES * R::RB + ((lane % R::PIECES) ^ R::swap_v(lane / R::PIECES)) * 16;
+    // the page of the wave's 16 keys of a tile (any entry of the table past the end); and their row in
+    // the cache, -1 where they have no page
+    auto page_of = [&](int i) {
         const int key = item.span.tile(i0 + i) * R::TK + 16 * wave;
-        const int id = key < limit ? table[key >> a.page_shift] : -1;
-        return id >= 0 && id < a.pages
-            ? ((((int64_t)id * a.Hkv + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) : (int64_t)-1;
+        const int64_t b = PREFIX || key < a.shared ? 0 : item.b;
+        return load_scalar(a.table + b * a.max_pages + min(key >> a.page_shift, a.max_pages - 1));
     };
-    auto announce = [&](uint32_t stage, int64_t row) {
-        if (lane == 0) lds_write<int>(stage + R::LIVE + 4 * wave, row >= 0);
+    auto row_of = [&](int i, int page) {
+        const int key = item.span.tile(i0 + i) * R::TK + 16 * wave;
+        return key < limit && page >= 0 && page < a.pages
+            ? ((((int64_t)page * a.Hkv + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) : (int64_t)-1;
     };
-    auto copy = [&](int i, int64_t row) {                // bf16
-        const uint32_t stage = lds0 + (i & 1) * R::STAGE, to = stage + 16 * wave * R::RB;
-        const int64_t at = max(row, (int64_t)0) * R::RB;
-#pragma unroll
-        for (int j = 0; j < R::LOADS; ++j) {
-            lds_copy_b128(static_cast<const unsigned char*>(a.k) + at, koff[j], to + R::K0 + j * 1024);
-            lds_copy_b128(static_cast<const unsigned char*>(a.v) + at, voff[j], to + R::V0 + j * 1024);
-        }
-        announce(stage, row);
-    };
-    // e4m3: 16 codes a lane and load; the lane's key and piece of the wave's 16 keys
-    constexpr int CLOADS = D / 64;                       // 16 D codes of keys, 16 bytes a lane
-    u32x4 kc[CLOADS], vc[CLOADS];
-    float sc = 0.0f;
-    int64_t held_row = -1;
-    auto fetch = [&](int64_t row) {
-        held_row = row;
+    // copies of tile i: bf16 straight into the stage that is multiplied, e4m3 into the wave's raw tile
+    uint32_t alive = 0;                                  // e4m3: which raw tiles' keys have a page
+    auto copy = [&](int i, int64_t row) {
         const int64_t at = max(row, (int64_t)0);
+        if constexpr (E4M3) {
+            const int slot = i % R::NR;
+            const uint32_t to = lds0 + R::RAW0 + (slot * R::WAVES + wave) * R::RAW;
 #pragma unroll
-        for (int j = 0; j < CLOADS; ++j) {
-            kc[j] = *reinterpret_cast<const u32x4*>(static_cast<const unsigned char*>(a.k) + at * D + j * 1024 + lane * 16);
-            vc[j] = *reinterpret_cast<const u32x4*>(static_cast<const unsigned char*>(a.v) + at * D + j * 1024 + lane * 16);
-        }
-        if (lane < 32) sc = (lane < 16 ? a.k_scale : a.v_scale)[at + (lane & 15)];
-    };
-    auto place = [&](int i) {
-        const uint32_t stage = lds0 + (i & 1) * R::STAGE;
-#pragma unroll
-        for (int j = 0; j < CLOADS; ++j) {
-            const int key = (j * 1024 + lane * 16) / D, piece = (j * 1024 + lane * 16) % D / 8;
-            const uint32_t row = stage + (16 * wave + key) * R::RB;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const u32x4 k = e4m3_to_bf16(x ? u32x2{kc[j].z, kc[j].w} : u32x2{kc[j].x, kc[j].y});
-                const u32x4 v = e4m3_to_bf16(x ? u32x2{vc[j].z, vc[j].w} : u32x2{vc[j].x, vc[j].y});
-                lds_write(row + R::K0 + ((piece + x) ^ R::swap_k(key)) * 16, k);
-                lds_write(row + R::V0 + ((piece + x) ^ R::swap_v(key)) * 16, v);
+            for (int j = 0; j < R::RLOADS; ++j) {
+                lds_copy_b128(static_cast<const unsigned char*>(a.k) + at * D, j * 1024 + lane * 16, to + R::RAWK + j * 1024);
+                lds_copy_b128(static_cast<const unsigned char*>(a.v) + at * D, j * 1024 + lane * 16, to + R::RAWV + j * 1024);
             }
+            lds_copy_b32((lane & 16 ? a.v_scale : a.k_scale) + at + (lane & 15), to + R::RAWS);
+            alive = (alive & ~(1u << slot)) | (uint32_t)(row >= 0) << slot;
+        } else {
+            const uint32_t stage = lds0 + i % R::NB * R::STAGE, to = stage + 16 * wave * R::RB;
+#pragma unroll
+            for (int j = 0; j < R::LOADS; ++j) {
+                lds_copy_b128(static_cast<const unsigned char*>(a.k) + at * R::RB, (koff ^ (64 * j)) + 1024 * j, to + R::K0 + j * 1024);
+                lds_copy_b128(static_cast<const unsigned char*>(a.v) + at * R::RB, (voff ^ (D == 128 ? j % 2 * 32 : 0)) + 1024 * j, to + R::V0 + j * 1024);
+            }
+            if (lane == 0) lds_write<int>(stage + R::LIVE + 4 * wave, row >= 0);
         }
-        if (lane < 32) lds_write(stage + (lane < 16 ? R::KS : R::VS) + 4 * (16 * wave + (lane & 15)), sc);
-        announce(stage, held_row);
+    };
+    // whether rows from position `first` to `last` see all of a tile
+    const auto whole_for = [&](int key0, int first, int last) {
+        return key0 >= key_begin && key0 + R::TK <= limit && key0 + R::TK - 1 <= first &&
+               (a.window <= 0 || key0 > last - a.window || key0 + R::TK - 1 < a.sinks);
     };
 
     // a lane's place in a tile: its key's row with the first of its pieces, from which piece 2 ks (a
     // step of keys) and 4 d (a block of values) away is an exclusive or (stages and rows are
     // multiples of what it changes)
-    const uint32_t kat = R::K0 + c * R::RB + (hf ^ R::swap_k(c)) * 16;
+    uint32_t kat = R::K0 + c * R::RB + (hf ^ R::swap_k(c)) * 16;
     const int vkey = 4 * hf + (lane >> 2 & 3);
-    const uint32_t vat = R::V0 + vkey * R::RB + ((2 * (c >> 4) + (lane >> 1 & 1)) ^ R::swap_v(vkey)) * 16 + (lane & 1) * 8;
+    uint32_t vat = R::V0 + vkey * R::RB + ((2 * (c >> 4) + (lane >> 1 & 1)) ^ R::swap_v(vkey)) * 16 + (lane & 1) * 8;
 
     // this lane's query: 8 elements of every 16, negated for a negative scale
     bf16x8 q[D / 16];
@@ -835,14 +984,15 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
     }
     const float scale2 = fabsf(a.scale2);
 
-    if (tiles > 0) {
-        if constexpr (E4M3) {
-            fetch(row_of(0));
-            place(0);
-        } else {
-            copy(0, row_of(0));
-        }
-    }
+    constexpr int FAR = E4M3 ? R::NR : R::NB - 1;        // tiles on their way
+    int page[FAR + 1];
+#pragma unroll
+    for (int i = 0; i <= FAR; ++i) page[i] = page_of(i);
+    int next = page[FAR];                                // the page of the tile to copy next
+    arrived(q);
+#pragma unroll
+    for (int i = 0; i < FAR; ++i)
+        if (i < tiles) copy(i, row_of(i, page[i]));
 
     Running run;
     f32x16 o[D / 32];
@@ -852,47 +1002,84 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
 
     for (int i = 0; i < tiles; ++i) {
-        // this tile has arrived, and every wave is done with the one before it
-        if constexpr (!E4M3) wait_vmem<0>();
-        __syncthreads();
-        if (i + 1 < tiles) {
-            if constexpr (E4M3) fetch(row_of(i + 1));
-            else copy(i + 1, row_of(i + 1));
-        }
         const int key0 = item.span.tile(i0 + i) * R::TK;
-        const uint32_t stage = lds0 + (i & 1) * R::STAGE;
-        const auto whole_for = [&](int first, int last) {
-            return key0 >= key_begin && key0 + R::TK <= limit && key0 + R::TK - 1 <= first &&
-                   (a.window <= 0 || key0 > last - a.window || key0 + R::TK - 1 < a.sinks);
-        };
-        const i32x4 live4 = lds_read<i32x4>(stage + R::LIVE);
-        const bool live = __builtin_amdgcn_readfirstlane(live4[0] & live4[1] & live4[2] & live4[3]) != 0;
-        const bool whole = live && whole_for(pos_min, pos_max);
-        // Where a row of the workgroup does not see all keys: values of positions that hold no key
-        // become zeros (a wave its own 16), and an infinity or NaN among the others is found.
-        const bool clean = live && whole_for(all_min, all_max);
-        bool bad = false;
-        if (!clean) {
-            const bool page = live4[wave] != 0;
-            bool odd = false;
+        const uint32_t stage = lds0 + (E4M3 ? 0 : i % R::NB * R::STAGE);
+        // (what follows from these is computed anew in every tile: kept, it takes registers from the products)
+        asm volatile("" : "+v"(kat), "+v"(vat), "+v"(koff), "+v"(voff));
+        wait_tiles<R::COPIES, E4M3 ? R::NR - 1 : R::NB - 2>(tiles - 1 - i);
+        const bool clean = whole_for(key0, all_min, all_max);
+        if constexpr (E4M3) {
+            // the wave's 16 keys and values become bf16.  Where a row of the workgroup does not see all keys, values
+            // of positions that hold no key become zeros, and a NaN or infinity among the others is found.
+            const int slot = i % R::NR;
+            const uint32_t raw = lds0 + R::RAW0 + (slot * R::WAVES + wave) * R::RAW;
+            const bool paged = alive >> slot & 1;
+            u32x4 kc[R::RLOADS], vc[R::RLOADS];
 #pragma unroll
-            for (int j = 0; j < R::LOADS; ++j) {
-                const int key = 16 * wave + j * R::KEYS + lane / R::PIECES;
-                const uint32_t at = stage + R::V0 + 16 * wave * R::RB + j * 1024 + 16 * lane;
-                if (page && key0 + key < limit) odd |= nonfinite8(lds_read<u32x4>(at));
-                else lds_write(at, u32x4{0u, 0u, 0u, 0u});
+            for (int j = 0; j < R::RLOADS; ++j) {
+                kc[j] = lds_read<u32x4>(raw + R::RAWK + j * 1024 + lane * 16);
+                vc[j] = lds_read<u32x4>(raw + R::RAWV + j * 1024 + lane * 16);
             }
-            if (E4M3 && lane < 16) {
-                const uint32_t at = stage + R::VS + 4 * (16 * wave + lane);
-                if (page && key0 + 16 * wave + lane < limit) odd |= !__builtin_isfinite(lds_read<float>(at));
-                else lds_write(at, 0.0f);
+            float scale = lds_read<float>(raw + R::RAWS + (lane & 31) * 4);
+            bool odd = false;
+            if (!clean || !paged) {
+#pragma unroll
+                for (int j = 0; j < R::RLOADS; ++j) {
+                    const bool holds = paged && key0 + 16 * wave + (j * 1024 + lane * 16) / D < limit;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        odd |= holds && (((vc[j][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u);
+                        vc[j][e] = holds ? vc[j][e] : 0u;
+                    }
+                }
+                const bool holds = paged && key0 + 16 * wave + (lane & 15) < limit;
+                odd |= holds && (lane & 16) && !__builtin_isfinite(scale);
+                scale = holds ? scale : 0.0f;
             }
             const uint64_t some = __ballot(odd);
-            if (lane == 0) lds_write<int>(stage + R::BAD + 4 * wave, some != 0);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (i + R::NR < tiles) copy(i + R::NR, row_of(i + R::NR, next));
+            __syncthreads();                             // every wave is done with the tile before
+#pragma unroll
+            for (int j = 0; j < R::RLOADS; ++j) {
+                const int key = (j * 1024 + lane * 16) / D, piece = (j * 1024 + lane * 16) % D / 8;
+                const uint32_t row = stage + (16 * wave + key) * R::RB;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    lds_write(row + R::K0 + ((piece + x) ^ R::swap_k(key)) * 16, e4m3_to_bf16(u32x2{kc[j][2 * x], kc[j][2 * x + 1]}));
+                    lds_write(row + R::V0 + ((piece + x) ^ R::swap_v(key)) * 16, e4m3_to_bf16(u32x2{vc[j][2 * x], vc[j][2 * x + 1]}));
+                }
+            }
+            if (lane < 32) lds_write(stage + (lane < 16 ? R::KS : R::VS) + 4 * (16 * wave + (lane & 15)), scale);
+            if (lane == 0) {
+                lds_write<int>(stage + R::LIVE + 4 * wave, paged);
+                lds_write<int>(stage + R::BAD + 4 * wave, some != 0);
+            }
             __syncthreads();
-            const i32x4 found = lds_read<i32x4>(stage + R::BAD);
-            bad = __builtin_amdgcn_readfirstlane(found[0] | found[1] | found[2] | found[3]) != 0;
+        } else {
+            __syncthreads();                             // this tile has arrived, and every wave is done with the one before it
         }
+        const i32x4 live4 = lds_read<i32x4>(stage + R::LIVE);
+        if constexpr (!E4M3)
+            if (i + R::NB - 1 < tiles) copy(i + R::NB - 1, row_of(i + R::NB - 1, next));
+        const bool live = __builtin_amdgcn_readfirstlane(live4[0] & live4[1] & live4[2] & live4[3]) != 0;
+        const bool whole = live && whole_for(key0, pos_min, pos_max);
+        if constexpr (!E4M3)
+            if (!clean || !live) {
+                // as above, on the values in LDS, a wave its own 16
+                const bool paged = live4[wave] != 0;
+                bool odd = false;
+#pragma unroll
+                for (int j = 0; j < R::LOADS; ++j) {
+                    const int key = 16 * wave + j * R::KEYS + lane / R::PIECES;
+                    const uint32_t at = stage + R::V0 + 16 * wave * R::RB + j * 1024 + 16 * lane;
+                    if (paged && key0 + key < limit) odd |= nonfinite8(lds_read<u32x4>(at));
+                    else lds_write(at, u32x4{0u, 0u, 0u, 0u});
+                }
+                const uint64_t some = __ballot(odd);
+                if (lane == 0) lds_write<int>(stage + R::BAD + 4 * wave, some != 0);
+                __syncthreads();
+            }
         // the keys of the tile that this lane's row sees, its half's first key in bit 0
         const auto seen_keys = [&] {
             uint64_t m = ~0ull;
@@ -928,6 +1115,7 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                         const f32x4 k = lds_read<f32x4>(stage + R::KS + (32 * x + 2 * e + 4 * hf) * 4);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) s[x][e + r] *= k[r];
+                        __builtin_amdgcn_sched_barrier(0);
                     }
             }
             if (!whole) {
@@ -940,12 +1128,12 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                         s[x][e] = w & (1u << (8 * (e >> 2) + (e & 3))) ? s[x][e] : -__builtin_inff();
                 }
             }
-            float top = fmaxf(s[0][0], s[1][0]);
+            float top = larger(s[0][0], s[1][0]);
 #pragma unroll
-            for (int e = 1; e < 16; ++e) top = fmaxf(top, fmaxf(s[0][e], s[1][e]));
+            for (int e = 1; e < 16; ++e) top = larger(top, larger(s[0][e], s[1][e]));
             float t2;
             top = both32(top, t2);
-            top = fmaxf(top, t2) * scale2;
+            top = larger(top, t2) * scale2;
             if (__ballot(run.outgrown(top))) {
                 const float w = run.follow(top);
 #pragma unroll
@@ -974,6 +1162,7 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                         }
                     }
                     p[2 * x + y] = pack8(f);
+                    if constexpr (E4M3) __builtin_amdgcn_sched_barrier(0);       // registers: its scales one group at a time
                 }
             // V^T: lane (c, hf) takes element 32 d + c of keys 16 y + 4 hf .. and 16 y + 8 + 4 hf ..
             auto values = [&](int d, int y) {
@@ -981,7 +1170,12 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                 const u32x2 v0 = lds_columns_b16(at), v1 = lds_columns_b16(at + 8 * R::RB);
                 return u32x4{v0.x, v0.y, v1.x, v1.y};
             };
-            if (whole || !bad) {
+            bool bad = false;
+            if (!whole) {
+                const i32x4 found = lds_read<i32x4>(stage + R::BAD);
+                bad = __builtin_amdgcn_readfirstlane(found[0] | found[1] | found[2] | found[3]) != 0;
+            }
+            if (!bad) {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
@@ -990,40 +1184,57 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                         o[d] = mfma_bf16_32x32x16(as_bf16x8(values(d, y)), as_bf16x8(p[y]), o[d]);
                 feed_products<D / 8, 2, 4>();
             } else {
-                // column by column, with zeros for what that column does not see (a probability times a scale
-                // that is not finite is a zero there, too)
+                // Column by column, with zeros for what that column does not see (a probability times a scale that is
+                // not finite is a zero there, too).  The results wait in memory: the registers are the other path's.
+                f32x16 parked[D / 32];
+                u32x4 parked_p[4];
+                in_memory(parked);
+                in_memory(parked_p);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const uint32_t w = (uint32_t)(seen_keys() >> (16 * y));
-                    const uint32_t mine8 = (w & 15u) | (w >> 4 & 0xf0u);
+                for (int d = 0; d < D / 32; ++d) parked[d] = o[d];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        p[y][e] &= (mine8 >> (2 * e) & 1 ? 0xffffu : 0u) | (mine8 >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+                for (int y = 0; y < 4; ++y) parked_p[y] = p[y];
+                in_memory(parked);
+                in_memory(parked_p);
+                const uint64_t seen = seen_keys();
 #pragma unroll 1
-                    for (int col = 0; col < 32; ++col) {
-                        const uint32_t its = __shfl(mine8, col + 32 * hf, 64);
-                        u32x4 keep;
+                for (int d = 0; d < D / 32; ++d) {
+                    f32x16 sum = parked[d];
+#pragma unroll 1
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t w = (uint32_t)(seen >> (16 * y)), mine8 = (w & 15u) | (w >> 4 & 0xf0u);
+                        const u32x4 v = values(d, y);
+                        u32x4 its = parked_p[y], keep;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            keep[e] = (its >> (2 * e) & 1 ? 0xffffu : 0u) | (its >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+                            its[e] &= (mine8 >> (2 * e) & 1 ? 0xffffu : 0u) | (mine8 >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+#pragma unroll 1
+                        for (int col = 0; col < 32; ++col) {
+                            const uint32_t of = __shfl(mine8, col + 32 * hf, 64);
 #pragma unroll
-                        for (int d = 0; d < D / 32; ++d) {
-                            const f32x16 r = mfma_bf16_32x32x16(as_bf16x8(values(d, y) & keep), as_bf16x8(p[y]), o[d]);
-                            if (c == col) o[d] = r;
-                            __builtin_amdgcn_sched_barrier(0);
+                            for (int e = 0; e < 4; ++e)
+                                keep[e] = (of >> (2 * e) & 1 ? 0xffffu : 0u) | (of >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+                            const f32x16 r = mfma_bf16_32x32x16(as_bf16x8(v & keep), as_bf16x8(its), sum);
+                            if (c == col) sum = r;
                         }
                     }
+                    parked[d] = sum;
+                }
+                in_memory(parked);
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d) {
+                    o[d] = parked[d];
+                    asm volatile("" : "+v"(o[d]));       // arrived: see above
                 }
             }
         }
-        if constexpr (E4M3)
-            if (i + 1 < tiles) place(i + 1);
+        next = page_of(i + FAR + 1);                     // on its way while the waves gather (LDS reads would wait for it)
     }
 
     float t2;
     float l = both32(run.l, t2);
     l += t2;
-    float m = run.m;
+    const float m = run.m;
     // element 32 d + 8 y + 4 hf + r of the row is o[d][4 y + r]
     if constexpr (PREFIX) {
         if (!mine) return;
@@ -1037,63 +1248,18 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
         if (hf == 0) *reinterpret_cast<f32x2*>(a.prior_ml + 2 * row) = f32x2{m, l};
         return;
     }
-    // joins another part of this row, its elements given four at a time
-    auto join = [&](float m2, float l2, auto&& part) {
-        const float m1 = fmaxf(m, m2);
-        const float ref = m1 == -__builtin_inff() ? 0.0f : m1;
-        const float w1 = __builtin_amdgcn_exp2f(m - ref), w2 = __builtin_amdgcn_exp2f(m2 - ref);
-        m = m1;
-        l = l * w1 + l2 * w2;
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const f32x4 v = part(32 * d + 8 * y + 4 * hf);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[d][4 * y + r] = o[d][4 * y + r] * w1 + v[r] * w2;
-            }
-    };
-    if (item.chunks > 1) {
-        float* slot = a.slots + ((int64_t)item.first * a.Hkv + (int64_t)h * item.chunks) * R::SLOT;
-        const int r = 32 * wave + c;
-        if (mine) {
-            float* to = slot + (int64_t)item.chunk * R::SLOT;
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const float v[4] = {o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]};
-                    store_agent<4>(to + r * D + 32 * d + 8 * y + 4 * hf, v);
-                }
-            const float ml[2] = {m, l};
-            if (hf == 0) store_agent<2>(to + R::BM * D + 2 * r, ml);
-        }
-        unsigned* counter = a.counters + (int64_t)item.first * a.Hkv + h;
-        if (!arrive_and_check_last(counter, item.chunks, reinterpret_cast<int*>(smem + R::FLAG))) return;
-        if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (!mine) return;
-        m = -__builtin_inff();
-        l = 0.0f;
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
-        for (int x = 0; x < item.chunks; ++x) {
-            const float* from = slot + (int64_t)x * R::SLOT;
-            float ml[2];
-            load_agent<2>(from + R::BM * D + 2 * r, ml);
-            join(ml[0], ml[1], [&](int at) {
-                float v[4];
-                load_agent<4>(from + r * D + at, v);
-                return f32x4{v[0], v[1], v[2], v[3]};
-            });
-        }
-    }
     if (!mine) return;
-    for (int x = 0; x < a.prior_chunks; ++x) {
-        const int64_t row = ((int64_t)x * a.Hkv + h) * ((int64_t)a.T * a.G) + (int64_t)token * a.G + my_row % a.G;
-        join(a.prior_ml[2 * row], a.prior_ml[2 * row + 1],
-             [&](int at) { return *reinterpret_cast<const f32x4*>(a.prior + row * D + at); });
+    if (item.chunks > 1 || a.prior_chunks) {             // a part: attention_join_kernel joins them
+        const int r = 32 * wave + c;
+        float* slot = a.slots + ((int64_t)item.first * a.Hkv + (int64_t)h * item.chunks + item.chunk) * R::SLOT;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                *reinterpret_cast<f32x4*>(slot + r * D + 32 * d + 8 * y + 4 * hf) =
+                    f32x4{o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]};
+        if (hf == 0) *reinterpret_cast<f32x2*>(slot + R::BM * D + 2 * r) = f32x2{m, l};
+        return;
     }
     const int64_t row = (int64_t)token * a.Hq + head;
 #pragma unroll
@@ -1109,43 +1275,89 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
         }
 }
 
+// Joins the parts that attention_tiles_kernel left: 16 rows of a row tile a workgroup, so
+// that the parts' 66 KB of each tile and chunk are read by many CUs (joined by the last
+// workgroup of a tile, 64 chunks took 120 us).
+template <int D>
+__global__ __launch_bounds__(256) void attention_join_kernel(Call a) {
+    using R = Tiles<D, false>;
+    __shared__ __attribute__((aligned(16))) unsigned char smem[kJoinBytes<D>];
+    constexpr int GROUPS = R::BM / 16;
+    const int h = blockIdx.x % a.Hkv, group = blockIdx.x / a.Hkv % GROUPS;
+    Item item;
+    if (!find_item<R::BM, R::TK, true, true>(a, (int)(blockIdx.x / a.Hkv / GROUPS), item)) return;
+    if (item.chunks == 1 && !a.prior_chunks) return;     // written already
+    const int row0 = item.row0 + 16 * group;
+    const int rows = min(16, item.s.tokens * a.G - row0);
+    if (rows <= 0) return;
+    const float* slot = a.slots + ((int64_t)item.first * a.Hkv + (int64_t)h * item.chunks) * R::SLOT + 16 * group * D;
+    constexpr int N = D / 16;
+    Joined<N> j;
+    join_parts<D>(a, smem, h, rows, (int64_t)item.s.first_token * a.G + row0, slot, R::SLOT,
+                  R::BM * D - 16 * group * D + 2 * 16 * group, item.chunks, j);
+    const int r = threadIdx.x >> 4, at = row0 + r;
+    if (r < rows)
+        store_row<N>(a, D, (int64_t)(item.s.first_token + at / a.G) * a.Hq + h * a.G + at % a.G, (threadIdx.x & 15) * N, j);
+}
+
 // ---------------------------------------------------------------------------
 // The plan of a call, from its sizes alone.
 // ---------------------------------------------------------------------------
 struct Plan {
-    bool rows, tiles;            // which kernels run
-    int row_items, row_target;   // their work items for each key head at most; chunks wanted (0: keys are not split)
-    int tile_items, tile_target;
-    int prior_chunks, prior_tiles;       // of the shared prefix: chunks, and key tiles of one
+    bool rows, tiles, join;      // which kernels run
+    int row_items, row_target, row_least;        // their work items for each key head at most; chunks wanted (0: keys are
+    int tile_items, tile_target, tile_tiles;     // not split) and key tiles of one at least; row tiles
+    int prior_chunks, prior_tiles;               // of the shared prefix: chunks, and key tiles of one
+    bool stream;
     size_t slots, prior;         // floats
     size_t bytes() const { return slots + prior ? kCounterBytes + (slots + prior) * 4 : 0; }
 };
 
-Plan plan_of(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, int prefix, int max_q) {
+Plan plan_of(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, bool e4m3, int prefix, int max_q) {
     const int64_t G = Hq / Hkv, all = (int64_t)T * G;
     const int64_t cus = device_cu_count();
+    const int64_t most_rows = max_q > 0 ? std::min(all, max_q * G) : all;        // of a sequence
     Plan p{};
-    // Sequences of up to 16 rows stream their keys; more rows are worth tiles.  A ragged
-    // batch (fewer tokens than B times the largest count) holds both.
-    p.rows = max_q > 0 && max_q * G <= kFewRows;
+    // A shared prefix is worth a pass of its own from 64 MB of rereading on (that pass and its
+    // partial results cost about 12 us).
+    if ((int64_t)(B - 1) * prefix * Hkv * D * 4 < (int64_t)64 << 20) prefix = 0;
+    const int64_t own = max_kv - prefix;
+    // Sequences of up to 16 rows stream their keys; more rows are worth tiles.  A ragged batch (fewer tokens than B
+    // times the largest count) holds both.
+    p.rows = most_rows <= kFewRows;
     p.tiles = !p.rows;
     if (p.tiles && B > 1 && !(max_q > 0 && (int64_t)max_q * B == T)) p.rows = true;
-    const int64_t own = max_kv - prefix;
-    // Keys are split while row tiles leave workgroups free: four a CU, each of 256 keys at least
-    // (rows), two a CU of 256 keys at least (tiles).
-    auto split = [&](int64_t tiles, int64_t want, int BM, int& items, int& target) {
-        items = (int)tiles;
-        if (tiles < want && own > 256 && (tiles + want) * Hkv <= kMaxCounters) {
-            target = (int)want;
-            items = (int)(tiles + want);
-            p.slots = std::max(p.slots, (size_t)items * Hkv * BM * (D + 2));
+    if (p.rows) {
+        // beside the other kernel a sequence of few rows is one row tile
+        const int64_t tiles = p.tiles ? std::min<int64_t>(T, B) : std::min(all, all / 16 + B);
+        // Keys are split while the row tiles do not fill the GPU: into chunks of at least 256 keys for one workgroup a CU;
+        // from a row tile a CU on into finer ones of at least 1024 keys, which even out lengths.
+        const bool few = tiles * Hkv < cus;
+        const int64_t want = std::clamp<int64_t>((few ? 1 : 4) * cus / Hkv, 1, 160);
+        p.row_items = (int)tiles;
+        p.row_least = few ? 2 : 8;
+        if (tiles < want && own > 128 * p.row_least && (tiles + want) * Hkv <= kMaxCounters) {
+            p.row_target = (int)want;
+            p.row_items = (int)(tiles + want);
+            p.slots = (size_t)p.row_items * Hkv * 16 * (D + 2);
         }
-    };
-    if (p.rows) split(std::min(all, all / 16 + B), std::max<int64_t>(4 * cus / Hkv, 1), 16, p.row_items, p.row_target);
-    if (p.tiles) split(std::min(all, all / 128 + B), std::max<int64_t>(2 * cus / Hkv, 1), 128, p.tile_items, p.tile_target);
+        // read once, past the caches, where they cannot hold it
+        p.stream = !p.tiles && (int64_t)B * own * Hkv * D * (e4m3 ? 2 : 4) > (int64_t)128 << 20;
+    }
+    if (p.tiles) {
+        const int64_t tiles = std::min(all, all / 128 + B);
+        const int64_t want = std::clamp<int64_t>(2 * cus / Hkv, 1, 160);
+        p.tile_items = p.tile_tiles = (int)tiles;
+        if (tiles < want && own > 256) {
+            p.tile_target = (int)want;
+            p.tile_items = (int)(tiles + want);
+        }
+        p.join = p.tile_target || prefix > 0;
+        if (p.join) p.slots = std::max(p.slots, (size_t)p.tile_items * Hkv * 128 * (D + 2));
+    }
     if (prefix > 0) {
         const int64_t tiles = (prefix + 63) / 64, rows = (all + 127) / 128;
-        const int64_t chunks = std::clamp<int64_t>(2 * cus / (rows * Hkv), 1, (tiles + 3) / 4);
+        const int64_t chunks = std::clamp<int64_t>(2 * cus / (rows * Hkv), 1, std::min<int64_t>((tiles + 3) / 4, 64));
         p.prior_tiles = (int)((tiles + chunks - 1) / chunks);
         p.prior_chunks = (int)((tiles + p.prior_tiles - 1) / p.prior_tiles);
         p.prior = (size_t)p.prior_chunks * Hkv * all * (D + 2);
@@ -1162,7 +1374,7 @@ void launch(Kernel* kernel, std::atomic<uint64_t>& done, int64_t workgroups, int
 template <int D, bool E4M3>
 void launch_all(Call a, const Plan& p, void* ws, hipStream_t st) {
     using R = Rows<D, E4M3>;
-    using M = Tiles<D>;
+    using M = Tiles<D, E4M3>;
     static std::atomic<uint64_t> rows_done{0}, tiles_done{0}, prior_done{0};
     a.counters = static_cast<unsigned*>(ws);
     a.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kCounterBytes);
@@ -1183,27 +1395,31 @@ void launch_all(Call a, const Plan& p, void* ws, hipStream_t st) {
         c.target = p.tile_target;
         c.least = 4;
         launch(&attention_tiles_kernel<D, E4M3, false>, tiles_done, (int64_t)c.items * a.Hkv, M::LDS, c, st);
+        if (p.join) attention_join_kernel<D><<<dim3((unsigned)(p.tile_tiles * a.Hkv * (M::BM / 16))), 256, 0, st>>>(c);
     }
     if (p.rows) {
         a.few = p.tiles ? 1 : -1;
         a.items = p.row_items;
         a.target = p.row_target;
-        a.least = 2;
-        launch(&attention_rows_kernel<D, E4M3>, rows_done, (int64_t)a.items * a.Hkv, R::WAVES * R::WAVE_BYTES, a, st);
+        a.least = p.row_least;
+        a.stream = p.stream;
+        launch(&attention_rows_kernel<D, E4M3>, rows_done, (int64_t)a.items * a.Hkv, R::LDS, a, st);
     }
 }
 
 }  // namespace
 
 size_t paged_attention_workspace_bytes(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, int prefix, int max_q) {
-    return T == 0 || B == 0 ? 0 : plan_of(T, B, max_kv, Hq, Hkv, D, prefix, max_q).bytes();
+    return T == 0 || B == 0 ? 0 : plan_of(T, B, max_kv, Hq, Hkv, D, false, prefix, max_q).bytes();
 }
 
 void launch_paged_attention(const AttentionArgs& args, int D, void* ws, hipStream_t st) {
     Call a{args};
     a.G = a.Hq / a.Hkv;
     a.scale2 = a.scale * 1.44269504088896340736f;
-    const Plan p = plan_of(a.T, a.B, (int64_t)a.max_pages << a.page_shift, a.Hq, a.Hkv, D, a.prefix, a.max_q);
+    a.shared = a.prefix;
+    const Plan p = plan_of(a.T, a.B, (int64_t)a.max_pages << a.page_shift, a.Hq, a.Hkv, D, a.k_scale != nullptr, a.prefix, a.max_q);
+    if (!p.prior_chunks) a.prefix = 0;                   // every sequence reads the shared pages for itself
     if (D == 64) a.k_scale ? launch_all<64, true>(a, p, ws, st) : launch_all<64, false>(a, p, ws, st);
     else a.k_scale ? launch_all<128, true>(a, p, ws, st) : launch_all<128, false>(a, p, ws, st);
 }
