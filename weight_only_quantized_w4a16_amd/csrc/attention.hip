@@ -40,7 +40,7 @@ struct Call : AttentionArgs {
     float scale2;                // scale log2(e)
     // the plan
     int items;                   // work items for each key head at most, below 2^24
-    int few;                     // 1: sequences of up to kFewRows rows; 0: the others; -1: all
+    int few, few_rows;           // few = 1: sequences of up to few_rows rows; 0: the others; -1: all
     int target;                  // chunks wanted for each key head over the whole batch; 0: keys are not split
     int least;                   // tiles of a chunk at least
     unsigned* counters;          // one a split row tile, zero between calls
@@ -51,8 +51,6 @@ struct Call : AttentionArgs {
     int prior_chunks;
     float *prior, *prior_ml;
 };
-// rows of a sequence that the kernel of one row tile takes at once
-constexpr int kFewRows = 16;
 
 // Key tiles that some token of a sequence sees: [begin0, end0) around the first
 // positions and [begin1, end1), in tiles of TK positions.
@@ -101,7 +99,7 @@ __device__ __forceinline__ bool find_item(const Call& a, int it, Item& item) {
     };
     auto rows_of = [&](const Sequence& s) {
         const int rows = s.tokens * a.G;
-        return a.few < 0 || (rows <= kFewRows) == (a.few != 0) ? (rows + BM - 1) / BM : 0;
+        return a.few < 0 || (rows <= a.few_rows) == (a.few != 0) ? (rows + BM - 1) / BM : 0;
     };
     int chunk_tiles = 0x7fffffff;
     int lo, hi, len;
@@ -1305,6 +1303,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Call a) {
 // ---------------------------------------------------------------------------
 struct Plan {
     bool rows, tiles, join;      // which kernels run
+    int few_rows;                // of a sequence, for the first of them
     int row_items, row_target, row_least;        // their work items for each key head at most; chunks wanted (0: keys are
     int tile_items, tile_target, tile_tiles;     // not split) and key tiles of one at least; row tiles
     int prior_chunks, prior_tiles;               // of the shared prefix: chunks, and key tiles of one
@@ -1322,14 +1321,18 @@ Plan plan_of(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, bool e4m3, in
     // partial results cost about 12 us).
     if ((int64_t)(B - 1) * prefix * Hkv * D * 4 < (int64_t)64 << 20) prefix = 0;
     const int64_t own = max_kv - prefix;
-    // Sequences of up to 16 rows stream their keys; more rows are worth tiles.  A ragged batch (fewer tokens than B
-    // times the largest count) holds both.
-    p.rows = most_rows <= kFewRows;
+    // Sequences of few rows stream their keys, more are worth tiles.  Where the caches hold what the row tiles of a sequence
+    // read again, few is up to 64 rows (32 / 64 rows, one sequence of 8192 keys: 19.5 / 20.5 us, on tiles 29.6 / 30.8; 64
+    // sequences of up to 600 keys, 48 rows: 19 and 38), else 16 (32 rows, 64 sequences of 8192 keys: 403 and 362 us).  A
+    // ragged batch (fewer tokens than B times the largest count) holds both.
+    const bool large = (int64_t)B * own * Hkv * D * (e4m3 ? 2 : 4) > (int64_t)128 << 20;
+    p.few_rows = large ? 16 : 64;
+    p.rows = most_rows <= p.few_rows;
     p.tiles = !p.rows;
     if (p.tiles && B > 1 && !(max_q > 0 && (int64_t)max_q * B == T)) p.rows = true;
     if (p.rows) {
-        // beside the other kernel a sequence of few rows is one row tile
-        const int64_t tiles = p.tiles ? std::min<int64_t>(T, B) : std::min(all, all / 16 + B);
+        int64_t tiles = std::min(all, all / 16 + B);
+        if (p.tiles) tiles = std::min<int64_t>(tiles, (int64_t)B * (p.few_rows / 16));
         // Keys are split while the row tiles do not fill the GPU: into chunks of at least 256 keys for one workgroup a CU;
         // from a row tile a CU on into finer ones of at least 1024 keys, which even out lengths.
         const bool few = tiles * Hkv < cus;
@@ -1341,8 +1344,9 @@ Plan plan_of(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, bool e4m3, in
             p.row_items = (int)(tiles + want);
             p.slots = (size_t)p.row_items * Hkv * 16 * (D + 2);
         }
-        // read once, past the caches, where they cannot hold it
-        p.stream = !p.tiles && (int64_t)B * own * Hkv * D * (e4m3 ? 2 : 4) > (int64_t)128 << 20;
+        // read once, past the caches, where they cannot hold it: 64 x 8192 keys 356 -> 317 us (6.0 -> 6.8 TB/s), e4m3 196 -> 172;
+        // 67 MB that the caches did hold 21.0 -> 22.7
+        p.stream = large && !p.tiles;
     }
     if (p.tiles) {
         const int64_t tiles = std::min(all, all / 128 + B);
@@ -1388,6 +1392,7 @@ void launch_all(Call a, const Plan& p, void* ws, hipStream_t st) {
         launch(&attention_tiles_kernel<D, E4M3, true>, prior_done, (rows + M::BM - 1) / M::BM * p.prior_chunks * a.Hkv, M::LDS, c, st);
     }
     a.prior_chunks = p.prior_chunks;
+    a.few_rows = p.few_rows;
     if (p.tiles) {
         Call c = a;
         c.few = p.rows ? 0 : -1;
@@ -1410,7 +1415,9 @@ void launch_all(Call a, const Plan& p, void* ws, hipStream_t st) {
 }  // namespace
 
 size_t paged_attention_workspace_bytes(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, int prefix, int max_q) {
-    return T == 0 || B == 0 ? 0 : plan_of(T, B, max_kv, Hq, Hkv, D, false, prefix, max_q).bytes();
+    if (T == 0 || B == 0) return 0;
+    return std::max(plan_of(T, B, max_kv, Hq, Hkv, D, false, prefix, max_q).bytes(),
+                    plan_of(T, B, max_kv, Hq, Hkv, D, true, prefix, max_q).bytes());
 }
 
 void launch_paged_attention(const AttentionArgs& args, int D, void* ws, hipStream_t st) {
