@@ -63,7 +63,7 @@ __device__ __forceinline__ Span span_of(const Call& a, const Sequence& s) {
     const int limit = (int)min((int64_t)s.len, (int64_t)a.max_pages << a.page_shift);
     int lo = a.prefix, seen_first = 0;
     if (a.window > 0) {
-        lo = max(lo, s.len - s.tokens - a.window + 1);
+        lo = max(lo, min(s.len - s.tokens - a.window + 1, limit));       // (a length past the table leaves no tile)
         seen_first = min(min(a.sinks, lo), limit);
     }
     Span r;
@@ -149,7 +149,7 @@ __device__ __forceinline__ bool find_item(const Call& a, int it, Item& item) {
             return item.first + item.chunks <= a.items;
         }
         carry = total;
-        if (BY_TILE) carry_items = __builtin_amdgcn_readlane(incl_items, 63);
+        if (BY_TILE) carry_items = min(__builtin_amdgcn_readlane(incl_items, 63), 1 << 24);
     }
     return false;
 }

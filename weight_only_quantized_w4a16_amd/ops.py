@@ -925,3 +925,128 @@ class MoeRouting:
             dw = torch.empty((self.B, self.k), dtype=torch.float32, device=dy.device)
             moe_combine_backward(dy, rows, self.row_of_slot, self._weights(weights), self.B, self.k, K, drows, dw)
         return drows, dw
+
+
+# ---- from the qkv product to the o product: tensor-level helpers -----------------
+
+def rotary_frequencies(rotary_dim, base=10000.0, device="cuda"):
+    """fp64 [rotary_dim / 2] radians a position: base^(-2 i / rotary_dim)."""
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    return base ** (-2.0 * i / max(rotary_dim, 1))
+
+
+def _rotation(inv_freq):
+    """(inv_freq or None, rotary_dim)"""
+    if inv_freq is None:
+        return None, 0
+    _is(inv_freq, (torch.float64,), (inv_freq.numel(),), "inv_freq")
+    return inv_freq, 2 * inv_freq.numel()
+
+
+def _fused(qkv, q_heads, kv_heads, head_dim):
+    T = qkv.shape[0]
+    _is(qkv, _BF16, (T, (q_heads + 2 * kv_heads) * head_dim), "qkv")
+    return T
+
+
+def _head_weight(w, head_dim, what):
+    return None if w is None else _is(w, _BF16, (head_dim,), what)
+
+
+def norm_rope(qkv, positions, q_heads, kv_heads, head_dim, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+              interleaved=False, stream=None):
+    """(q [T, q_heads, D], k [T, kv_heads, D]) of fused rows [T, (q_heads + 2 kv_heads) D]: per head the RMS norm
+    with a bf16 weight [D] (None: none), then the rotation by int32 positions [T] (inv_freq None: none)."""
+    T = _fused(qkv, q_heads, kv_heads, head_dim)
+    _is(positions, (torch.int32,), (T,), "positions")
+    inv_freq, rot = _rotation(inv_freq)
+    wq, wk = _head_weight(q_weight, head_dim, "q_weight"), _head_weight(k_weight, head_dim, "k_weight")
+    with _on(stream, qkv):
+        q = torch.empty((T, q_heads, head_dim), dtype=torch.bfloat16, device=qkv.device)
+        k = torch.empty((T, kv_heads, head_dim), dtype=torch.bfloat16, device=qkv.device)
+        qk_norm_rope(qkv, wq, wk, eps, positions, inv_freq, rot, interleaved, T, q_heads, kv_heads, head_dim, q, k)
+    return q, k
+
+
+class PagedKVCache:
+    """Keys and values of one layer, [pages, kv_heads, page_size, head_dim]: bf16, or with fmt "e4m3" codes and a fp32
+    scale for each position and head.  What an unwritten row holds never matters."""
+
+    def __init__(self, pages, kv_heads, head_dim, page_size=64, fmt="bf16", device="cuda"):
+        if fmt not in ("bf16", "e4m3"):
+            raise ValueError(f"fmt must be 'bf16' or 'e4m3', got {fmt!r}")
+        self.pages, self.kv_heads, self.head_dim, self.page_size, self.fmt = pages, kv_heads, head_dim, page_size, fmt
+        shape = (pages, kv_heads, page_size, head_dim)
+        self.k, self.v = (torch.empty(shape, dtype=torch.bfloat16 if fmt == "bf16" else torch.uint8, device=device)
+                          for _ in range(2))
+        self.k_scale, self.v_scale = (None if fmt == "bf16" else torch.empty(shape[:3], dtype=torch.float32, device=device)
+                                      for _ in range(2))
+
+
+class PagedAttention(_Scratch):
+    """The attention of one layer over its PagedKVCache, between the qkv and the o product: norms of query and key heads
+    (bf16 weights [D] or None), rotation (inv_freq fp64, as from rotary_frequencies, or None), causal attention with an
+    optional sliding `window` and `sinks` first positions that stay visible.
+
+    The batch: q_offsets int32 [B + 1] (sequence b owns rows q_offsets[b] .. q_offsets[b + 1] - 1 of the new tokens),
+    kv_len int32 [B] its positions with the new tokens, block_table int32 [B, max_pages] its pages, all on the device.
+    Owns a reusable workspace: its calls must not overlap in time."""
+
+    def __init__(self, cache: PagedKVCache, q_heads, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                 scale=None, window=0, sinks=0):
+        self.cache, self.q_heads, self.eps, self.interleaved = cache, q_heads, float(eps), bool(interleaved)
+        self.inv_freq, self.rotary_dim = _rotation(inv_freq)
+        self.q_weight = _head_weight(q_weight, cache.head_dim, "q_weight")
+        self.k_weight = _head_weight(k_weight, cache.head_dim, "k_weight")
+        self.scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+        self.window, self.sinks = window, sinks
+
+    @staticmethod
+    def _batch(block_table, q_offsets, kv_len):
+        B = kv_len.shape[0]
+        _is(kv_len, (torch.int32,), (B,), "kv_len")
+        _is(q_offsets, (torch.int32,), (B + 1,), "q_offsets")
+        if block_table.dim() != 2:
+            raise ValueError(f"block_table: expected [{B}, max_pages], got {tuple(block_table.shape)}")
+        _is(block_table, (torch.int32,), (B, block_table.shape[1]), "block_table")
+        return B, block_table.shape[1]
+
+    def append(self, qkv, block_table, q_offsets, kv_len, stream=None):
+        """Puts the new tokens' keys and values into the cache; their queries [T, q_heads, D], normed and rotated.
+        Rows of no sequence are not written."""
+        c = self.cache
+        T = _fused(qkv, self.q_heads, c.kv_heads, c.head_dim)
+        B, width = self._batch(block_table, q_offsets, kv_len)
+        with _on(stream, qkv):
+            q = torch.empty((T, self.q_heads, c.head_dim), dtype=torch.bfloat16, device=qkv.device)
+            kv_append(qkv, self.q_weight, self.k_weight, self.eps, self.inv_freq, self.rotary_dim, self.interleaved, q_offsets,
+                      kv_len, block_table, T, B, width, self.q_heads, c.kv_heads, c.head_dim, c.k, c.v, c.k_scale, c.v_scale,
+                      c.pages, c.page_size, q)
+        return q
+
+    def attend(self, q, block_table, q_offsets, kv_len, max_q=0, shared_prefix=0, with_lse=False, out=None, stream=None):
+        """bf16 [T, q_heads D], the o product's input (rows of no sequence are not written); with_lse: (out, fp32 [T, q_heads]
+        logarithms of the sums of exponentials).  max_q: the largest number of new tokens of a sequence, 0 for not known.
+        shared_prefix: the first positions of every sequence are the same pages (a multiple of the page size), read once."""
+        c = self.cache
+        T = q.shape[0]
+        _is(q, _BF16, (T, self.q_heads, c.head_dim), "q")
+        B, width = self._batch(block_table, q_offsets, kv_len)
+        with _on(stream, q):
+            if out is None:
+                out = torch.empty((T, self.q_heads * c.head_dim), dtype=torch.bfloat16, device=q.device)
+            else:
+                _is(out, _BF16, (T, self.q_heads * c.head_dim), "out")
+            lse = torch.empty((T, self.q_heads), dtype=torch.float32, device=q.device) if with_lse else None
+            need = paged_attention_workspace_bytes(T, B, width, self.q_heads, c.kv_heads, c.head_dim, c.page_size,
+                                                   shared_prefix, max_q)
+            ws, need = self._scratch(need, q.device)     # zero-filled once; every call resets the counters it uses
+            paged_attention(q, c.k, c.v, c.k_scale, c.v_scale, c.pages, c.page_size, q_offsets, kv_len, block_table, T, B,
+                            width, self.q_heads, c.kv_heads, c.head_dim, self.scale, self.window, self.sinks, shared_prefix,
+                            max_q, out, lse, ws, need)
+        return (out, lse) if with_lse else out
+
+    def __call__(self, qkv, block_table, q_offsets, kv_len, max_q=0, shared_prefix=0, stream=None):
+        """append, then attend."""
+        q = self.append(qkv, block_table, q_offsets, kv_len, stream)
+        return self.attend(q, block_table, q_offsets, kv_len, max_q, shared_prefix, stream=stream)
