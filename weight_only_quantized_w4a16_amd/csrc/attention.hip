@@ -805,9 +805,8 @@ __global__ __launch_bounds__(256, 2) void attention_rows_kernel(Call a) {
 // ---------------------------------------------------------------------------
 // Many rows (prefill, several tokens a sequence, a prefix shared by a batch): a
 // workgroup takes a row tile of 128, each of its four waves 32 rows, and goes over tiles of 64
-// keys that all waves read from LDS.  bf16 tiles are copied straight into LDS one tile
-// ahead; e4m3 codes go through registers, where they become bf16 (exact, and once for
-// all waves), their scales beside them.
+// keys that all waves read from LDS, where they are copied straight from the cache, one to
+// three tiles ahead.  e4m3 codes become bf16 (exact) as they are read.
 //
 // Bound by the matrix instructions and, nearly as much, by the exponentials: two
 // workgroups on a CU let one wave's softmax run under another's products.
@@ -815,24 +814,28 @@ __global__ __launch_bounds__(256, 2) void attention_rows_kernel(Call a) {
 template <int D, bool E4M3>
 struct Tiles {
     static constexpr int WAVES = 4, BM = 32 * WAVES, TK = 64;
-    static constexpr int RB = 2 * D, PIECES = RB / 16;   // a row of a tile that is multiplied: bf16
+    static constexpr int RB = E4M3 ? D : 2 * D, PIECES = RB / 16;        // a cached row
     static constexpr int KEYS = 64 / PIECES;             // keys of one copy
     static constexpr int LOADS = 16 / KEYS;              // a wave copies 16 keys and 16 values
-    static constexpr int K0 = 0, V0 = TK * RB, KS = 2 * TK * RB, VS = KS + 4 * TK, LIVE = VS + 4 * TK, BAD = LIVE + 16;
+    static constexpr int COPIES = 2 * LOADS + (E4M3 ? 1 : 0);
+    // a stage: keys, values, with e4m3 256 bytes of a wave's scales (16 of keys, 16 of values), and by wave whether
+    // its keys have a page and whether one of its values is not finite
+    static constexpr int K0 = 0, V0 = TK * RB, S0 = 2 * TK * RB, LIVE = S0 + (E4M3 ? 256 * WAVES : 0), BAD = LIVE + 16;
     static constexpr int STAGE = (BAD + 16 + 255) / 256 * 256;
-    // bf16: NB stages, one multiplied, the others on their way.  e4m3: one, and NR raw tiles of codes.
-    static constexpr int NB = E4M3 ? 1 : D == 64 ? 4 : 2, NR = E4M3 ? (D == 64 ? 4 : 2) : 0;
-    static constexpr int RLOADS = D / 64;                // copies of a wave's 16 raw keys
-    static constexpr int RAWK = 0, RAWV = 16 * D, RAWS = 32 * D, RAW = RAWS + 256;       // of one wave
-    static constexpr int COPIES = E4M3 ? 2 * RLOADS + 1 : 2 * LOADS;
-    static constexpr int RAW0 = NB * STAGE;
-    static constexpr int ENDS = RAW0 + NR * WAVES * RAW;                 // the waves' first and last positions
-    static constexpr int LDS = ENDS + 8 * WAVES;
+    static constexpr int NB = RB == 256 ? 2 : 4;         // stages: one multiplied, the others on their way
+    static constexpr int ENDS = NB * STAGE, LDS = ENDS + 8 * WAVES;      // and the waves' first and last positions
     static constexpr int SLOT = BM * (D + 2);            // floats
-    __device__ static __forceinline__ int swap_k(int key) { return PIECES == 16 ? key & 15 : (key >> 1) & 7; }
+    // Where a row's 16-byte piece lies: pieces change places by the key so that the lanes of a read meet different banks.
+    __device__ static __forceinline__ int swap_k(int key) {
+        return PIECES == 16 ? key & 15 : PIECES == 8 ? (key >> 1) & 7 : (key >> 2) & 3;
+    }
     __device__ static __forceinline__ int swap_v(int key) {
+        if (E4M3) return PIECES == 8 ? (key >> 1 & 1) * 2 + (key >> 3 & 1) * 4 : (key >> 3 & 1) * 2;
         return PIECES == 16 ? (key & 3) * 4 + (key >> 2 & 1) * 2 : (key >> 1 & 1) * 4 + (key >> 2 & 1) * 2;
     }
+    // what copy j's offsets differ by from the first copy's, beside 1024 j
+    static constexpr int flip_k(int j) { return 64 * j; }
+    static constexpr int flip_v(int j) { return E4M3 ? 64 * j : D == 128 ? j % 2 * 32 : 0; }
 };
 
 // PREFIX: the rows are all T tokens' and the keys the shared ones; partial results.
@@ -918,8 +921,7 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
         }
     }
 
-    // bf16: a wave brings 16 keys of every tile; the first copy's offset from their first row, from
-    // which copy j lies 64 j (keys; values of 128 elements: 32 (j % 2)) away by exclusive or
+    // a wave brings 16 keys of every tile; the first copy's offsets from their first row
     uint32_t koff = lane / R::PIECES * R::RB + ((lane % R::PIECES) ^ R::swap_k(lane / R::PIECES)) * 16;
     uint32_t voff = lane / R::PIECES * R::RB + ((lane % R::PIECES) ^ R::swap_v(lane / R::PIECES)) * 16;
     // the page of the wave's 16 keys of a tile (any entry of the table past the end); and their row in
@@ -934,29 +936,18 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
         return key < limit && page >= 0 && page < a.pages
             ? ((((int64_t)page * a.Hkv + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) : (int64_t)-1;
     };
-    // copies of tile i: bf16 straight into the stage that is multiplied, e4m3 into the wave's raw tile
-    uint32_t alive = 0;                                  // e4m3: which raw tiles' keys have a page
     auto copy = [&](int i, int64_t row) {
+        const uint32_t stage = lds0 + i % R::NB * R::STAGE, to = stage + 16 * wave * R::RB;
         const int64_t at = max(row, (int64_t)0);
-        if constexpr (E4M3) {
-            const int slot = i % R::NR;
-            const uint32_t to = lds0 + R::RAW0 + (slot * R::WAVES + wave) * R::RAW;
+        const unsigned char* k = static_cast<const unsigned char*>(a.k) + at * R::RB;
+        const unsigned char* v = static_cast<const unsigned char*>(a.v) + at * R::RB;
 #pragma unroll
-            for (int j = 0; j < R::RLOADS; ++j) {
-                lds_copy_b128(static_cast<const unsigned char*>(a.k) + at * D, j * 1024 + lane * 16, to + R::RAWK + j * 1024);
-                lds_copy_b128(static_cast<const unsigned char*>(a.v) + at * D, j * 1024 + lane * 16, to + R::RAWV + j * 1024);
-            }
-            lds_copy_b32((lane & 16 ? a.v_scale : a.k_scale) + at + (lane & 15), to + R::RAWS);
-            alive = (alive & ~(1u << slot)) | (uint32_t)(row >= 0) << slot;
-        } else {
-            const uint32_t stage = lds0 + i % R::NB * R::STAGE, to = stage + 16 * wave * R::RB;
-#pragma unroll
-            for (int j = 0; j < R::LOADS; ++j) {
-                lds_copy_b128(static_cast<const unsigned char*>(a.k) + at * R::RB, (koff ^ (64 * j)) + 1024 * j, to + R::K0 + j * 1024);
-                lds_copy_b128(static_cast<const unsigned char*>(a.v) + at * R::RB, (voff ^ (D == 128 ? j % 2 * 32 : 0)) + 1024 * j, to + R::V0 + j * 1024);
-            }
-            if (lane == 0) lds_write<int>(stage + R::LIVE + 4 * wave, row >= 0);
+        for (int j = 0; j < R::LOADS; ++j) {
+            lds_copy_b128(k, (koff ^ R::flip_k(j)) + 1024 * j, to + R::K0 + j * 1024);
+            lds_copy_b128(v, (voff ^ R::flip_v(j)) + 1024 * j, to + R::V0 + j * 1024);
         }
+        if constexpr (E4M3) lds_copy_b32((lane & 16 ? a.v_scale : a.k_scale) + at + (lane & 15), stage + R::S0 + 256 * wave);
+        if (lane == 0) lds_write<int>(stage + R::LIVE + 4 * wave, row >= 0);
     };
     // whether rows from position `first` to `last` see all of a tile
     const auto whole_for = [&](int key0, int first, int last) {
@@ -964,12 +955,12 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                (a.window <= 0 || key0 > last - a.window || key0 + R::TK - 1 < a.sinks);
     };
 
-    // a lane's place in a tile: its key's row with the first of its pieces, from which piece 2 ks (a
-    // step of keys) and 4 d (a block of values) away is an exclusive or (stages and rows are
-    // multiples of what it changes)
-    uint32_t kat = R::K0 + c * R::RB + (hf ^ R::swap_k(c)) * 16;
-    const int vkey = 4 * hf + (lane >> 2 & 3);
-    uint32_t vat = R::V0 + vkey * R::RB + ((2 * (c >> 4) + (lane >> 1 & 1)) ^ R::swap_v(vkey)) * 16 + (lane & 1) * 8;
+    // a lane's place in a tile: its key's row with the first of its pieces, from which that of another step of
+    // keys and block of values is an exclusive or away (stages and rows are multiples of what it changes)
+    uint32_t kat = R::K0 + c * R::RB + (E4M3 ? R::swap_k(c) * 16 + hf * 8 : (hf ^ R::swap_k(c)) * 16);
+    const int vkey = E4M3 ? 4 * hf + (lane >> 1 & 3) + (lane >> 3 & 1) * 8 : 4 * hf + (lane >> 2 & 3);
+    const int vpiece = E4M3 ? c >> 4 : 2 * (c >> 4) + (lane >> 1 & 1);
+    uint32_t vat = R::V0 + vkey * R::RB + (vpiece ^ R::swap_v(vkey)) * 16 + (lane & 1) * 8;
 
     // this lane's query: 8 elements of every 16, negated for a negative scale
     bf16x8 q[D / 16];
@@ -982,7 +973,7 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
     }
     const float scale2 = fabsf(a.scale2);
 
-    constexpr int FAR = E4M3 ? R::NR : R::NB - 1;        // tiles on their way
+    constexpr int FAR = R::NB - 1;                       // tiles on their way
     int page[FAR + 1];
 #pragma unroll
     for (int i = 0; i <= FAR; ++i) page[i] = page_of(i);
@@ -1001,83 +992,45 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
 
     for (int i = 0; i < tiles; ++i) {
         const int key0 = item.span.tile(i0 + i) * R::TK;
-        const uint32_t stage = lds0 + (E4M3 ? 0 : i % R::NB * R::STAGE);
+        const uint32_t stage = lds0 + i % R::NB * R::STAGE;
         // (what follows from these is computed anew in every tile: kept, it takes registers from the products)
         asm volatile("" : "+v"(kat), "+v"(vat), "+v"(koff), "+v"(voff));
-        wait_tiles<R::COPIES, E4M3 ? R::NR - 1 : R::NB - 2>(tiles - 1 - i);
-        const bool clean = whole_for(key0, all_min, all_max);
-        if constexpr (E4M3) {
-            // the wave's 16 keys and values become bf16.  Where a row of the workgroup does not see all keys, values
-            // of positions that hold no key become zeros, and a NaN or infinity among the others is found.
-            const int slot = i % R::NR;
-            const uint32_t raw = lds0 + R::RAW0 + (slot * R::WAVES + wave) * R::RAW;
-            const bool paged = alive >> slot & 1;
-            u32x4 kc[R::RLOADS], vc[R::RLOADS];
-#pragma unroll
-            for (int j = 0; j < R::RLOADS; ++j) {
-                kc[j] = lds_read<u32x4>(raw + R::RAWK + j * 1024 + lane * 16);
-                vc[j] = lds_read<u32x4>(raw + R::RAWV + j * 1024 + lane * 16);
-            }
-            float scale = lds_read<float>(raw + R::RAWS + (lane & 31) * 4);
-            bool odd = false;
-            if (!clean || !paged) {
-#pragma unroll
-                for (int j = 0; j < R::RLOADS; ++j) {
-                    const bool holds = paged && key0 + 16 * wave + (j * 1024 + lane * 16) / D < limit;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        odd |= holds && (((vc[j][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u);
-                        vc[j][e] = holds ? vc[j][e] : 0u;
-                    }
-                }
-                const bool holds = paged && key0 + 16 * wave + (lane & 15) < limit;
-                odd |= holds && (lane & 16) && !__builtin_isfinite(scale);
-                scale = holds ? scale : 0.0f;
-            }
-            const uint64_t some = __ballot(odd);
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            if (i + R::NR < tiles) copy(i + R::NR, row_of(i + R::NR, next));
-            __syncthreads();                             // every wave is done with the tile before
-#pragma unroll
-            for (int j = 0; j < R::RLOADS; ++j) {
-                const int key = (j * 1024 + lane * 16) / D, piece = (j * 1024 + lane * 16) % D / 8;
-                const uint32_t row = stage + (16 * wave + key) * R::RB;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    lds_write(row + R::K0 + ((piece + x) ^ R::swap_k(key)) * 16, e4m3_to_bf16(u32x2{kc[j][2 * x], kc[j][2 * x + 1]}));
-                    lds_write(row + R::V0 + ((piece + x) ^ R::swap_v(key)) * 16, e4m3_to_bf16(u32x2{vc[j][2 * x], vc[j][2 * x + 1]}));
-                }
-            }
-            if (lane < 32) lds_write(stage + (lane < 16 ? R::KS : R::VS) + 4 * (16 * wave + (lane & 15)), scale);
-            if (lane == 0) {
-                lds_write<int>(stage + R::LIVE + 4 * wave, paged);
-                lds_write<int>(stage + R::BAD + 4 * wave, some != 0);
-            }
-            __syncthreads();
-        } else {
-            __syncthreads();                             // this tile has arrived, and every wave is done with the one before it
-        }
+        wait_tiles<R::COPIES, R::NB - 2>(tiles - 1 - i);
+        __syncthreads();                                 // this tile has arrived, and every wave is done with the one before it
         const i32x4 live4 = lds_read<i32x4>(stage + R::LIVE);
-        if constexpr (!E4M3)
-            if (i + R::NB - 1 < tiles) copy(i + R::NB - 1, row_of(i + R::NB - 1, next));
+        if (i + FAR < tiles) copy(i + FAR, row_of(i + FAR, next));
         const bool live = __builtin_amdgcn_readfirstlane(live4[0] & live4[1] & live4[2] & live4[3]) != 0;
         const bool whole = live && whole_for(key0, pos_min, pos_max);
-        if constexpr (!E4M3)
-            if (!clean || !live) {
-                // as above, on the values in LDS, a wave its own 16
-                const bool paged = live4[wave] != 0;
-                bool odd = false;
+        if (!live || !whole_for(key0, all_min, all_max)) {
+            // Where a row of the workgroup does not see all keys: values of positions that hold no key become zeros
+            // (a wave its own 16), and a NaN or infinity among the others is found.
+            const bool paged = live4[wave] != 0;
+            bool odd = false;
 #pragma unroll
-                for (int j = 0; j < R::LOADS; ++j) {
-                    const int key = 16 * wave + j * R::KEYS + lane / R::PIECES;
-                    const uint32_t at = stage + R::V0 + 16 * wave * R::RB + j * 1024 + 16 * lane;
-                    if (paged && key0 + key < limit) odd |= nonfinite8(lds_read<u32x4>(at));
-                    else lds_write(at, u32x4{0u, 0u, 0u, 0u});
+            for (int j = 0; j < R::LOADS; ++j) {
+                const int key = 16 * wave + j * R::KEYS + lane / R::PIECES;
+                const uint32_t at = stage + R::V0 + 16 * wave * R::RB + j * 1024 + 16 * lane;
+                if (paged && key0 + key < limit) {
+                    const u32x4 v = lds_read<u32x4>(at);
+                    if constexpr (E4M3) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) odd |= (((v[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+                    } else {
+                        odd |= nonfinite8(v);
+                    }
+                } else {
+                    lds_write(at, u32x4{0u, 0u, 0u, 0u});
                 }
-                const uint64_t some = __ballot(odd);
-                if (lane == 0) lds_write<int>(stage + R::BAD + 4 * wave, some != 0);
-                __syncthreads();
             }
+            if (E4M3 && lane < 16) {
+                const uint32_t at = stage + R::S0 + 256 * wave + 64 + 4 * lane;
+                if (paged && key0 + 16 * wave + lane < limit) odd |= !__builtin_isfinite(lds_read<float>(at));
+                else lds_write(at, 0.0f);
+            }
+            const uint64_t some = __ballot(odd);
+            if (lane == 0) lds_write<int>(stage + R::BAD + 4 * wave, some != 0);
+            __syncthreads();
+        }
         // the keys of the tile that this lane's row sees, its half's first key in bit 0
         const auto seen_keys = [&] {
             uint64_t m = ~0ull;
@@ -1101,7 +1054,9 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const u32x4 k = lds_read<u32x4>(((stage + kat) ^ (32 * ks)) + 32 * x * R::RB);
+                    u32x4 k;
+                    if constexpr (E4M3) k = e4m3_to_bf16(lds_read<u32x2>(((stage + kat) ^ (16 * ks)) + 32 * x * R::RB));
+                    else k = lds_read<u32x4>(((stage + kat) ^ (32 * ks)) + 32 * x * R::RB);
                     s[x] = mfma_bf16_32x32x16(as_bf16x8(k), q[ks], s[x]);
                 }
             feed_products<D / 8, 1, 4>();
@@ -1110,7 +1065,7 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int e = 0; e < 16; e += 4) {
-                        const f32x4 k = lds_read<f32x4>(stage + R::KS + (32 * x + 2 * e + 4 * hf) * 4);
+                        const f32x4 k = lds_read<f32x4>(stage + R::S0 + 256 * (2 * x + e / 8) + (2 * e % 16 + 4 * hf) * 4);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) s[x][e + r] *= k[r];
                         __builtin_amdgcn_sched_barrier(0);
@@ -1153,7 +1108,7 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                     if constexpr (E4M3) {
 #pragma unroll
                         for (int e = 0; e < 8; e += 4) {
-                            const f32x4 v = lds_read<f32x4>(stage + R::VS + (32 * x + 16 * y + 2 * e + 4 * hf) * 4);
+                            const f32x4 v = lds_read<f32x4>(stage + R::S0 + 256 * (2 * x + y) + 64 + (2 * e + 4 * hf) * 4);
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
                                 f[e + r] *= v[r];
@@ -1164,6 +1119,7 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                 }
             // V^T: lane (c, hf) takes element 32 d + c of keys 16 y + 4 hf .. and 16 y + 8 + 4 hf ..
             auto values = [&](int d, int y) {
+                if constexpr (E4M3) return e4m3_to_bf16(lds_columns_b8(((stage + vat) ^ (32 * d)) + 16 * y * R::RB));
                 const uint32_t at = ((stage + vat) ^ (64 * d)) + 16 * y * R::RB;
                 const u32x2 v0 = lds_columns_b16(at), v1 = lds_columns_b16(at + 8 * R::RB);
                 return u32x4{v0.x, v0.y, v1.x, v1.y};
@@ -1180,7 +1136,7 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d)
                         o[d] = mfma_bf16_32x32x16(as_bf16x8(values(d, y)), as_bf16x8(p[y]), o[d]);
-                feed_products<D / 8, 2, 4>();
+                feed_products<D / 8, E4M3 ? 1 : 2, 4>();
             } else {
                 // Column by column, with zeros for what that column does not see (a probability times a scale that is
                 // not finite is a zero there, too).  The results wait in memory: the registers are the other path's.
