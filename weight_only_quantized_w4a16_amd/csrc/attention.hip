@@ -989,6 +989,12 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
+    f32x16 odd_o[D / 32];                                // the sums of tiles whose values are not all finite
+    in_memory(odd_o);
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) odd_o[d] = o[d];
+    in_memory(odd_o);
+    bool any_odd = false;
 
     for (int i = 0; i < tiles; ++i) {
         const int key0 = item.span.tile(i0 + i) * R::TK;
@@ -1091,6 +1097,9 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                 const float w = run.follow(top);
 #pragma unroll
                 for (int d = 0; d < D / 32; ++d) o[d] *= w;
+                if (any_odd)
+#pragma unroll 1
+                    for (int d = 0; d < D / 32; ++d) odd_o[d] *= w;
             }
             const float ref = run.reference();
             // P^T: the operand of 16 keys is eight neighbouring results
@@ -1139,26 +1148,22 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                 feed_products<D / 8, E4M3 ? 1 : 2, 4>();
             } else {
                 // Column by column, with zeros for what that column does not see (a probability times a scale that is
-                // not finite is a zero there, too).  The results wait in memory: the registers are the other path's.
-                f32x16 parked[D / 32];
-                u32x4 parked_p[4];
+                // not finite is a zero there, too).  These sums and the probabilities are kept in memory: the registers
+                // are the other path's.
+                u32x4 parked[4];
                 in_memory(parked);
-                in_memory(parked_p);
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d) parked[d] = o[d];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) parked_p[y] = p[y];
+                for (int y = 0; y < 4; ++y) parked[y] = p[y];
                 in_memory(parked);
-                in_memory(parked_p);
                 const uint64_t seen = seen_keys();
 #pragma unroll 1
                 for (int d = 0; d < D / 32; ++d) {
-                    f32x16 sum = parked[d];
+                    f32x16 sum = odd_o[d];
 #pragma unroll 1
                     for (int y = 0; y < 4; ++y) {
                         const uint32_t w = (uint32_t)(seen >> (16 * y)), mine8 = (w & 15u) | (w >> 4 & 0xf0u);
                         const u32x4 v = values(d, y);
-                        u32x4 its = parked_p[y], keep;
+                        u32x4 its = parked[y], keep;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             its[e] &= (mine8 >> (2 * e) & 1 ? 0xffffu : 0u) | (mine8 >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
@@ -1172,19 +1177,18 @@ __global__ __launch_bounds__(256, 2) void attention_tiles_kernel(Call a) {
                             if (c == col) sum = r;
                         }
                     }
-                    parked[d] = sum;
+                    odd_o[d] = sum;
                 }
-                in_memory(parked);
-#pragma unroll
-                for (int d = 0; d < D / 32; ++d) {
-                    o[d] = parked[d];
-                    asm volatile("" : "+v"(o[d]));       // arrived: see above
-                }
+                in_memory(odd_o);
+                any_odd = true;
             }
         }
         next = page_of(i + FAR + 1);                     // on its way while the waves gather (LDS reads would wait for it)
     }
 
+    if (any_odd)
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) o[d] += odd_o[d];
     float t2;
     float l = both32(run.l, t2);
     l += t2;
