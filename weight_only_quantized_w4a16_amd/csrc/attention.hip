@@ -808,10 +808,11 @@ __global__ __launch_bounds__(256, 2) void attention_rows_kernel(Call a) {
 // keys that all waves read from LDS, where they are copied straight from the cache, one to
 // three tiles ahead.  e4m3 codes become bf16 (exact) as they are read.
 //
-// Bound by the matrix instructions and, nearly as much, by the exponentials: two
-// workgroups on a CU let one wave's softmax run under another's products; heads of 64, with
-// half the products to as many exponentials, take three (7 ragged chunks under a window
-// of 512: 78 -> 68 us, e4m3 99 -> 86; 4096 rows of 8192: 293 -> 282, 377 -> 367).
+// Bound by the matrix instructions and, nearly as much, by the exponentials: a wave multiplies
+// the next tile's scores while it takes this one's exponentials (4096 rows of 8192 keys: 465 ->
+// 425 us, 970 TFLOP/s; e4m3 525 -> 485), and two workgroups on a CU let one's softmax run under
+// another's products; heads of 64, with half the products to as many exponentials, take three
+// (the same rows: 276 -> 269, e4m3 330 -> 320; 7 ragged chunks under a window of 512 75 -> 72).
 // ---------------------------------------------------------------------------
 template <int D, bool E4M3>
 struct Tiles {
@@ -824,7 +825,7 @@ struct Tiles {
     // its keys have a page and whether one of its values is not finite
     static constexpr int K0 = 0, V0 = TK * RB, S0 = 2 * TK * RB, LIVE = S0 + (E4M3 ? 256 * WAVES : 0), BAD = LIVE + 16;
     static constexpr int STAGE = (BAD + 16 + 255) / 256 * 256;
-    static constexpr int NB = RB == 256 ? 2 : D == 64 && RB == 128 ? 3 : 4;         // stages: one multiplied, the others on their way
+    static constexpr int NB = RB == 256 ? 2 : RB == 128 && D == 64 ? 3 : 4;         // stages: one multiplied, the others on their way
     static constexpr int ENDS = NB * STAGE, LDS = ENDS + 8 * WAVES;      // and the waves' first and last positions
     static constexpr int SLOT = BM * (D + 2);            // floats
     // Where a row's 16-byte piece lies: pieces change places by the key so that the lanes of a read meet different banks.
@@ -926,36 +927,56 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
     // a wave brings 16 keys of every tile; the first copy's offsets from their first row
     uint32_t koff = lane / R::PIECES * R::RB + ((lane % R::PIECES) ^ R::swap_k(lane / R::PIECES)) * 16;
     uint32_t voff = lane / R::PIECES * R::RB + ((lane % R::PIECES) ^ R::swap_v(lane / R::PIECES)) * 16;
-    // the page of the wave's 16 keys of a tile (any entry of the table past the end); and their row in
-    // the cache, -1 where they have no page
-    auto page_of = [&](int i) {
-        const int key = item.span.tile(i0 + i) * R::TK + 16 * wave;
+    const uint32_t page_bytes = ((uint32_t)a.Hkv << a.page_shift) * R::RB;
+    const unsigned char* keys = static_cast<const unsigned char*>(a.k) + ((int64_t)h << a.page_shift) * R::RB;
+    const unsigned char* values = static_cast<const unsigned char*>(a.v) + ((int64_t)h << a.page_shift) * R::RB;
+    // the first of the wave's keys of a tile, and their page (any entry of the table past the end)
+    auto key_of = [&](int i) { return item.span.tile(i0 + i) * R::TK + 16 * wave; };
+    auto page_of = [&](int key) {
         const int64_t b = PREFIX || key < a.shared ? 0 : item.b;
         return load_scalar(a.table + b * a.max_pages + min(key >> a.page_shift, a.max_pages - 1));
     };
-    auto row_of = [&](int i, int page) {
-        const int key = item.span.tile(i0 + i) * R::TK + 16 * wave;
-        return key < limit && page >= 0 && page < a.pages
-            ? ((((int64_t)page * a.Hkv + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) : (int64_t)-1;
+    // where they lie in the cache (without a page: anywhere in it)
+    struct Place {
+        int64_t at;
+        bool paged;
     };
-    auto copy = [&](int i, int64_t row) {
-        const uint32_t stage = lds0 + i % R::NB * R::STAGE, to = stage + 16 * wave * R::RB;
-        const int64_t at = max(row, (int64_t)0);
-        const unsigned char* k = static_cast<const unsigned char*>(a.k) + at * R::RB;
-        const unsigned char* v = static_cast<const unsigned char*>(a.v) + at * R::RB;
+    auto place_of = [&](int key, int page) {
+        const bool paged = key < limit && (unsigned)page < (unsigned)a.pages;
+        return Place{(int64_t)(paged ? page : 0) * page_bytes + (key & ((1 << a.page_shift) - 1)) * R::RB, paged};
+    };
+    auto copy_keys = [&](uint32_t stage, const Place& p) {
 #pragma unroll
-        for (int j = 0; j < R::LOADS; ++j) {
-            lds_copy_b128(k, (koff ^ R::flip_k(j)) + 1024 * j, to + R::K0 + j * 1024);
-            lds_copy_b128(v, (voff ^ R::flip_v(j)) + 1024 * j, to + R::V0 + j * 1024);
+        for (int j = 0; j < R::LOADS; ++j)
+            lds_copy_b128(keys + p.at, (koff ^ R::flip_k(j)) + 1024 * j, stage + R::K0 + 16 * wave * R::RB + j * 1024);
+    };
+    auto copy_values = [&](uint32_t stage, const Place& p) {
+#pragma unroll
+        for (int j = 0; j < R::LOADS; ++j)
+            lds_copy_b128(values + p.at, (voff ^ R::flip_v(j)) + 1024 * j, stage + R::V0 + 16 * wave * R::RB + j * 1024);
+        if constexpr (E4M3) {
+            const int64_t row = ((int64_t)h << a.page_shift) + p.at / R::RB;
+            lds_copy_b32((lane & 16 ? a.v_scale : a.k_scale) + row + (lane & 15), stage + R::S0 + 256 * wave);
         }
-        if constexpr (E4M3) lds_copy_b32((lane & 16 ? a.v_scale : a.k_scale) + at + (lane & 15), stage + R::S0 + 256 * wave);
-        if (lane == 0) lds_write<int>(stage + R::LIVE + 4 * wave, row >= 0);
+        if (lane == 0) lds_write<int>(stage + R::LIVE + 4 * wave, p.paged);
     };
-    // whether rows from position `first` to `last` see all of a tile
-    const auto whole_for = [&](int key0, int first, int last) {
-        return key0 >= key_begin && key0 + R::TK <= limit && key0 + R::TK - 1 <= first &&
-               (a.window <= 0 || key0 > last - a.window || key0 + R::TK - 1 < a.sinks);
+    // the tiles that rows from position `first` to `last` see all of
+    struct Whole {
+        int lo, n, sink_lo, sink_n;
+        __device__ __forceinline__ bool has(int tile) const {
+            return (unsigned)(tile - lo) < (unsigned)n || (unsigned)(tile - sink_lo) < (unsigned)sink_n;
+        }
     };
+    auto whole_for = [&](int first, int last) {
+        const int begin = (key_begin + R::TK - 1) / R::TK, end = (min(limit - 1, first) + 1) / R::TK;
+        Whole w;
+        w.lo = a.window > 0 && last >= a.window ? max((last - a.window) / R::TK + 1, begin) : begin;
+        w.n = max(end - w.lo, 0);
+        w.sink_lo = begin;
+        w.sink_n = a.window > 0 ? max(min(end, a.sinks / R::TK) - begin, 0) : 0;
+        return w;
+    };
+    const Whole all_whole = whole_for(all_min, all_max);
 
     // a lane's place in a tile: its key's row with the first of its pieces, from which that of another step of
     // keys and block of values is an exclusive or away (stages and rows are multiples of what it changes)
@@ -963,6 +984,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
     const int vkey = E4M3 ? 4 * hf + (lane >> 1 & 3) + (lane >> 3 & 1) * 8 : 4 * hf + (lane >> 2 & 3);
     const int vpiece = E4M3 ? c >> 4 : 2 * (c >> 4) + (lane >> 1 & 1);
     uint32_t vat = R::V0 + vkey * R::RB + (vpiece ^ R::swap_v(vkey)) * 16 + (lane & 1) * 8;
+    uint32_t sat = R::S0 + 16 * hf;                      // scales of keys 8 j + 4 hf ..: 256 (j / 2) + 32 (j % 2) on, of values 64 behind
 
     // this lane's query: 8 elements of every 16, negated for a negative scale
     bf16x8 q[D / 16];
@@ -975,15 +997,26 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
     }
     const float scale2 = fabsf(a.scale2);
 
-    constexpr int FAR = R::NB - 1;                       // tiles on their way
-    int page[FAR + 1];
+    // A stage holds a tile's values and the next tile's keys: while the softmax of a tile runs,
+    // the next one's scores are multiplied.
+    constexpr int FAR = R::NB - 1;                       // stages on their way
+    int page[FAR + 2];
 #pragma unroll
-    for (int i = 0; i <= FAR; ++i) page[i] = page_of(i);
-    int next = page[FAR];                                // the page of the tile to copy next
+    for (int i = 0; i < FAR + 2; ++i) page[i] = page_of(key_of(i));
     arrived(q);
+    uint32_t stage = lds0, behind = lds0 + FAR * R::STAGE;
+    Place place = place_of(key_of(0), page[0]);          // of the tile whose values are copied next
+    if (tiles > 0) copy_keys(behind, place);
 #pragma unroll
-    for (int i = 0; i < FAR; ++i)
-        if (i < tiles) copy(i, row_of(i, page[i]));
+    for (int i = 0; i < FAR; ++i) {
+        const Place after = place_of(key_of(i + 1), page[i + 1]);
+        if (i < tiles) {
+            copy_keys(lds0 + i * R::STAGE, after);
+            copy_values(lds0 + i * R::STAGE, place);
+        }
+        place = after;
+    }
+    int next_key = key_of(FAR + 1), next = page[FAR + 1];
 
     Running run;
     f32x16 o[D / 32];
@@ -998,18 +1031,58 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
     in_memory(odd_o);
     bool any_odd = false;
 
-    for (int i = 0; i < tiles; ++i) {
-        const int key0 = item.span.tile(i0 + i) * R::TK;
-        const uint32_t stage = lds0 + i % R::NB * R::STAGE;
+    // S^T of the keys in a stage: lane (c, hf) receives keys 32 x + 8 (e / 4) + 4 hf + e % 4 of column c.
+    // Product n takes elements n / 2 of keys 32 (n % 2) ..; its keys are on their way AHEAD products before.
+    constexpr int N = D / 8, AHEAD = 4;
+    using Fragment = std::conditional_t<E4M3, u32x2, u32x4>;
+    auto bf16_of = [&](Fragment f) {
+        if constexpr (E4M3) return as_bf16x8(e4m3_to_bf16(f));
+        else return as_bf16x8(f);
+    };
+    auto key_fragment = [&](uint32_t stage, int n) {
+        return lds_read<Fragment>(((stage + kat) ^ (n / 2 * (E4M3 ? 16 : 32))) + n % 2 * 32 * R::RB);
+    };
+    // V^T: lane (c, hf) takes element 32 d + c of keys 16 y + 4 hf .. and 16 y + 8 + 4 hf ..
+    auto value_fragment = [&](uint32_t stage, int d, int y) -> Fragment {
+        if constexpr (E4M3) {
+            return lds_columns_b8(((stage + vat) ^ (32 * d)) + 16 * y * R::RB);
+        } else {
+            const uint32_t at = ((stage + vat) ^ (64 * d)) + 16 * y * R::RB;
+            const u32x2 v0 = lds_columns_b16(at), v1 = lds_columns_b16(at + 8 * R::RB);
+            return u32x4{v0.x, v0.y, v1.x, v1.y};
+        }
+    };
+    auto scores = [&](uint32_t stage, f32x16 (&s)[2]) {
+        Fragment k[AHEAD];
+        static_for<AHEAD>([&](auto n) { k[n] = key_fragment(stage, n); });
+        static_for<2>([&](auto x) { s[x] = f32x16{}; });
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<N>([&](auto n_) {
+            constexpr int n = decltype(n_)::value;
+            s[n % 2] = mfma_bf16_32x32x16(bf16_of(k[n % AHEAD]), q[n / 2], s[n % 2]);
+            if constexpr (n + AHEAD < N) k[n % AHEAD] = key_fragment(stage, n + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    // one tile: its scores s, the next tile's s2
+    auto step = [&](int i, f32x16 (&s)[2], f32x16 (&s2)[2]) {
         // (what follows from these is computed anew in every tile: kept, it takes registers from the products)
-        asm volatile("" : "+v"(kat), "+v"(vat), "+v"(koff), "+v"(voff));
+        asm volatile("" : "+v"(kat), "+v"(vat), "+v"(sat), "+v"(koff), "+v"(voff));
         wait_tiles<R::COPIES, R::NB - 2>(tiles - 1 - i);
-        __syncthreads();                                 // this tile has arrived, and every wave is done with the one before it
+        __syncthreads();                                 // this stage has arrived, and every wave is done with the one behind
         const i32x4 live4 = lds_read<i32x4>(stage + R::LIVE);
-        if (i + FAR < tiles) copy(i + FAR, row_of(i + FAR, next));
+        if (i + FAR < tiles) {
+            const Place after = place_of(next_key, next);
+            copy_keys(behind, after);
+            copy_values(behind, place);
+            place = after;
+        }
+        const int tile = item.span.tile(i0 + i), key0 = tile * R::TK;
         const bool live = __builtin_amdgcn_readfirstlane(live4[0] & live4[1] & live4[2] & live4[3]) != 0;
-        const bool whole = live && whole_for(key0, pos_min, pos_max);
-        if (!live || !whole_for(key0, all_min, all_max)) {
+        bool whole = live && all_whole.has(tile), useful = pos_max >= 0;
+        if (!whole) {
+            whole = live && whole_for(pos_min, pos_max).has(tile);
+            useful = key0 <= pos_max && (a.window <= 0 || key0 + R::TK > pos_min - a.window || key0 < a.sinks);
             // Where a row of the workgroup does not see all keys: values of positions that hold no key become zeros
             // (a wave its own 16), and a NaN or infinity among the others is found.
             const bool paged = live4[wave] != 0;
@@ -1039,7 +1112,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
             if (lane == 0) lds_write<int>(stage + R::BAD + 4 * wave, some != 0);
             __syncthreads();
         }
-        // the keys of the tile that this lane's row sees, its half's first key in bit 0
+        // the keys of the tile that this lane's row sees
         const auto seen_keys = [&] {
             uint64_t m = ~0ull;
             if (a.window > 0) m = ~bits_to(pos - a.window - key0) | bits_to(a.sinks - 1 - key0);
@@ -1047,40 +1120,19 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
 #pragma unroll
             for (int w = 0; w < R::WAVES; ++w)
                 if (!__builtin_amdgcn_readfirstlane(live4[w])) m &= ~(0xffffull << (16 * w));
-            return m >> (4 * hf);
+            return m;
         };
-        const bool useful = key0 <= pos_max && (a.window <= 0 || key0 + R::TK > pos_min - a.window || key0 < a.sinks);
         if (useful) {
-            // S^T: lane (c, hf) receives keys 32 x + 8 (e / 4) + 4 hf + e % 4 of column c
-            f32x16 s[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) s[x][e] = 0.0f;
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    u32x4 k;
-                    if constexpr (E4M3) k = e4m3_to_bf16(lds_read<u32x2>(((stage + kat) ^ (16 * ks)) + 32 * x * R::RB));
-                    else k = lds_read<u32x4>(((stage + kat) ^ (32 * ks)) + 32 * x * R::RB);
-                    s[x] = mfma_bf16_32x32x16(as_bf16x8(k), q[ks], s[x]);
-                }
-            feed_products<D / 8, 1, 4>();
             if constexpr (E4M3) {
+                f32x4 k[8];
+                static_for<8>([&](auto j) { k[j] = lds_read<f32x4>(stage + sat + j / 2 * 256 + j % 2 * 32); });
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int j = 0; j < 8; ++j)
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const f32x4 k = lds_read<f32x4>(stage + R::S0 + 256 * (2 * x + e / 8) + (2 * e % 16 + 4 * hf) * 4);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) s[x][e + r] *= k[r];
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                    for (int r = 0; r < 4; ++r) s[j / 4][4 * (j % 4) + r] *= k[j][r];
             }
             if (!whole) {
-                const uint64_t seen = seen_keys();
+                const uint64_t seen = seen_keys() >> (4 * hf);       // its half's first key in bit 0
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const uint32_t w = (uint32_t)(seen >> (32 * x));
@@ -1106,52 +1158,49 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
             const float ref = run.reference();
             // P^T: the operand of 16 keys is eight neighbouring results
             u32x4 p[4];
+            Fragment ring[AHEAD];                        // keys, then values
+            float f[8];
+            f32x4 scale;                                 // of values, with e4m3: the next four keys'
+            if constexpr (E4M3) scale = lds_read<f32x4>(stage + sat + 64);
+            static_for<AHEAD>([&](auto n) { ring[n] = key_fragment(stage, n); });
+            static_for<2>([&](auto x) { s2[x] = f32x16{}; });
+            __builtin_amdgcn_sched_barrier(0);
+            static_for<N>([&](auto n_) {
+                constexpr int n = decltype(n_)::value, EACH = 32 / N;
+                s2[n % 2] = mfma_bf16_32x32x16(bf16_of(ring[n % AHEAD]), q[n / 2], s2[n % 2]);
+                if constexpr (n + AHEAD < N) ring[n % AHEAD] = key_fragment(stage, n + AHEAD);
+                static_for<EACH>([&](auto j) {
+                    constexpr int e = n * EACH + decltype(j)::value;
+                    f[e % 8] = __builtin_amdgcn_exp2f(fmaf(s[e / 16][e % 16], scale2, -ref));
+                    run.l += f[e % 8];
+                    if constexpr (E4M3 && e % 4 == 3) {
+                        constexpr int next = e / 4 + 1;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    float f[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        f[e] = __builtin_amdgcn_exp2f(fmaf(s[x][8 * y + e], scale2, -ref));
-                        run.l += f[e];
+                        for (int r = 0; r < 4; ++r) f[e % 8 - 3 + r] *= scale[r];
+                        if constexpr (next < 8) scale = lds_read<f32x4>(stage + sat + 64 + next / 2 * 256 + next % 2 * 32);
                     }
-                    if constexpr (E4M3) {
-#pragma unroll
-                        for (int e = 0; e < 8; e += 4) {
-                            const f32x4 v = lds_read<f32x4>(stage + R::S0 + 256 * (2 * x + y) + 64 + (2 * e + 4 * hf) * 4);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                f[e + r] *= v[r];
-                        }
-                    }
-                    p[2 * x + y] = pack8(f);
-                    if constexpr (E4M3) __builtin_amdgcn_sched_barrier(0);       // registers: its scales one group at a time
-                }
-            // V^T: lane (c, hf) takes element 32 d + c of keys 16 y + 4 hf .. and 16 y + 8 + 4 hf ..
-            auto values = [&](int d, int y) {
-                if constexpr (E4M3) return e4m3_to_bf16(lds_columns_b8(((stage + vat) ^ (32 * d)) + 16 * y * R::RB));
-                const uint32_t at = ((stage + vat) ^ (64 * d)) + 16 * y * R::RB;
-                const u32x2 v0 = lds_columns_b16(at), v1 = lds_columns_b16(at + 8 * R::RB);
-                return u32x4{v0.x, v0.y, v1.x, v1.y};
-            };
+                    if constexpr (e % 8 == 7) p[e / 8] = pack8(f);
+                });
+                asm volatile("" : "+v"(run.l));          // (added here, or the terms stay in registers)
+                __builtin_amdgcn_sched_barrier(0);
+            });
             bool bad = false;
             if (!whole) {
                 const i32x4 found = lds_read<i32x4>(stage + R::BAD);
                 bad = __builtin_amdgcn_readfirstlane(found[0] | found[1] | found[2] | found[3]) != 0;
             }
             if (!bad) {
+                static_for<AHEAD>([&](auto n) { ring[n] = value_fragment(stage, n % (D / 32), n / (D / 32)); });
                 __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-#pragma unroll
-                    for (int d = 0; d < D / 32; ++d)
-                        o[d] = mfma_bf16_32x32x16(as_bf16x8(values(d, y)), as_bf16x8(p[y]), o[d]);
-                feed_products<D / 8, E4M3 ? 1 : 2, 4>();
+                static_for<N>([&](auto n_) {
+                    constexpr int n = decltype(n_)::value, BLOCKS = D / 32;
+                    o[n % BLOCKS] = mfma_bf16_32x32x16(bf16_of(ring[n % AHEAD]), as_bf16x8(p[n / BLOCKS]), o[n % BLOCKS]);
+                    if constexpr (n + AHEAD < N) ring[n % AHEAD] = value_fragment(stage, (n + AHEAD) % BLOCKS, (n + AHEAD) / BLOCKS);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
             } else {
-                // Column by column, with zeros for what that column does not see (a probability times a scale that is
-                // not finite is a zero there, too).  These sums and the probabilities are kept in memory: the registers
-                // are the other path's.
+                // Key by key, and nothing of a key that the column does not see.  These sums and the probabilities are
+                // kept in memory: the registers are the other path's.
                 u32x4 parked[4];
                 in_memory(parked);
 #pragma unroll
@@ -1162,21 +1211,29 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                 for (int d = 0; d < D / 32; ++d) {
                     f32x16 sum = odd_o[d];
 #pragma unroll 1
-                    for (int y = 0; y < 4; ++y) {
-                        const uint32_t w = (uint32_t)(seen >> (16 * y)), mine8 = (w & 15u) | (w >> 4 & 0xf0u);
-                        const u32x4 v = values(d, y);
-                        u32x4 its = parked[y], keep;
+                    for (int key = 0; key < R::TK; ++key) {
+                        // in the half (key / 4) % 2 of its operand
+                        const uint32_t two = parked[key >> 4][(key >> 3 & 1) * 2 + (key >> 1 & 1)];
+                        float upper;
+                        const float lower = both32(__uint_as_float(key & 1 ? two & 0xffff0000u : two << 16), upper);
+                        const float prob = key & 4 ? upper : lower;
+                        const bool sees = seen >> key & 1;
+                        const uint32_t row = stage + R::V0 + key * R::RB;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            its[e] &= (mine8 >> (2 * e) & 1 ? 0xffffu : 0u) | (mine8 >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
-#pragma unroll 1
-                        for (int col = 0; col < 32; ++col) {
-                            const uint32_t of = __shfl(mine8, col + 32 * hf, 64);
+                        for (int y = 0; y < 4; ++y) {
+                            u32x2 v;                     // elements 32 d + 8 y + 4 hf ..
+                            if constexpr (E4M3) {
+                                const u32x4 w = e4m3_to_bf16(
+                                    u32x2{lds_read<uint32_t>(row + ((2 * d + y / 2) ^ R::swap_v(key)) * 16 + y % 2 * 8 + 4 * hf), 0u});
+                                v = u32x2{w.x, w.y};
+                            } else {
+                                v = lds_read<u32x2>(row + ((4 * d + y) ^ R::swap_v(key)) * 16 + 8 * hf);
+                            }
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                keep[e] = (of >> (2 * e) & 1 ? 0xffffu : 0u) | (of >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
-                            const f32x16 r = mfma_bf16_32x32x16(as_bf16x8(v & keep), as_bf16x8(its), sum);
-                            if (c == col) sum = r;
+                            for (int r = 0; r < 4; ++r) {
+                                const float with = fmaf(prob, __uint_as_float(r & 1 ? v[r / 2] & 0xffff0000u : v[r / 2] << 16), sum[4 * y + r]);
+                                sum[4 * y + r] = sees ? with : sum[4 * y + r];
+                            }
                         }
                     }
                     odd_o[d] = sum;
@@ -1184,8 +1241,25 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                 in_memory(odd_o);
                 any_odd = true;
             }
+        } else if (i + 1 < tiles) {
+            scores(stage, s2);
         }
-        next = page_of(i + FAR + 1);                     // on its way while the waves gather (LDS reads would wait for it)
+        next_key = key_of(i + FAR + 2);
+        next = page_of(next_key);                        // on its way while the waves gather (LDS reads would wait for it)
+        behind = stage;
+        stage = stage == lds0 + FAR * R::STAGE ? lds0 : stage + R::STAGE;
+    };
+    if (tiles > 0) {
+        f32x16 even[2], odd[2];
+        wait_tiles<R::COPIES, FAR>(tiles);
+        __syncthreads();
+        scores(behind, even);
+        for (int i = 0;;) {
+            step(i, even, odd);
+            if (++i == tiles) break;
+            step(i, odd, even);
+            if (++i == tiles) break;
+        }
     }
 
     if (any_odd)
