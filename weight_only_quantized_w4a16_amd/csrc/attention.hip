@@ -945,6 +945,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
         const bool paged = key < limit && (unsigned)page < (unsigned)a.pages;
         return Place{(int64_t)(paged ? page : 0) * page_bytes + (key & ((1 << a.page_shift) - 1)) * R::RB, paged};
     };
+    bool all_paged = true;                               // whether every key of the item has a page; found below
     auto copy_keys = [&](uint32_t stage, const Place& p) {
 #pragma unroll
         for (int j = 0; j < R::LOADS; ++j)
@@ -958,7 +959,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
             const int64_t row = ((int64_t)h << a.page_shift) + p.at / R::RB;
             lds_copy_b32((lane & 16 ? a.v_scale : a.k_scale) + row + (lane & 15), stage + R::S0 + 256 * wave);
         }
-        if (lane == 0) lds_write<int>(stage + R::LIVE + 4 * wave, p.paged);
+        if (!all_paged && lane == 0) lds_write<int>(stage + R::LIVE + 4 * wave, p.paged);
     };
     // the tiles that rows from position `first` to `last` see all of
     struct Whole {
@@ -1000,23 +1001,40 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
     // A stage holds a tile's values and the next tile's keys: while the softmax of a tile runs,
     // the next one's scores are multiplied.
     constexpr int FAR = R::NB - 1;                       // stages on their way
-    int page[FAR + 2];
+    int page[FAR + 3];
 #pragma unroll
-    for (int i = 0; i < FAR + 2; ++i) page[i] = page_of(key_of(i));
+    for (int i = 0; i < FAR + 3; ++i) page[i] = page_of(key_of(i));
+    for (int j = lane; j < 4 * tiles; j += 64) {         // 16 keys of the item, by lane, while the query is on its way
+        const int key = item.span.tile(i0 + (j >> 2)) * R::TK + 16 * (j & 3);
+        const int64_t b = PREFIX || key < a.shared ? 0 : item.b;
+        const int id = a.table[b * a.max_pages + min(key >> a.page_shift, a.max_pages - 1)];
+        if (key < limit && (unsigned)id >= (unsigned)a.pages) all_paged = false;
+    }
+    all_paged = __ballot(!all_paged) == 0;
     arrived(q);
     uint32_t stage = lds0, behind = lds0 + FAR * R::STAGE;
-    Place place = place_of(key_of(0), page[0]);          // of the tile whose values are copied next
+    Place place = place_of(key_of(0), page[0]);          // of the tile whose values are copied next, and of the one after it
     if (tiles > 0) copy_keys(behind, place);
+    Place after = place_of(key_of(1), page[1]);
 #pragma unroll
     for (int i = 0; i < FAR; ++i) {
-        const Place after = place_of(key_of(i + 1), page[i + 1]);
         if (i < tiles) {
             copy_keys(lds0 + i * R::STAGE, after);
             copy_values(lds0 + i * R::STAGE, place);
         }
         place = after;
+        after = place_of(key_of(i + 2), page[i + 2]);
     }
-    int next_key = key_of(FAR + 1), next = page[FAR + 1];
+    int next_key = key_of(FAR + 2), next = page[FAR + 2];
+    int tile = item.span.tile(i0);
+    bool plain = all_paged && all_whole.has(tile);       // every row sees all of the tile
+    // what the next tile needs, found under this one's products
+    auto ahead = [&](int i) {
+        place = after;
+        after = place_of(next_key, next);
+        tile = item.span.tile(i0 + i + 1);
+        plain = all_paged && all_whole.has(tile);
+    };
 
     Running run;
     f32x16 o[D / 32];
@@ -1070,18 +1088,16 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
         asm volatile("" : "+v"(kat), "+v"(vat), "+v"(sat), "+v"(koff), "+v"(voff));
         wait_tiles<R::COPIES, R::NB - 2>(tiles - 1 - i);
         __syncthreads();                                 // this stage has arrived, and every wave is done with the one behind
-        const i32x4 live4 = lds_read<i32x4>(stage + R::LIVE);
         if (i + FAR < tiles) {
-            const Place after = place_of(next_key, next);
             copy_keys(behind, after);
             copy_values(behind, place);
-            place = after;
         }
-        const int tile = item.span.tile(i0 + i), key0 = tile * R::TK;
-        const bool live = __builtin_amdgcn_readfirstlane(live4[0] & live4[1] & live4[2] & live4[3]) != 0;
-        bool whole = live && all_whole.has(tile), useful = pos_max >= 0;
-        if (!whole) {
-            whole = live && whole_for(pos_min, pos_max).has(tile);
+        const int key0 = tile * R::TK;
+        i32x4 live4{1, 1, 1, 1};
+        bool whole = plain, useful = pos_max >= 0;
+        if (!plain) {
+            if (!all_paged) live4 = lds_read<i32x4>(stage + R::LIVE);
+            whole = __builtin_amdgcn_readfirstlane(live4[0] & live4[1] & live4[2] & live4[3]) && whole_for(pos_min, pos_max).has(tile);
             useful = key0 <= pos_max && (a.window <= 0 || key0 + R::TK > pos_min - a.window || key0 < a.sinks);
             // Where a row of the workgroup does not see all keys: values of positions that hold no key become zeros
             // (a wave its own 16), and a NaN or infinity among the others is found.
@@ -1196,6 +1212,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                     constexpr int n = decltype(n_)::value, BLOCKS = D / 32;
                     o[n % BLOCKS] = mfma_bf16_32x32x16(bf16_of(ring[n % AHEAD]), as_bf16x8(p[n / BLOCKS]), o[n % BLOCKS]);
                     if constexpr (n + AHEAD < N) ring[n % AHEAD] = value_fragment(stage, (n + AHEAD) % BLOCKS, (n + AHEAD) / BLOCKS);
+                    if constexpr (n == AHEAD) ahead(i);
                     __builtin_amdgcn_sched_barrier(0);
                 });
             } else {
@@ -1240,11 +1257,13 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                 }
                 in_memory(odd_o);
                 any_odd = true;
+                ahead(i);
             }
-        } else if (i + 1 < tiles) {
-            scores(stage, s2);
+        } else {
+            if (i + 1 < tiles) scores(stage, s2);
+            ahead(i);
         }
-        next_key = key_of(i + FAR + 2);
+        next_key = key_of(i + FAR + 3);
         next = page_of(next_key);                        // on its way while the waves gather (LDS reads would wait for it)
         behind = stage;
         stage = stage == lds0 + FAR * R::STAGE ? lds0 : stage + R::STAGE;
