@@ -808,11 +808,14 @@ __global__ __launch_bounds__(256, 2) void attention_rows_kernel(Call a) {
 // keys that all waves read from LDS, where they are copied straight from the cache, one to
 // three tiles ahead.  e4m3 codes become bf16 (exact) as they are read.
 //
-// Bound by the matrix instructions and, nearly as much, by the exponentials: a wave multiplies
-// the next tile's scores while it takes this one's exponentials (4096 rows of 8192 keys: 465 ->
-// 425 us, 970 TFLOP/s; e4m3 525 -> 485), and two workgroups on a CU let one's softmax run under
-// another's products; heads of 64, with half the products to as many exponentials, take three
-// (the same rows: 276 -> 269, e4m3 330 -> 320; 7 ragged chunks under a window of 512 75 -> 72).
+// Bound by the matrix instructions and, nearly as much, by the exponentials.  A wave multiplies
+// the next tile's scores while it takes this one's exponentials (4096 rows of 8192 keys 465 ->
+// 425 us; e4m3 525 -> 485), and finds what the next tile needs under the second product (425
+// -> 418).  Two workgroups on a CU let one's softmax run under another's products; heads of 64,
+// with half the products to as many exponentials, take three, in 168 registers: what is cheap
+// to find again is not kept over the loop (7 ragged chunks under a window of 512 70 -> 59 us;
+// e4m3 with sinks 88 -> 77).  Now 4096 rows of 8192 keys: 410 us (1000 TFLOP/s), e4m3 477 (865);
+// heads of 64 259 (795), e4m3 313 (658).
 // ---------------------------------------------------------------------------
 template <int D, bool E4M3>
 struct Tiles {
@@ -868,7 +871,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
     const bool mine = my_row < total_rows;
     const int token = item.s.first_token + min(my_row, total_rows - 1) / a.G;
     const int head = h * a.G + min(my_row, total_rows - 1) % a.G;
-    int pos = -1;                                        // sees nothing
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
+    // this row's position (-1 sees nothing), and the first and last of the wave's and of the workgroup's rows that exist
+    int pos = -1, pos_min, pos_max, all_min, all_max;
     if constexpr (PREFIX) {
         // the last offset that is not above the token
         int lo = 0, hi = a.B;
@@ -879,30 +884,34 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
         }
         if (mine && lo < a.B) {
             const Sequence s = sequence_of(a.q_offsets[lo], a.q_offsets[lo + 1], a.kv_len[lo], a.T);
-            if (token >= s.first_token && token < s.first_token + s.tokens) pos = s.len - s.tokens + token - s.first_token;
+            if (token >= s.first_token && token < s.first_token + s.tokens) pos = max(s.len - s.tokens + token - s.first_token, -1);
         }
-    } else if (mine) {
-        pos = item.s.len - item.s.tokens + (token - item.s.first_token);
-    }
-    pos = max(pos, -1);
-    // the wave's rows that exist: their first and last position
-    int pos_min = mine ? pos : 0x7fffffff, pos_max = mine ? pos : -1;
+        pos_min = mine ? pos : 0x7fffffff;
+        pos_max = mine ? pos : -1;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        pos_min = min(pos_min, __shfl_xor(pos_min, o, 64));
-        pos_max = max(pos_max, __shfl_xor(pos_max, o, 64));
-    }
-    pos_min = __builtin_amdgcn_readfirstlane(pos_min);
-    pos_max = __builtin_amdgcn_readfirstlane(pos_max);
-    // and the workgroup's
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
-    int all_min = pos_min, all_max = pos_max;
-    if (lane == 0) lds_write(lds0 + R::ENDS + 8 * wave, i32x2{pos_min, pos_max});
-    __syncthreads();
-    for (int w = 0; w < R::WAVES; ++w) {
-        const i32x2 ends = lds_read<i32x2>(lds0 + R::ENDS + 8 * w);
-        all_min = min(all_min, __builtin_amdgcn_readfirstlane(ends[0]));
-        all_max = max(all_max, __builtin_amdgcn_readfirstlane(ends[1]));
+        for (int o = 1; o < 64; o <<= 1) {
+            pos_min = min(pos_min, __shfl_xor(pos_min, o, 64));
+            pos_max = max(pos_max, __shfl_xor(pos_max, o, 64));
+        }
+        all_min = pos_min = __builtin_amdgcn_readfirstlane(pos_min);
+        all_max = pos_max = __builtin_amdgcn_readfirstlane(pos_max);
+        if (lane == 0) lds_write(lds0 + R::ENDS + 8 * wave, i32x2{pos_min, pos_max});
+        __syncthreads();
+        for (int w = 0; w < R::WAVES; ++w) {
+            const i32x2 ends = lds_read<i32x2>(lds0 + R::ENDS + 8 * w);
+            all_min = min(all_min, __builtin_amdgcn_readfirstlane(ends[0]));
+            all_max = max(all_max, __builtin_amdgcn_readfirstlane(ends[1]));
+        }
+    } else {
+        // rows are in order of position: lanes 0 .. 3 find the ends
+        const int before = item.s.len - item.s.tokens, first = item.row0 + 32 * wave;
+        if (mine) pos = max(before + token - item.s.first_token, -1);
+        const int end = min((lane & 1 ? first : item.row0) + (lane & 1 ? 31 : lane & 2 ? R::BM - 1 : 0), total_rows - 1);
+        const int ends = max(before + end / a.G, -1);
+        pos_min = first < total_rows ? __builtin_amdgcn_readfirstlane(pos) : 0x7fffffff;
+        pos_max = first < total_rows ? __builtin_amdgcn_readlane(ends, 1) : -1;
+        all_min = __builtin_amdgcn_readlane(ends, 0);
+        all_max = __builtin_amdgcn_readlane(ends, 2);
     }
     const int key_begin = PREFIX ? 0 : a.prefix;
     const int limit = PREFIX ? a.prefix : (int)min((int64_t)item.s.len, (int64_t)a.max_pages << a.page_shift);
@@ -1042,16 +1051,13 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
-    f32x16 odd_o[D / 32];                                // the sums of tiles whose values are not all finite
+    f32x16 odd_o[D / 32];                                // the sums of tiles whose values are not all finite, if
     in_memory(odd_o);
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) odd_o[d] = o[d];
-    in_memory(odd_o);
-    bool any_odd = false;
+    bool any_odd = false;                                // there is one
 
     // S^T of the keys in a stage: lane (c, hf) receives keys 32 x + 8 (e / 4) + 4 hf + e % 4 of column c.
     // Product n takes elements n / 2 of keys 32 (n % 2) ..; its keys are on their way AHEAD products before.
-    constexpr int N = D / 8, AHEAD = 4;
+    constexpr int N = D / 8, AHEAD = D == 64 ? 3 : 4;    // (3: registers)
     using Fragment = std::conditional_t<E4M3, u32x2, u32x4>;
     auto bf16_of = [&](Fragment f) {
         if constexpr (E4M3) return as_bf16x8(e4m3_to_bf16(f));
@@ -1103,6 +1109,10 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
             // (a wave its own 16), and a NaN or infinity among the others is found.
             const bool paged = live4[wave] != 0;
             bool odd = false;
+            int lane = tid & 63;
+            asm volatile("" : "+v"(lane));               // (see above)
+            u32x4 zeros{};
+            asm volatile("" : "+v"(zeros));
 #pragma unroll
             for (int j = 0; j < R::LOADS; ++j) {
                 const int key = 16 * wave + j * R::KEYS + lane / R::PIECES;
@@ -1116,7 +1126,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                         odd |= nonfinite8(v);
                     }
                 } else {
-                    lds_write(at, u32x4{0u, 0u, 0u, 0u});
+                    lds_write(at, zeros);
                 }
             }
             if (E4M3 && lane < 16) {
@@ -1153,8 +1163,11 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                 for (int x = 0; x < 2; ++x) {
                     const uint32_t w = (uint32_t)(seen >> (32 * x));
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        s[x][e] = w & (1u << (8 * (e >> 2) + (e & 3))) ? s[x][e] : -__builtin_inff();
+                    for (int e = 0; e < 16; ++e) {
+                        int sees = __builtin_amdgcn_sbfe((int)w, 8 * (e >> 2) + (e & 3), 1);     // 0 or -1
+                        asm("" : "+v"(sees));
+                        s[x][e] = __int_as_float((__float_as_int(s[x][e]) & sees) | (0xff800000 & ~sees));
+                    }
                 }
             }
             float top = larger(s[0][0], s[1][0]);
@@ -1226,7 +1239,8 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                 const uint64_t seen = seen_keys();
 #pragma unroll 1
                 for (int d = 0; d < D / 32; ++d) {
-                    f32x16 sum = odd_o[d];
+                    f32x16 sum{};
+                    if (any_odd) sum = odd_o[d];
 #pragma unroll 1
                     for (int key = 0; key < R::TK; ++key) {
                         // in the half (key / 4) % 2 of its operand
@@ -1302,8 +1316,10 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
         return;
     }
     if (!mine) return;
+    int again = threadIdx.x;                             // the row once more: kept over the loop it would take registers
+    asm volatile("" : "+v"(again));
     if (item.chunks > 1 || a.prior_chunks) {             // a part: attention_join_kernel joins them
-        const int r = 32 * wave + c;
+        const int r = 32 * wave + (again & 31);
         float* slot = a.slots + ((int64_t)item.first * a.Hkv + (int64_t)h * item.chunks + item.chunk) * R::SLOT;
 #pragma unroll
         for (int d = 0; d < D / 32; ++d)
@@ -1314,7 +1330,8 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
         if (hf == 0) *reinterpret_cast<f32x2*>(slot + R::BM * D + 2 * r) = f32x2{m, l};
         return;
     }
-    const int64_t row = (int64_t)token * a.Hq + head;
+    const int its = item.row0 + 32 * wave + (again & 31);
+    const int64_t row = (int64_t)(item.s.first_token + its / a.G) * a.Hq + h * a.G + its % a.G;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
