@@ -232,19 +232,6 @@ __device__ __forceinline__ T lds_read(uint32_t at) {
     return *(const __attribute__((address_space(3))) T*)(uintptr_t)at;
 }
 
-// The order of N products whose operands come from LDS in READS reads each: AHEAD of them are
-// on their way before the first product, then one product's reads behind every product.  (Left
-// alone the compiler requests them all at once, into registers that it does not have.)
-template <int N, int READS, int AHEAD>
-__device__ __forceinline__ void feed_products() {
-    static_for<N>([](auto i) {
-        if constexpr (decltype(i)::value == 0) __builtin_amdgcn_sched_group_barrier(0x100, READS * AHEAD, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if constexpr (decltype(i)::value + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
-    });
-    __builtin_amdgcn_sched_barrier(0);
-}
-
 // Eight e4m3 codes as bf16: exact.
 __device__ __forceinline__ u32x4 e4m3_to_bf16(u32x2 c) {
     u32x4 r;
