@@ -1075,6 +1075,16 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
             __builtin_amdgcn_sched_barrier(0);
         });
     };
+    // The lane's largest score, in eight steps.
+    float peak;
+    auto peaks = [&](int j, const f32x16 (&s)[2]) {
+        const float a = larger(s[j / 4][4 * (j % 4)], s[j / 4][4 * (j % 4) + 1]), b = larger(s[j / 4][4 * (j % 4) + 2], s[j / 4][4 * (j % 4) + 3]);
+        peak = j == 0 ? larger(a, b) : larger(peak, larger(a, b));
+    };
+    auto all_peaks = [&](const f32x16 (&s)[2]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) peaks(j, s);
+    };
     // one tile: its scores s, the next tile's s2
     auto step = [&](int i, f32x16 (&s)[2], f32x16 (&s2)[2]) {
         // (what follows from these is computed anew in every tile: kept, it takes registers from the products)
@@ -1157,11 +1167,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                     }
                 }
             }
-            float top = larger(s[0][0], s[1][0]);
-#pragma unroll
-            for (int e = 1; e < 16; ++e) top = larger(top, larger(s[0][e], s[1][e]));
+            if (E4M3 || !whole) all_peaks(s);
             float t2;
-            top = both32(top, t2);
+            float top = both32(peak, t2);
             top = larger(top, t2) * scale2;
             if (__ballot(run.outgrown(top))) {
                 const float w = run.follow(top);
@@ -1213,6 +1221,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                     o[n % BLOCKS] = mfma_bf16_32x32x16(bf16_of(ring[n % AHEAD]), as_bf16x8(p[n / BLOCKS]), o[n % BLOCKS]);
                     if constexpr (n + AHEAD < N) ring[n % AHEAD] = value_fragment(stage, (n + AHEAD) % BLOCKS, (n + AHEAD) / BLOCKS);
                     if constexpr (n == AHEAD) ahead(i);
+                    if constexpr (!E4M3 && n % (N / 8) == 0) peaks(n / (N / 8), s2);
                     __builtin_amdgcn_sched_barrier(0);
                 });
             } else {
@@ -1258,10 +1267,14 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                 }
                 in_memory(odd_o);
                 any_odd = true;
+                all_peaks(s2);
                 ahead(i);
             }
         } else {
-            if (i + 1 < tiles) scores(stage, s2);
+            if (i + 1 < tiles) {
+                scores(stage, s2);
+                all_peaks(s2);
+            }
             ahead(i);
         }
         next_key = key_of(i + FAR + 3);
@@ -1274,6 +1287,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
         wait_tiles<R::COPIES, FAR>(tiles);
         __syncthreads();
         scores(behind, even);
+        all_peaks(even);
         for (int i = 0;;) {
             step(i, even, odd);
             if (++i == tiles) break;
