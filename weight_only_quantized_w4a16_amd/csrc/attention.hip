@@ -797,12 +797,13 @@ __global__ __launch_bounds__(256, 2) void attention_rows_kernel(Call a) {
 //
 // Bound by the matrix instructions and, nearly as much, by the exponentials.  A wave multiplies
 // the next tile's scores while it takes this one's exponentials (4096 rows of 8192 keys 465 ->
-// 425 us; e4m3 525 -> 485), and finds what the next tile needs under the second product (425
-// -> 418).  Two workgroups on a CU let one's softmax run under another's products; heads of 64,
-// with half the products to as many exponentials, take three, in 168 registers: what is cheap
-// to find again is not kept over the loop (7 ragged chunks under a window of 512 70 -> 59 us;
-// e4m3 with sinks 88 -> 77).  Now 4096 rows of 8192 keys: 410 us (1000 TFLOP/s), e4m3 477 (865);
-// heads of 64 259 (795), e4m3 313 (658).
+// 425 us; e4m3 525 -> 485), and finds what the next tile needs, its largest score with it, under
+// the second product (425 -> 407), which goes before the other workgroup's work where a row has
+// 128 elements (400 -> 391, e4m3 473 -> 461; heads of 64 254 -> 263).  Two workgroups on a CU let
+// one's softmax run under another's products; heads of 64, with half the products to as many
+// exponentials, take three, in 168 registers: what is cheap to find again is not kept over the
+// loop (7 ragged chunks under a window of 512 70 -> 59 us; e4m3 with sinks 88 -> 77).  Now 4096
+// rows of 8192 keys: 391 us (1055 TFLOP/s), e4m3 461 (895); heads of 64 254 (812), e4m3 314 (656).
 // ---------------------------------------------------------------------------
 template <int D, bool E4M3>
 struct Tiles {
@@ -1214,6 +1215,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                 bad = __builtin_amdgcn_readfirstlane(found[0] | found[1] | found[2] | found[3]) != 0;
             }
             if (!bad) {
+                if constexpr (D == 128) __builtin_amdgcn_s_setprio(1);   // (see Tiles)
                 static_for<AHEAD>([&](auto n) { ring[n] = value_fragment(stage, n % (D / 32), n / (D / 32)); });
                 __builtin_amdgcn_sched_barrier(0);
                 static_for<N>([&](auto n_) {
@@ -1224,6 +1226,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
                     if constexpr (!E4M3 && n % (N / 8) == 0) peaks(n / (N / 8), s2);
                     __builtin_amdgcn_sched_barrier(0);
                 });
+                if constexpr (D == 128) __builtin_amdgcn_s_setprio(0);
             } else {
                 // Key by key, and nothing of a key that the column does not see.  These sums and the probabilities are
                 // kept in memory: the registers are the other path's.
