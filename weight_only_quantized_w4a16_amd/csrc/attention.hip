@@ -1397,12 +1397,12 @@ Plan plan_of(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, bool e4m3, in
     // partial results cost about 12 us).
     if ((int64_t)(B - 1) * prefix * Hkv * D * 4 < (int64_t)64 << 20) prefix = 0;
     const int64_t own = max_kv - prefix;
-    // Sequences of few rows stream their keys, more are worth tiles.  Where the caches hold what the row tiles of a sequence
-    // read again, few is up to 64 rows (32 / 64 rows, one sequence of 8192 keys: 19.5 / 20.5 us, on tiles 29.6 / 30.8; 64
-    // sequences of up to 600 keys, 48 rows: 19 and 38), else 16 (32 rows, 64 sequences of 8192 keys: 403 and 362 us).  A
-    // ragged batch (fewer tokens than B times the largest count) holds both.
-    const bool large = (int64_t)B * own * Hkv * D * (e4m3 ? 2 : 4) > (int64_t)128 << 20;
-    p.few_rows = large ? 16 : 64;
+    // Sequences of few rows stream their keys once for every 16 rows, more are worth tiles of 128: few is 16 rows, and up to
+    // 128 where that is little work, 3/4 of a million keys, heads and row tiles in all.  On rows and on tiles: one sequence
+    // of 8192 keys with 32 / 64 / 128 rows 19.5 / 21 / 29 us and 28.5 / 30 / 33; 64 of up to 600 with 32 rows 21 and 31, with
+    // 48 rows 33 and 38; 8 of 4096 with 64 rows 48 and 40 (e4m3); 64 of 8192 with 32 rows 505 and 365.  A ragged batch
+    // (fewer tokens than B times the largest count) holds both.
+    p.few_rows = 16 * (int)std::clamp<int64_t>((3 << 18) / std::max<int64_t>(1, (int64_t)B * own * Hkv), 1, 8);
     p.rows = most_rows <= p.few_rows;
     p.tiles = !p.rows;
     if (p.tiles && B > 1 && !(max_q > 0 && (int64_t)max_q * B == T)) p.rows = true;
@@ -1420,9 +1420,9 @@ Plan plan_of(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, bool e4m3, in
             p.row_items = (int)(tiles + want);
             p.slots = (size_t)p.row_items * Hkv * 16 * (D + 2);
         }
-        // read once, past the caches, where they cannot hold it: 64 x 8192 keys 356 -> 317 us (6.0 -> 6.8 TB/s), e4m3 196 -> 172;
+        // Read once, past the caches, where they cannot hold it: 64 x 8192 keys 356 -> 317 us (6.0 -> 6.8 TB/s), e4m3 196 -> 172;
         // 67 MB that the caches did hold 21.0 -> 22.7
-        p.stream = large && !p.tiles;
+        p.stream = most_rows <= 16 && (int64_t)B * own * Hkv * D * (e4m3 ? 2 : 4) > (int64_t)128 << 20;
     }
     if (p.tiles) {
         const int64_t tiles = std::min(all, all / 128 + B);
