@@ -604,8 +604,8 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  *                heads, value heads.
  *   q_offsets    in  int32 [B + 1], on the device, as the next two.
  *   kv_len       in  int32 [B].
- *   block_table  in  int32 [B, max_pages]; only entries of positions below kv_len are
- *                read.
+ *   block_table  in  int32 [B, max_pages]; only entries of positions below kv_len
+ *                matter.
  * Hq is a multiple of Hkv (query head h reads key head h / (Hq / Hkv)), Hq <= 1024,
  * D is 64 or 128, page_size 16, 32, 64, 128 or 256, T < 2^22, T Hq <= 2^27, B <= 2^14,
  * max_pages page_size <= 2^30 (QG_ERR_SHAPE otherwise).
@@ -632,7 +632,8 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  * positions j of the token's sequence up to its own; with window > 0 only those less
  * than `window` before it and the first `sinks` positions of the sequence.  Scores,
  * softmax and sums fp32, out rounded once; above 16 rows (token, head of the key
- * head's group) a sequence the probabilities are rounded to bf16 before their product.
+ * head's group) a sequence the probabilities may be rounded to bf16 before their
+ * product.
  *   q_bf16       in  [T, Hq, D].  It must not overlap out_bf16.
  *   window       0: none; up to 2^30.  sinks >= 0: not read without a window.
  *   shared_prefix   the first positions of every sequence are the same pages: a

@@ -31,6 +31,19 @@ def test_every_number_of_tiles(ops, D, fmt):
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 70)])
+def test_many_tiles_without_a_split(ops, D, fmt, window, sinks):
+    """Row tiles enough to fill the GPU, so that a workgroup goes over all keys of its rows: up to 18 tiles."""
+    b = Batch([900], [1150], 64, 64, D, 64, fmt, seed=D)
+    some = slice(3, None, 30)
+    want = oracle.paged_attention(b.q[:, some], b.k[:, some], b.v[:, some], b.table, b.q_offsets, b.kv_len, D ** -0.5, window, sinks)
+    announce(f"many tiles {fmt} D={D} window={window}")
+    out, lse = attend(ops, b, window=window, sinks=sinks, max_q=900)
+    check(b, out[:, some], lse[:, some], want, f"window={window}")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (150, 20)])
 def test_positions_without_pages(ops, D, fmt, page, window, sinks):
