@@ -16,8 +16,9 @@
 //
 // What a masked key holds never matters: its probability is an exact zero, values that
 // no row sees are replaced by zeros before the product (uninitialised memory may hold
-// NaN), and where a value that only some rows see is infinite or NaN those rows are
-// multiplied one by one.  A row that sees no key is zero, its lse minus infinity.
+// NaN), and a step with a value that only some rows see and that is infinite or NaN is
+// multiplied apart, row by row or key by key.  A row that sees no key is zero, its lse
+// minus infinity.
 
 #include <algorithm>
 #include <atomic>
@@ -342,20 +343,29 @@ __device__ __forceinline__ void load_agent(const float* p, float* v) {
     }
 }
 
-// A row's result: N neighbouring elements from element d0, and once a row the lse.
+// N elements of a row's result, rounded, and its lse.
 template <int N>
-__device__ __forceinline__ void store_row(const Call& a, int D, int64_t row, int d0, const Joined<N>& j) {
+__device__ __forceinline__ void rounded(const Joined<N>& j, uint32_t (&w)[N / 2]) {
     const float inv = 1.0f / j.l;
-    uint32_t w[N / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
         const f32x2 v = j.l == 0.0f ? f32x2{0.0f, 0.0f} : f32x2{j.o[2 * i] * inv, j.o[2 * i + 1] * inv};
         w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
     }
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+// A row's result: N neighbouring elements from element d0, and once a row the lse.
+template <int N>
+__device__ __forceinline__ void store_row(const Call& a, int D, int64_t row, int d0, const Joined<N>& j) {
+    uint32_t w[N / 2];
+    rounded<N>(j, w);
     uint16_t* p = a.out + row * D + d0;
     if constexpr (N == 8) *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
     else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    if (a.lse && d0 == 0) a.lse[row] = j.l == 0.0f ? -__builtin_inff() : (j.m + log2f(j.l)) * 0.69314718055994530942f;
+    if (a.lse && d0 == 0) a.lse[row] = lse_of(j.m, j.l);
 }
 
 // ---------------------------------------------------------------------------
@@ -1338,17 +1348,25 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
     }
     const int its = item.row0 + 32 * wave + (again & 31);
     const int64_t row = (int64_t)(item.s.first_token + its / a.G) * a.Hq + h * a.G + its % a.G;
+    // the halves exchange, so that a lane stores eight neighbouring elements
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            Joined<4> j;
-            j.m = m;
-            j.l = l;
+        for (int y = 0; y < 4; y += 2) {
+            uint32_t w[2][2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) j.o[r] = o[d][4 * y + r];
-            store_row<4>(a, D, row, 32 * d + 8 * y + 4 * hf, j);
+            for (int x = 0; x < 2; ++x) {
+                Joined<4> j;
+                j.l = l;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) j.o[r] = o[d][4 * (y + x) + r];
+                rounded<4>(j, w[x]);
+            }
+            const auto first = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+            const auto second = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+            *reinterpret_cast<u32x4*>(a.out + row * D + 32 * d + 8 * (y + hf)) = u32x4{first[0], second[0], first[1], second[1]};
         }
+    if (a.lse && hf == 0) a.lse[row] = lse_of(m, l);
 }
 
 // Joins the parts that attention_tiles_kernel left: 16 rows of a row tile a workgroup, so
