@@ -996,16 +996,26 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
     uint32_t vat = R::V0 + vkey * R::RB + (vpiece ^ R::swap_v(vkey)) * 16 + (lane & 1) * 8;
     uint32_t sat = R::S0 + 16 * hf;                      // scales of keys 8 j + 4 hf ..: 256 (j / 2) + 32 (j % 2) on, of values 64 behind
 
-    // this lane's query: 8 elements of every 16, negated for a negative scale
+    // This lane's query: 8 elements of every 16, times the sign of the scale, or zero for a scale of zero (exact; masked
+    // scores are minus infinity before they are scaled, and zero times that would be NaN).
     bf16x8 q[D / 16];
     {
         const uint16_t* from = a.q + ((int64_t)token * a.Hq + head) * D + 8 * hf;
-        const uint32_t sign = a.scale2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-            q[ks] = as_bf16x8(*reinterpret_cast<const u32x4*>(from + 16 * ks) ^ u32x4{sign, sign, sign, sign});
+        for (int ks = 0; ks < D / 16; ++ks) q[ks] = as_bf16x8(*reinterpret_cast<const u32x4*>(from + 16 * ks));
+        if (a.scale2 <= 0.0f) {
+            const float sign = a.scale2 < 0.0f ? -1.0f : 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                float f[8];
+                unpack8(__builtin_bit_cast(u32x4, q[ks]), f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] *= sign;
+                q[ks] = as_bf16x8(pack8(f));
+            }
+        }
     }
-    const float scale2 = fabsf(a.scale2);
+    const float scale2 = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(a.scale2 == 0.0f ? 1.0f : fabsf(a.scale2))));
 
     // A stage holds a tile's values and the next tile's keys: while the softmax of a tile runs,
     // the next one's scores are multiplied.
