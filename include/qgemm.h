@@ -635,6 +635,8 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  * head's group) a sequence the probabilities may be rounded to bf16 before their
  * product.
  *   q_bf16       in  [T, Hq, D].  It must not overlap out_bf16.
+ *   scale        any number whose product with log2(e) is a finite fp32 one (|scale| up
+ *                to 2.358e38; QG_ERR_SHAPE otherwise).  0: every seen key counts alike.
  *   window       0: none; up to 2^30.  sinks >= 0: not read without a window.
  *   shared_prefix   the first positions of every sequence are the same pages: a
  *                multiple of page_size (0: none).  They are read by row 0 of the

@@ -135,7 +135,7 @@ qg_status paged_attention(const uint16_t* q_bf16, const void* k_cache, const voi
                           int window, int sinks, int shared_prefix, int max_q, uint16_t* out_bf16, float* lse,
                           void* workspace, size_t workspace_bytes, qg_stream stream) {
     if (!heads_ok(T, Hq, Hkv, D) || !batch_ok(B, max_pages, page_size, Hkv) || !cache_ok(pages, page_size, Hkv) ||
-        !isfinite(scale) || window < 0 || window > kMaxPositions || sinks < 0 || max_q < 0 || shared_prefix < 0 ||
+        !isfinite(scale * kLog2E) || window < 0 || window > kMaxPositions || sinks < 0 || max_q < 0 || shared_prefix < 0 ||
         shared_prefix % page_size != 0 || shared_prefix > (int64_t)max_pages * page_size)
         return QG_ERR_SHAPE;
     if (T == 0 || B == 0) return QG_OK;

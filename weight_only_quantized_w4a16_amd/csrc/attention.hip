@@ -1531,7 +1531,7 @@ size_t paged_attention_workspace_bytes(int T, int B, int64_t max_kv, int Hq, int
 void launch_paged_attention(const AttentionArgs& args, int D, void* ws, hipStream_t st) {
     Call a{args};
     a.G = a.Hq / a.Hkv;
-    a.scale2 = a.scale * 1.44269504088896340736f;
+    a.scale2 = a.scale * kLog2E;
     a.shared = a.prefix;
     const Plan p = plan_of(a.T, a.B, (int64_t)a.max_pages << a.page_shift, a.Hq, a.Hkv, D, a.k_scale != nullptr, a.prefix, a.max_q);
     if (!p.prior_chunks) a.prefix = 0;                   // every sequence reads the shared pages for itself

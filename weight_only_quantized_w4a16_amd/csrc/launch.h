@@ -143,7 +143,8 @@ struct RopeArgs {
 void launch_qk_norm_rope(const RopeArgs& p, int D, hipStream_t st);
 void launch_kv_append(const RopeArgs& p, int D, hipStream_t st);
 
-// Attention over a paged cache (attention.hip)
+// Attention over a paged cache (attention.hip).  Scores are kept in base 2: scale kLog2E is finite.
+constexpr float kLog2E = 1.44269504088896340736f;
 struct AttentionArgs {
     const uint16_t* q;           // [T, Hq, D]
     const void *k, *v;           // [pages, Hkv, page, D]
