@@ -141,8 +141,8 @@ qg_status paged_attention(const uint16_t* q_bf16, const void* k_cache, const voi
     if (T == 0 || B == 0) return QG_OK;
     if (!q_bf16 || !k_cache || !v_cache || !k_scale != !v_scale || !q_offsets || !kv_len || !block_table || !out_bf16)
         return QG_ERR_NULL;
-    if (!aligned(q_bf16, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) ||
-        !aligned(v_scale, 16) || !aligned(q_offsets, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4) ||
+    if (!aligned(q_bf16, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) ||
+        !aligned(v_scale, 4) || !aligned(q_offsets, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4) ||
         !aligned(out_bf16, 16) || !aligned(lse, 4))
         return QG_ERR_ALIGN;
     const int most = max_q < T ? max_q : T;
