@@ -1381,15 +1381,15 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attention_tiles_kernel(C
 
 // Joins the parts that attention_tiles_kernel left: 16 rows of a row tile a workgroup, so
 // that the parts' 66 KB of each tile and chunk are read by many CUs (joined by the last
-// workgroup of a tile, 64 chunks took 120 us).
+// workgroup of a tile, 64 chunks took 120 us).  Row tiles are the grid's y and z: along x
+// alone a large batch behind a shared prefix would have 2^32 threads and more.
 template <int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(Call a) {
     using R = Tiles<D, false>;
     __shared__ __attribute__((aligned(16))) unsigned char smem[kJoinBytes<D>];
-    constexpr int GROUPS = R::BM / 16;
-    const int h = blockIdx.x % a.Hkv, group = blockIdx.x / a.Hkv % GROUPS;
+    const int h = blockIdx.x % a.Hkv, group = blockIdx.x / a.Hkv;
     Item item;
-    if (!find_item<R::BM, R::TK, true, true>(a, (int)(blockIdx.x / a.Hkv / GROUPS), item)) return;
+    if (!find_item<R::BM, R::TK, true, true>(a, (int)(blockIdx.y + gridDim.y * blockIdx.z), item)) return;
     if (item.chunks == 1 && !a.prior_chunks) return;     // written already
     const int row0 = item.row0 + 16 * group;
     const int rows = min(16, item.s.tokens * a.G - row0);
@@ -1508,7 +1508,10 @@ void launch_all(Call a, const Plan& p, void* ws, hipStream_t st) {
         c.target = p.tile_target;
         c.least = 4;
         launch(&attention_tiles_kernel<D, E4M3, false>, tiles_done, (int64_t)c.items * a.Hkv, M::LDS, c, st);
-        if (p.join) attention_join_kernel<D><<<dim3((unsigned)(p.tile_tiles * a.Hkv * (M::BM / 16))), 256, 0, st>>>(c);
+        if (p.join) {
+            const unsigned y = (unsigned)std::min(p.tile_tiles, 1 << 15), z = ((unsigned)p.tile_tiles + y - 1) / y;
+            attention_join_kernel<D><<<dim3((unsigned)(a.Hkv * (M::BM / 16)), y, z), 256, 0, st>>>(c);
+        }
     }
     if (p.rows) {
         a.few = p.tiles ? 1 : -1;
