@@ -1457,10 +1457,12 @@ Plan plan_of(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, bool e4m3, in
     if (p.tiles) {
         const int64_t tiles = std::min(all, all / 128 + B);
         const int64_t want = std::clamp<int64_t>(2 * cus / Hkv, 1, 160);
-        p.tile_items = p.tile_tiles = (int)tiles;
+        // (where the other kernel takes the sequences of few rows, only so many are left: partial results are for these)
+        const int64_t left = p.rows ? std::min(tiles, all / 128 + all / (p.few_rows + 1)) : tiles;
+        p.tile_items = p.tile_tiles = (int)left;
         if (tiles < want && own > 256) {
             p.tile_target = (int)want;
-            p.tile_items = (int)(tiles + want);
+            p.tile_items = (int)(left + want);
         }
         p.join = p.tile_target || prefix > 0;
         if (p.join) p.slots = std::max(p.slots, (size_t)p.tile_items * Hkv * 128 * (D + 2));
