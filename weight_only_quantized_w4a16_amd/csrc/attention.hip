@@ -1457,7 +1457,8 @@ Plan plan_of(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, bool e4m3, in
     if (p.tiles) {
         const int64_t tiles = std::min(all, all / 128 + B);
         const int64_t want = std::clamp<int64_t>(2 * cus / Hkv, 1, 160);
-        // (where the other kernel takes the sequences of few rows, only so many are left: partial results are for these)
+        // Where the other kernel takes the sequences of few rows, only so many are left, and partial results are for these
+        // (1000 tokens of as many sequences behind 8192 shared positions, 32 heads over 8 of 128: 582 -> 175 MB).
         const int64_t left = p.rows ? std::min(tiles, all / 128 + all / (p.few_rows + 1)) : tiles;
         p.tile_items = p.tile_tiles = (int)left;
         if (tiles < want && own > 256) {
