@@ -6,8 +6,8 @@
 //   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)    angle = position * inv_freq[i]
 //       half-split pairs (i, i + R / 2) or neighbours (2 i, 2 i + 1), i < R / 2
 //
-// fp32 from the bf16 inputs to the one rounding of each output, the squares summed in
-// fp64 (rows near 1e+-30 stay finite).  Angles are fp64 turns: position * inv_freq /
+// fp32 from the bf16 inputs to the one rounding of each output; squares whose fp32 sum
+// leaves [2^-80, 2^100] are summed in fp64 (rows near 1e+-30 stay finite).  Angles are fp64 turns: position * inv_freq /
 // (2 pi), less its nearest whole number, is exact to 2^-22 turns at any 32-bit position
 // and feeds the hardware's sine and cosine of turns (1.3e-7 absolute over a whole turn).
 // No table of angles: positions have no limit, and a token's 64 angles cost less than
@@ -55,29 +55,32 @@ __device__ __forceinline__ float head_max(float a) {
     return __uint_as_float(u);
 }
 
-// The norm's factor 1 / sqrt(mean(x^2) + eps) of a head, x and its pairs' halves y.  Squares
-// and sum in fp32 where that neither overflows nor loses the small ones; else in fp64, and
-// the factor is applied here, before the weight could overflow.
+// Multiplies a head's x and its pairs' halves y by the norm's factor 1 / sqrt(mean(x^2) + eps):
+// before the weight, with which either may leave fp32's range though their quotient's product
+// does not.  Squares and sum are fp32 where that neither overflows nor loses the small ones (all
+// rows but extreme ones), else fp64.
 template <int L>
-__device__ __forceinline__ float rstd_of_head(float* x, float* y, double inv_D, float eps) {
+__device__ __forceinline__ void norm_head(float* x, float* y, double inv_D, float eps) {
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
     sum = head_sum<L>(sum);
+    float r;
     if (sum >= 0x1p-80f && sum <= 0x1p100f) {
-        const float v = fmaf(sum, (float)inv_D, eps), r = __builtin_amdgcn_rsqf(v);
-        return fmaf(r * 0.5f, fmaf(-v * r, r, 1.0f), r);
-    }
-    double wide = 0.0;
+        const float v = fmaf(sum, (float)inv_D, eps);
+        r = __builtin_amdgcn_rsqf(v);
+        r = fmaf(r * 0.5f, fmaf(-v * r, r, 1.0f), r);
+    } else {
+        double wide = 0.0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) wide = fma((double)x[j], (double)x[j], wide);
-    const float r = rstd_of(head_sum<L>(wide), inv_D, eps);
+        for (int j = 0; j < 8; ++j) wide = fma((double)x[j], (double)x[j], wide);
+        r = rstd_of(head_sum<L>(wide), inv_D, eps);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         x[j] *= r;
         y[j] *= r;
     }
-    return 1.0f;
 }
 
 // Where a token's key and value go: a row of the cache, or nowhere (-1).
@@ -175,9 +178,9 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
             float x[8];
             unpack8(packed, x);
             if (KIND != Kind::value && (moves || norm)) {
-                float y[8], r = 1.0f;
+                float y[8];
                 unpack8(NEXT ? packed : in[(h0 + h) * L + other], y);
-                if (norm) r = rstd_of_head<L>(x, y, 1.0 / D, p.eps);
+                if (norm) norm_head<L>(x, y, 1.0 / D, p.eps);
                 if (moves) {
                     if constexpr (NEXT) {
 #pragma unroll
@@ -189,8 +192,6 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[j] *= cg[j];
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= r;
                 packed = pack8(x);
             }
             if constexpr (KIND == Kind::query) {
