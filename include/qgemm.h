@@ -625,7 +625,9 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  *   q_bf16, k_bf16   out [T, Hq, D] and [T, Hkv, D].
  *
  * kv_append -- the same by the batch's own positions, the keys and the values (as
- * they are) into the cache, the queries into q_bf16 [T, Hq, D].  Two tokens that name
+ * they are) into the cache, the queries into q_bf16 [T, Hq, D].  An 8-bit key's codes
+ * are of its fp32 elements, not rounded to bf16 before; a head with a NaN or an
+ * infinity has a scale that is not finite.  Two tokens that name
  * the same row of the cache leave unspecified contents there.
  *
  * paged_attention -- out[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j over the

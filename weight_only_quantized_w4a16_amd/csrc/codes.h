@@ -27,7 +27,9 @@ __device__ __forceinline__ uint32_t encode4(const float* q) {
 // a finite reciprocal divides.  The scale is the row's own maximum over q_max, so
 // |y / s| exceeds q_max by roundings only -- except where s is subnormal, a whole
 // number of steps of 2^-149 that max|y| / q_max may be far from (max|y| = 178
-// steps: an int8 scale of one).  There the quotient is clamped.
+// steps: an int8 scale of one).  There the quotient is clamped.  EXACT: the codes are those
+// of the IEEE quotient (quant_act_per_token's), by one correction of the product: for
+// every bf16 y the quantizer can meet, as an exhaustive check has shown.
 struct RowScale {
     float s, r;
     bool fast;
@@ -39,13 +41,16 @@ struct RowScale {
         q.fast = q.s >= 0x1p-100f;
         return q;
     }
-    template <class Fmt>
+    template <class Fmt, bool EXACT = false>
     __device__ __forceinline__ uint2 codes(const float* y) const {
         if (s == 0.0f) return make_uint2(0u, 0u);
         float q[8];
-        if (fast) {
+        if (fast && (!EXACT || s < __builtin_inff())) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = y[j] * r;
+            for (int j = 0; j < 8; ++j) {
+                q[j] = y[j] * r;
+                if constexpr (EXACT) q[j] = fmaf(fmaf(-q[j], s, y[j]), r, q[j]);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {

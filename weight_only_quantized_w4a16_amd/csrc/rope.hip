@@ -208,7 +208,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) top = max_abs(top, x[j]);
                     const RowScale scale = RowScale::of<FmtE4M3>(head_max<L>(top));
-                    static_cast<uint2*>(KIND == Kind::key ? p.k : p.v)[at * L + piece] = scale.codes<FmtE4M3>(x);
+                    static_cast<uint2*>(KIND == Kind::key ? p.k : p.v)[at * L + piece] = scale.codes<FmtE4M3, true>(x);
                     if (piece == 0) (KIND == Kind::key ? p.k_scale : p.v_scale)[at] = scale.s;
                 }
             }
