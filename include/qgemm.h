@@ -633,9 +633,10 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  * paged_attention -- out[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j over the
  * positions j of the token's sequence up to its own; with window > 0 only those less
  * than `window` before it and the first `sinks` positions of the sequence.  Scores,
- * softmax and sums fp32, out rounded once; above 16 rows (token, head of the key
- * head's group) a sequence the probabilities may be rounded to bf16 before their
- * product.
+ * softmax and sums fp32, out rounded once.  Above 16 rows (token, head of the key
+ * head's group) a sequence, and over the positions of a shared_prefix for every row,
+ * the probabilities may be rounded to bf16 before their product (2^-8 of the mean of
+ * |v| at most); else they lose nothing that out could show.
  *   q_bf16       in  [T, Hq, D].  It must not overlap out_bf16.
  *   scale        any number whose product with log2(e) is a finite fp32 one (|scale| up
  *                to 2.358e38; QG_ERR_SHAPE otherwise).  0: every seen key counts alike.
@@ -643,7 +644,8 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  *   shared_prefix   the first positions of every sequence are the same pages: a
  *                multiple of page_size (0: none).  They are read by row 0 of the
  *                table, once for all; the entries of the other rows are not read there.
- *                The results are those of the same call without it.
+ *                The results are those of the same call without it, but for the
+ *                rounding of probabilities above.
  *   max_q        the largest number of new tokens of a sequence, or 0: not known.  It
  *                chooses kernels and changes no result beyond their rounding.
  *   out_bf16     out [T, Hq, D].  A row that sees no key is zero.
