@@ -652,9 +652,11 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  *   lse          out fp32 [T, Hq] log of the sum of exponentials (-inf for a row that
  *                sees no key), or NULL.
  *   workspace    qg_paged_attention_workspace_bytes(...) bytes (NULL when that is 0),
- *                16-byte aligned, zero-filled before its first use; one sized for the
- *                largest call serves calls of any shape in any order that do not
- *                overlap in time.
+ *                16-byte aligned, zero-filled before its first use; one of the largest
+ *                of the sizes returned for a set of calls serves them in any order,
+ *                while they do not overlap in time.  The size does not grow with the
+ *                call: a decode step may need more than a prefill, whose row tiles
+ *                fill the GPU without a split.
  * Masked positions never matter, whatever they hold.  A row whose scores are all -inf
  * counts as one that sees no key.  The same call gives the same bits on every run.
  */

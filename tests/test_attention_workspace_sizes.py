@@ -25,3 +25,16 @@ def test_ragged_batch_behind_a_shared_prefix(B, T, G, Hkv, D):
     split = 512 // Hkv                                       # chunks that a few row tiles are split into, at most
     part = Hkv * 128 * (D + 2) * 4                           # of a row tile, all key heads
     assert need <= known + (row_tiles + split) * part
+
+
+def test_a_smaller_call_may_need_more():
+    """The sizes are not monotone: a workspace is for the largest size of the calls to come, not for the largest call, and one
+    that is too small is refused before anything is launched."""
+    from weight_only_quantized_w4a16_amd import ops
+    size = lambda T, B, max_q: ops.paged_attention_workspace_bytes(T, B, 128, 32, 8, 128, 64, 0, max_q)
+    assert size(8192, 1, 8192) == 0 and size(1, 1, 1) > 0
+    assert size(512, 1, 512) > size(8192, 1, 8192)
+    fake = 0x4000000
+    call = lambda ws, n: ops._lib.paged_attention(fake, fake, fake, None, None, 200, 64, fake, fake, fake, 1, 1, 128, 32, 8, 128, 0.1, 0, 0,
+                                                  0, 1, fake, None, ws, n, None)
+    assert call(None, 0) == 1 and call(fake, size(1, 1, 1) - 1) == 4     # QG_ERR_NULL, QG_ERR_WORKSPACE
