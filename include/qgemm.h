@@ -643,7 +643,8 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  *   window       0: none; up to 2^30.  sinks >= 0: not read without a window.
  *   shared_prefix   the first positions of every sequence are the same pages: a
  *                multiple of page_size (0: none).  They are read by row 0 of the
- *                table, once for all; the entries of the other rows are not read there.
+ *                table, once for all sequences where that is faster; the entries of the
+ *                other rows are not read there.
  *                The results are those of the same call without it, but for the
  *                rounding of probabilities above.
  *   max_q        the largest number of new tokens of a sequence, or 0: not known.  It

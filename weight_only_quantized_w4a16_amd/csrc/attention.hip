@@ -821,7 +821,7 @@ __global__ __launch_bounds__(256, 2) void attention_rows_kernel(Call a) {
 // of its size where its own rounding makes 0.0017.  The pass over a shared prefix does so for
 // every row, also of sequences whose own keys the kernel above takes without that loss: the rest
 // as a second product would cost 32 / 128 sequences behind 8192 / 16384 tokens 29.8 -> 31.4 us and
-// 130 -> 159, 16 prompts of 64 tokens behind 8192 180 -> 237.
+// 130 -> 159, 64 of 4 tokens behind 8192 82 -> 96.
 // ---------------------------------------------------------------------------
 template <int D, bool E4M3>
 struct Tiles {
@@ -1429,9 +1429,12 @@ Plan plan_of(int T, int B, int64_t max_kv, int Hq, int Hkv, int D, bool e4m3, in
     const int64_t cus = device_cu_count();
     const int64_t most_rows = max_q > 0 ? std::min(all, max_q * G) : all;        // of a sequence
     Plan p{};
-    // A shared prefix is worth a pass of its own from 64 MB of rereading on (that pass and its
-    // partial results cost about 12 us).
-    if ((int64_t)(B - 1) * prefix * Hkv * D * 4 < (int64_t)64 << 20) prefix = 0;
+    // A shared prefix is worth a pass of its own from 64 MB of rereading on (that pass and its partial results cost about
+    // 12 us), and while a sequence has fewer rows than a row tile: the rows of a prompt fill tiles by themselves, to which a
+    // pass adds only partial results.  16 sequences of 4 / 64 / 128 / 256 / 1024 rows behind 8192 tokens with a pass 22 / 56 /
+    // 92 / 161 / 590 us, without 46 / 72 / 86 / 148 / 511; 32 behind 2048 with 21 / 46 / 76 / 115 / 462, without 31 / 47 / 51 /
+    // 76 / 302.
+    if ((int64_t)(B - 1) * prefix * Hkv * D * 4 < (int64_t)64 << 20 || all >= 128 * (int64_t)B) prefix = 0;
     const int64_t own = max_kv - prefix;
     // Sequences of few rows stream their keys once for every 16 rows, more are worth tiles of 128: few is 16 rows, and up to
     // 128 where that is little work, 3/4 of a million keys, heads and row tiles in all.  On rows and on tiles: one sequence
