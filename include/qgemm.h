@@ -605,7 +605,8 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  *   q_offsets    in  int32 [B + 1], on the device, as the next two.
  *   kv_len       in  int32 [B].
  *   block_table  in  int32 [B, max_pages]; only entries of positions below kv_len
- *                matter.
+ *                matter.  paged_attention chooses its kernels and splits by max_pages,
+ *                as if the sequences were that long.
  * Hq is a multiple of Hkv (query head h reads key head h / (Hq / Hkv)), Hq <= 1024,
  * D is 64 or 128, page_size 16, 32, 64, 128 or 256, T < 2^22, T Hq <= 2^27, B <= 2^14,
  * max_pages page_size <= 2^30 (QG_ERR_SHAPE otherwise).
@@ -616,9 +617,11 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  *
  * qk_norm_rope -- the queries and keys of fused rows: per head the RMS norm with a
  * weight, then the rotation by position, rounded once.
- *   q_weight_bf16, k_weight_bf16   in  [D], or NULL: no norm (eps is then not read).
+ *   q_weight_bf16, k_weight_bf16   in  [D] (16-byte aligned), or NULL: no norm (eps
+ *                is then not read).
  *   positions    in  int32 [T], any values.
- *   inv_freq     in  fp64 [rotary_dim / 2] radians a position; NULL for rotary_dim 0.
+ *   inv_freq     in  fp64 [rotary_dim / 2] (8-byte aligned) radians a position; NULL
+ *                for rotary_dim 0.
  *   rotary_dim   elements of a head that are rotated, the first ones: 0 .. D, a
  *                multiple of 16.
  *   interleaved  0: pairs (i, i + rotary_dim / 2); else neighbours (2 i, 2 i + 1).
@@ -636,7 +639,9 @@ qg_status moe_combine_backward(const uint16_t *dy_bf16, const uint16_t *rows_bf1
  * softmax and sums fp32, out rounded once.  Above 16 rows (token, head of the key
  * head's group) a sequence, and over the positions of a shared_prefix for every row,
  * the probabilities may be rounded to bf16 before their product (2^-8 of the mean of
- * |v| at most); else they lose nothing that out could show.
+ * |v| at most); else they lose nothing that out could show.  Sums are divided at the
+ * end and hold up to 2^8 max|v| for each seen key before: values that near the end of
+ * fp32's range overflow there.
  *   q_bf16       in  [T, Hq, D].  It must not overlap out_bf16.
  *   scale        any number whose product with log2(e) is a finite fp32 one (|scale| up
  *                to 2.358e38; QG_ERR_SHAPE otherwise).  0: every seen key counts alike.

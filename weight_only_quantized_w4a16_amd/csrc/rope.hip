@@ -13,10 +13,11 @@
 // No table of angles: positions have no limit, and a token's 64 angles cost less than
 // reading them.
 //
-// A lane holds eight neighbouring elements of a head (16 bytes), D / 8 lanes a head.  A wave
-// takes one token: each lane computes one pair's angle and the heads' lanes read theirs
-// from LDS (every lane its own eight took 4 KB of frequencies a wave, 78 us instead of 65 at
-// 8191 tokens).  A pair's other half is read again from the L1 rather than moved between lanes.
+// A lane holds eight neighbouring elements of a head (16 bytes), D / 8 lanes a head.  A token's
+// heads are taken by one wave, or dealt to several while those are few (`launch`): in each, a lane
+// computes one pair's angle and the heads' lanes read theirs from LDS (every lane its own eight
+// took 4 KB of frequencies a wave, 78 us instead of 65 at 8191 tokens).  A pair's other half is
+// read again from the L1 rather than moved between lanes.
 // Bound by memory: 8191 tokens of 64 + 8 heads, normed, 65 us (4.7 TB/s; a copy 5.2); a
 // head at a time and 8 waves a SIMD beat two or four heads at a time and fewer (71 / 81 us).
 

@@ -989,7 +989,8 @@ class PagedAttention(_Scratch):
     optional sliding `window` and `sinks` first positions that stay visible.
 
     The batch: q_offsets int32 [B + 1] (sequence b owns rows q_offsets[b] .. q_offsets[b + 1] - 1 of the new tokens),
-    kv_len int32 [B] its positions with the new tokens, block_table int32 [B, max_pages] its pages, all on the device.
+    kv_len int32 [B] its positions with the new tokens, block_table int32 [B, max_pages] its pages, all on the device
+    (kernels are chosen by max_pages: a table no wider than the batch needs is the fastest).
     Owns a reusable workspace: its calls must not overlap in time."""
 
     def __init__(self, cache: PagedKVCache, q_heads, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -1027,7 +1028,8 @@ class PagedAttention(_Scratch):
     def attend(self, q, block_table, q_offsets, kv_len, max_q=0, shared_prefix=0, with_lse=False, out=None, stream=None):
         """bf16 [T, q_heads D], the o product's input (rows of no sequence are not written); with_lse: (out, fp32 [T, q_heads]
         logarithms of the sums of exponentials).  max_q: the largest number of new tokens of a sequence, 0 for not known.
-        shared_prefix: the first positions of every sequence are the same pages (a multiple of the page size), read once."""
+        shared_prefix: the first positions of every sequence are the same pages (a multiple of the page size), read once
+        for all where that is faster.  `out` must not overlap q."""
         c = self.cache
         T = q.shape[0]
         _is(q, _BF16, (T, self.q_heads, c.head_dim), "q")
