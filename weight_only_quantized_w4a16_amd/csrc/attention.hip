@@ -377,7 +377,7 @@ __device__ __forceinline__ void store_row(const Call& a, int D, int64_t row, int
 // are joined in LDS, those of chunks by the last workgroup to arrive, in chunk order.
 //
 // Bound by memory: two workgroups a CU keep 100 KB on their way.  64 sequences of 8192 keys
-// take 317 us (6.8 TB/s), of ragged lengths in e4m3 122 (5.5); one of 16384 20.4 (3.3), 7 of
+// take 330 us (6.5 TB/s), of ragged lengths in e4m3 120 (5.5); one of 16384 20.4 (3.3), 7 of
 // them latency before and behind the stream.  The probabilities
 // enter the second product as a sum of two bf16 numbers, so it loses nothing to their
 // rounding (matrix instructions are idle here).
@@ -814,8 +814,11 @@ __global__ __launch_bounds__(256, 2) void attention_rows_kernel(Call a) {
 // 128 elements (400 -> 391, e4m3 473 -> 461; heads of 64 254 -> 263).  Two workgroups on a CU let
 // one's softmax run under another's products; heads of 64, with half the products to as many
 // exponentials, take three, in 168 registers: what is cheap to find again is not kept over the
-// loop (7 ragged chunks under a window of 512 70 -> 59 us; e4m3 with sinks 88 -> 77).  Now 4096
-// rows of 8192 keys: 391 us (1055 TFLOP/s), e4m3 461 (895); heads of 64 254 (812), e4m3 314 (656).
+// loop (7 ragged chunks under a window of 512 70 -> 59 us; e4m3 with sinks 88 -> 77).  The vector
+// units' cycles and the matrix units' add up to about the whole time: 53 and 56 % with 128
+// elements, 63 and 37 with 64, e4m3 68 and 41, 75 and 28.  Now 4096 rows of 8192 keys, in a long run
+// (short ones, as the steps above, are a few per cent slower): 380 us (1085 TFLOP/s), e4m3 439
+// (939); heads of 64 247 (836), e4m3 302 (683).
 //
 // Probabilities are rounded to bf16 once for the second product: the output is then off by 0.0023
 // of its size where its own rounding makes 0.0017.  The pass over a shared prefix does so for
