@@ -27,9 +27,10 @@ __device__ __forceinline__ uint32_t encode4(const float* q) {
 // a finite reciprocal divides.  The scale is the row's own maximum over q_max, so
 // |y / s| exceeds q_max by roundings only -- except where s is subnormal, a whole
 // number of steps of 2^-149 that max|y| / q_max may be far from (max|y| = 178
-// steps: an int8 scale of one).  There the quotient is clamped.  EXACT: the codes are those
-// of the IEEE quotient (quant_act_per_token's), by one correction of the product: for
-// every bf16 y the quantizer can meet, as an exhaustive check has shown.
+// steps: an int8 scale of one).  There the quotient is clamped.  EXACT: one correction of
+// the product, with which the codes are those of the IEEE quotient (quant_act_per_token's)
+// for every bf16 y that a row may hold, as an exhaustive check has shown, and for fp32 y
+// but where the quotient's last bit decides a tie.
 struct RowScale {
     float s, r;
     bool fast;

@@ -7,9 +7,10 @@
 //       half-split pairs (i, i + R / 2) or neighbours (2 i, 2 i + 1), i < R / 2
 //
 // fp32 from the bf16 inputs to the one rounding of each output; squares whose fp32 sum
-// leaves [2^-80, 2^100] are summed in fp64 (rows near 1e+-30 stay finite).  Angles are fp64 turns: position * inv_freq /
-// (2 pi), less its nearest whole number, is exact to 2^-22 turns at any 32-bit position
-// and feeds the hardware's sine and cosine of turns (1.3e-7 absolute over a whole turn).
+// leaves [2^-80, 2^100] are summed in fp64 (rows near 1e+-30 stay finite).  Angles are
+// fp64 turns: position * inv_freq / (2 pi), less its nearest whole number, is exact to
+// 2^-22 turns at any 32-bit position and feeds the hardware's sine and cosine of turns
+// (1.3e-7 absolute over a whole turn).
 // No table of angles: positions have no limit, and a token's 64 angles cost less than
 // reading them.
 //
